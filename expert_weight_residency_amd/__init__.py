@@ -23,8 +23,12 @@ MOE_MAX_TOPK = 32
 ENTRY_POINTS = ("moe_expert_bytes", "moe_ffn_workspace_bytes", "moe_route_split",
                 "moe_expert_ffn_mxfp4", "moe_expert_gate_up_mxfp4", "moe_expert_down_mxfp4",
                 "moe_stage_rows", "moe_finalize", "moe_usage_counts", "moe_swap_rows",
-                "moe_last_error", "moe_expert_ffn_mxfp4_noalloc", "moe_stage_rows_dma")
+                "moe_last_error", "moe_expert_ffn_mxfp4_noalloc", "moe_stage_rows_dma",
+                "moe_topk_gate", "moe_layer_few_workspace_bytes", "moe_layer_few_mxfp4")
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
+MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_H, MOE_FEW_MAX_I = 16, 8192, 4096
+# moe_topk_gate weights: softmax over the picks, or over all unmasked experts
+GATE_NORM_PICKS, GATE_NORM_ALL = 0, 1
 
 
 class MoeError(RuntimeError):
@@ -93,6 +97,14 @@ def lib():
         L.moe_swap_rows.restype = i32
         L.moe_swap_rows.argtypes = [ctypes.POINTER(MoeBankC), ctypes.POINTER(MoeBankC), i32, i32,
                                     i32, i32, vp, i32, vp, vp, vp, sz, i32, i32, vp]
+        i64, bankp = ctypes.c_int64, ctypes.POINTER(MoeBankC)
+        L.moe_topk_gate.restype = i32
+        L.moe_topk_gate.argtypes = [vp, i32, i64, i32, i32, i32, i32, vp, vp, vp]
+        L.moe_layer_few_workspace_bytes.restype = sz
+        L.moe_layer_few_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.moe_layer_few_mxfp4.restype = i32
+        L.moe_layer_few_mxfp4.argtypes = [bankp, bankp, vp, i32, vp, vp, vp, i32, i32, i32, i32,
+                                          vp, i32, vp, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -438,3 +450,82 @@ def moe_swap_rows(hot: Bank, cold: Bank, hot_row: int, cold_row: int, expect_hot
                                _gpu(row_map, "row_map", ("torch.int32",)),
                                int(row_map.shape[0]), hptr(hot_owner), hptr(cold_owner),
                                _gpu(staging, "staging"), nbytes, H, I, _stream(stream)))
+
+
+# ------------------------------------------------- around the residency split --
+
+_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
+
+
+def _rows2d(t, name: str):
+    """(pointer, dtype code, rows, columns, row stride) of a 2-D GPU tensor
+    whose rows are contiguous."""
+    code = _DTYPES.get(str(getattr(t, "dtype", "")))
+    if code is None or t.device.type != "cuda" or t.dim() != 2 or \
+            (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise _bad(name, "a 2-D GPU tensor (bfloat16, float16, float32) of contiguous rows", t)
+    rows, cols = int(t.shape[0]), int(t.shape[1])
+    return t.data_ptr(), code, rows, cols, int(t.stride(0)) if rows > 1 else cols
+
+
+def _same_device(*named) -> None:
+    """Raise MOE_EINVAL unless the GPU tensors sit on the current device (the
+    one the kernels are launched on)."""
+    import torch
+    cur = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.device.type == "cuda" and t.device.index != cur:
+            raise MoeError(MOE_EINVAL, f"{name}: on {t.device}, the current device is cuda:{cur}")
+
+
+def moe_topk_gate(logits, topk_ids, topk_w, norm: int = GATE_NORM_PICKS, stream=None) -> None:
+    """logits [T,E] (bfloat16, float16 or float32; rows may be strided) ->
+    topk_ids int32 [T,k], topk_w fp32 [T,k] (see the header for masked experts
+    and ties)."""
+    p, dtype, T, E, ld = _rows2d(logits, "logits")
+    _same_device(("logits", logits), ("topk_ids", topk_ids), ("topk_w", topk_w))
+    if topk_ids.dim() != 2 or int(topk_ids.shape[0]) != T or topk_w.shape != topk_ids.shape:
+        raise MoeError(MOE_EINVAL, f"topk_ids {tuple(topk_ids.shape)}, topk_w "
+                                   f"{tuple(topk_w.shape)}: need [{T}, k] each")
+    _check(lib().moe_topk_gate(p, dtype, ld, T, E, int(topk_ids.shape[1]), int(norm),
+                               _gpu(topk_ids, "topk_ids", ("torch.int32",)),
+                               _gpu(topk_w, "topk_w", ("torch.float32",)), _stream(stream)))
+
+
+def moe_layer_few_workspace_bytes(T: int, k: int, H: int, I: int) -> int:
+    return int(lib().moe_layer_few_workspace_bytes(T, k, H, I))
+
+
+def moe_layer_few_mxfp4(hot: Bank, cold: Bank, row_map, x, topk_ids, topk_w, I: int, workspace,
+                        out, n_invalid, counts_layer=None, count_tmax: int = 256,
+                        stream=None) -> None:
+    """The whole layer for at most MOE_FEW_MAX_TOKENS tokens in two launches:
+    x bf16 [T,H], topk_ids int32 [T,k], topk_w fp32 [T,k] -> out bf16 [T,H]."""
+    T, H, k, E = int(x.shape[0]), int(x.shape[1]), int(topk_ids.shape[1]), int(row_map.shape[0])
+    if int(topk_ids.shape[0]) != T or topk_w.shape != topk_ids.shape:
+        raise MoeError(MOE_EINVAL, f"topk_ids {tuple(topk_ids.shape)}, topk_w "
+                                   f"{tuple(topk_w.shape)}: need [{T}, k] each")
+    _same_device(("x", x), ("out", out), ("topk_ids", topk_ids), ("topk_w", topk_w),
+                 ("row_map", row_map), ("workspace", workspace), ("n_invalid", n_invalid),
+                 ("counts", counts_layer), ("hot bank", hot.w13), ("cold bank", cold.w13))
+    if T > 0:
+        _check_bank(hot, H, I, "hot bank")
+        _check_bank(cold, H, I, "cold bank")
+        ws = moe_layer_few_workspace_bytes(T, k, H, I)
+        if ws == 0:
+            raise MoeError(MOE_ENOTSUP, f"T={T}, k={k}, H={H}, I={I}: past the few-token layer's "
+                                        f"limits (T {MOE_FEW_MAX_TOKENS}, H {MOE_FEW_MAX_H}, "
+                                        f"I {MOE_FEW_MAX_I})")
+        _need(workspace, "workspace", ws)
+        _need(out, "out", 2 * T * H)
+        _need(n_invalid, "n_invalid", 4)
+        if counts_layer is not None:
+            _need(counts_layer, "counts_layer", 4 * E)
+    i32 = ("torch.int32",)
+    h, c = hot.abi(), cold.abi()
+    _check(lib().moe_layer_few_mxfp4(
+        ctypes.byref(h), ctypes.byref(c), _gpu(row_map, "row_map", i32), E,
+        _gpu(x, "x", _BF16_BITS), _gpu(topk_ids, "topk_ids", i32),
+        _gpu(topk_w, "topk_w", ("torch.float32",)), T, k, H, I,
+        _gpu_opt(counts_layer, "counts", i32), count_tmax, _gpu(n_invalid, "n_invalid", i32),
+        _gpu(workspace, "workspace"), _gpu(out, "out", _BF16_BITS), _stream(stream)))

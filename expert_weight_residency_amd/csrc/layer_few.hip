@@ -1,0 +1,673 @@
+// The whole routed MXFP4 layer for a few tokens (at most 16) in two launches,
+// against six for the split, the two banks' gate/up and down, and the finalize.
+//
+//   out[t] = sum over the distinct experts e of token t of
+//            Wdown[e] . bf16(w[t][e] * silu(Wgate[e] . x[t]) * (Wup[e] . x[t]))
+//
+// The router weight multiplies h before its one rounding to bf16 (the MFMA
+// operand type; an error of at most 2^-9 of each h, as the split path has), so
+// that the down products of a token's experts add up in one fp32 accumulator
+// and no row per pick is written: the second kernel ends in `out`.
+//
+// A step of one token touches 6 of 384 experts, 113 MB: it is bound by how
+// soon every CU has its share of those bytes in flight. Hence, in both kernels:
+//  - The reduction axis is cut over the wavefronts of a workgroup (512 of 4096
+//    elements each), and a work item is only 8 rows of the product (8 gate and
+//    8 up rows; 16 down rows), so that one expert already spreads over all CUs.
+//  - Each wavefront holds its slice of the activations in registers (gate/up)
+//    or in LDS of its own (down) and streams weights through a register ring
+//    several items ahead, with one barrier per gate/up item for the sum of the
+//    wavefronts' partial results and none until the end in the down kernel.
+//  - A weight load takes 8 rows x one whole 128-byte line (256 elements). Lanes
+//    r < 8 of the MFMA operand hold the first half of row r's line, lanes r >= 8
+//    the second half of row r - 8's; the B operand holds the tokens' first
+//    halves in columns 0-7 and their second halves in columns 8-15. The result
+//    tile's two diagonal 8 x 8 blocks are then the two halves' partial sums
+//    (the other two are discarded), and no lane exchange is needed. More than 8
+//    tokens take a second set of columns.
+// The order of every sum is fixed by the shapes and the picks' order alone, not
+// by the banks: a step gives the same bits wherever its experts are.
+#include <algorithm>
+
+#include "layer_ops.h"
+#include "mxfp4_common.h"
+
+namespace moe {
+namespace {
+
+using namespace mx;
+
+constexpr int kMaxPicks = MOE_FEW_MAX_TOKENS * MOE_MAX_TOPK;  // 512
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
+static_assert(kThreads >= kMaxPicks, "one thread per pick");
+constexpr int kMaxH = 8192, kMaxI = 4096;
+
+// What the gate/up kernel leaves for the down kernel, at the workspace's start;
+// the h rows follow it.
+struct Tables {
+  int32_t n_u;               // distinct experts, in the order of their first picks
+  int32_t pad[15];
+  int32_t row[kMaxPicks];    // row map entry of each: >= 0 hot, < 0 cold
+  int32_t mask[kMaxPicks];   // its tokens, one bit each
+  int32_t base[kMaxPicks];   // its first h row; one row per token, ascending
+};
+constexpr size_t kTableBytes = (sizeof(Tables) + 255) / 256 * 256;
+
+// How a reduction axis of K elements is cut: chunks of 256 elements, CPW
+// consecutive chunks per wavefront, KS wavefronts per row, SUB such groups.
+struct Cut {
+  int nchunk, cpw, ks, sub;
+};
+__host__ __device__ inline Cut cut_of(int K) {
+  Cut c;
+  c.nchunk = (K + kChunkElems - 1) / kChunkElems;
+  c.cpw = c.nchunk <= 8 ? 1 : (c.nchunk <= 16 ? 2 : 4);
+  c.ks = (c.nchunk + c.cpw - 1) / c.cpw;
+  c.sub = kWaves / c.ks;
+  return c;
+}
+
+// Orders LDS between the wavefronts of the workgroup and leaves global loads in
+// flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// One ring slot: the weights of 16 rows (two groups of 8) over the wavefront's
+// chunks, and the slice's scale bytes of row lane/4 (quarter lane%4 of them).
+template <int CPW>
+struct Slot {
+  uint4 w[2][CPW];
+  uint32_t s[(CPW + 1) / 2];
+};
+
+// The lane's place in the weight rows of a slice: rows of K/2 bytes, K/32
+// scale bytes. Pieces (32 elements, 16 bytes, 1 scale byte) past the end of the
+// axis are read at the row's start instead; their scale becomes 1 and their
+// activations are zero.
+template <int CPW, bool TAIL>
+struct Lane {
+  uint32_t woff[CPW];       // weight bytes, within a group of 8 rows
+  uint32_t soff[TAIL ? CPW : 1];  // scale bytes, within this lane's row
+  bool in[CPW];
+  int r, q, srow;
+
+  __device__ __forceinline__ void init(int lane, int slice, int K) {
+    r = lane & 15;
+    q = lane >> 4;
+    srow = lane >> 2;
+    const int nblk = K / 32, piece = q + (r >= 8 ? 4 : 0);
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      const int b = (slice * CPW + j) * 8 + piece;
+      in[j] = !TAIL || b < nblk;
+      woff[j] = (uint32_t)(r & 7) * (uint32_t)(K / 2) + 16u * (uint32_t)(in[j] ? b : 0);
+    }
+    const int s0 = slice * CPW * 8 + (lane & 3) * 2 * CPW;
+    if constexpr (TAIL) {
+#pragma unroll
+      for (int i = 0; i < CPW; ++i) soff[i] = s0 + 2 * i < nblk ? s0 + 2 * i : 0;
+    } else {
+      soff[0] = s0;
+    }
+  }
+
+  // g0, g1: the two groups' first weight rows; sp: this lane's scale row.
+  template <bool STREAM>
+  __device__ __forceinline__ void load(Slot<CPW>& o, const uint8_t* g0, const uint8_t* g1,
+                                       const uint8_t* sp) const {
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      if constexpr (STREAM) {
+        o.w[0][j] = ld_stream16(g0 + woff[j]);
+        o.w[1][j] = ld_stream16(g1 + woff[j]);
+      } else {
+        o.w[0][j] = *reinterpret_cast<const uint4*>(g0 + woff[j]);
+        o.w[1][j] = *reinterpret_cast<const uint4*>(g1 + woff[j]);
+      }
+    }
+    if constexpr (TAIL || CPW == 1) {
+      uint32_t h[CPW];
+#pragma unroll
+      for (int i = 0; i < CPW; ++i)
+        h[i] = *reinterpret_cast<const uint16_t*>(sp + soff[TAIL ? i : 0]);
+#pragma unroll
+      for (int i = 0; i < (CPW + 1) / 2; ++i)
+        o.s[i] = h[2 * i] | (2 * i + 1 < CPW ? h[2 * i + 1 < CPW ? 2 * i + 1 : 0] << 16 : 0u);
+    } else {
+      // K is a multiple of 256 * CPW: the row's scale bytes and this piece of
+      // them are 2 * CPW-byte aligned within the tensor
+      
+      if constexpr (CPW == 2) {
+        o.s[0] = *reinterpret_cast<const uint32_t*>(sp + soff[0]);
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(sp + soff[0]);
+        o.s[0] = v.x;
+        o.s[1] = v.y;
+      }
+    }
+  }
+
+  // This lane's scale for group g, chunk j: byte 8j + piece of row (r & 7) + 8g.
+  __device__ __forceinline__ float scale(const Slot<CPW>& o, int g, int j) const {
+    const int b = 8 * j + q + (r >= 8 ? 4 : 0);
+    const int src = 32 * g + 4 * (r & 7) + b / (2 * CPW), byte = b % (2 * CPW);
+    uint32_t v;
+    if constexpr (CPW == 4) {
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.s[0]);
+      const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.s[1]);
+      v = byte >= 4 ? hi : lo;
+    } else {
+      v = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.s[0]);
+    }
+    v = (v >> (8 * (byte & 3))) & 0xffu;
+    return e8m0_to_f32(in[j] ? v : 127u);
+  }
+};
+
+__device__ __forceinline__ uint32_t word4(const uint4& v, int m) {
+  return m == 0 ? v.x : (m == 1 ? v.y : (m == 2 ? v.z : v.w));
+}
+
+// ---- gate/up ----------------------------------------------------------------
+
+struct Shared {
+  int key[kMaxPicks];     // expert id of a pick that has a row, else -1
+  float w[kMaxPicks];
+  int upos[kMaxPicks];    // of a first pick: its expert's place among the distinct ones
+  int row[kMaxPicks], mask[kMaxPicks], base[kMaxPicks];
+  float wsum[kMaxPicks];  // per h row: the token's router weight for the expert
+  int list[kMaxPicks];    // experts in device banks, then the ones in host banks
+  int part[kWaves];
+  int n_u, n_dev;
+};
+
+// Exclusive prefix over the workgroup's threads of v; all threads call it.
+__device__ __forceinline__ int block_prefix(int v, int* part, int& total) {
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(s, d, 64);
+    if (lane >= d) s += o;
+  }
+  __syncthreads();  // part may still be read from an earlier call
+  if (lane == 63) part[wv] = s;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    before += i < wv ? part[i] : 0;
+    total += part[i];
+  }
+  return before + s - v;
+}
+
+// The step's distinct experts, their tokens and their h rows. Thread s is pick
+// s. Returns whether this thread's pick has no row in a bank.
+__device__ void build_tables(const FewArgs& a, Shared& L) {
+  const int n = a.T * a.k, s = threadIdx.x;
+  int id = -1, m = 0;
+  bool ok = false;
+  if (s < n) {
+    id = a.ids[s];
+    L.w[s] = a.w[s];
+    if ((uint32_t)id < (uint32_t)a.E) {
+      m = a.row_map[id];
+      ok = m >= 0 ? m < a.hot.n_rows : -1 - m < a.cold.n_rows;
+    }
+  }
+  L.key[s] = ok ? id : -1;
+  const int bad = __syncthreads_count(s < n && !ok);
+  if (blockIdx.x == 0) {
+    if (s == 0) *a.n_invalid = bad;
+    if (a.counts && (uint32_t)id < (uint32_t)a.E && s < n)
+      __hip_atomic_fetch_add(&a.counts[id], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  int first = s;  // earliest pick of the same expert
+  if (ok) {
+    for (int p = (s & ~3) - 4; p >= 0; p -= 4) {
+      const int4 v = *reinterpret_cast<const int4*>(&L.key[p]);
+      first = v.w == id ? p + 3 : first;
+      first = v.z == id ? p + 2 : first;
+      first = v.y == id ? p + 1 : first;
+      first = v.x == id ? p : first;
+    }
+    for (int p = s - 1; p >= (s & ~3); --p)
+      if (first >= (s & ~3) && L.key[p] == id) first = p;
+  }
+  const bool lead = ok && first == s;
+  int n_u;
+  const int u0 = block_prefix(lead ? 1 : 0, L.part, n_u);
+  if (lead) {
+    L.row[u0] = m;
+    L.mask[u0] = 0;
+    L.upos[s] = u0;
+  }
+  __syncthreads();
+  int u = 0;
+  const int t = s / a.k;
+  if (ok) {
+    u = L.upos[first];
+    atomicOr(&L.mask[u], 1 << t);
+  }
+  __syncthreads();
+  int rows;
+  const int mk = s < n_u ? L.mask[s] : 0;
+  const int b0 = block_prefix(__popc(mk), L.part, rows);
+  if (s < n_u) L.base[s] = b0;
+  // device-bank experts first, each kind in order
+  const int code = s < n_u ? L.row[s] : 0;
+  const bool host = s < n_u && (code >= 0 ? a.hot.host : a.cold.host);
+  int n_host;
+  const int h0 = block_prefix(host ? 1 : 0, L.part, n_host);
+  if (s < n_u) L.list[host ? n_u - n_host + h0 : s - h0] = s;
+  if (s == 0) {
+    L.n_u = n_u;
+    L.n_dev = n_u - n_host;
+  }
+  __syncthreads();
+  if (ok) {
+    // the token's weight for this expert: its picks of it, in order
+    bool mine = true;
+    float sum = 0.0f;
+    for (int p = t * a.k; p < (t + 1) * a.k; ++p)
+      if (L.key[p] == id) {
+        if (p < s) mine = false;
+        sum += L.w[p];
+      }
+    if (mine) L.wsum[L.base[u] + __popc(L.mask[u] & ((1 << t) - 1))] = sum;
+  }
+  __syncthreads();
+}
+
+// CUs that read experts in host memory; the others stream the device banks
+// beside them.
+constexpr int kHostBlocks = 8;
+
+template <int CPW, int SETS, int R, bool TAIL>
+__global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
+  extern __shared__ __align__(16) float red[];  // [2][SUB][2 groups][SETS][2 KS][8][8]
+  __shared__ __align__(16) Shared L;
+  const int H = a.H, I = a.I, T = a.T;
+  const Cut cut = cut_of(H);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ks = cut.ks, nsub = cut.sub;
+  const int slice = wv % ks, sub = wv / ks;
+  const bool active = sub < nsub;
+  Lane<CPW, TAIL> ln;
+  ln.init(lane, slice, H);
+
+  // this wavefront's slice of x as B operands: column c holds token c (first
+  // halves) or c - 8 (second halves) of its set
+  bf16x8 xb[SETS][CPW][4];
+#pragma unroll
+  for (int st = 0; st < SETS; ++st) {
+    const int t = st * 8 + (ln.r & 7);
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      const int e0 = (slice * CPW + j) * kChunkElems + (ln.r >= 8 ? 128 : 0) + 32 * ln.q;
+      const bool in = t < T && e0 < H;  // H is a multiple of 64: 32 elements at once
+      const uint4* p = reinterpret_cast<const uint4*>(a.x + (size_t)(t < T ? t : 0) * H +
+                                                      (e0 < H ? e0 : 0));
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint4 v = p[m];
+        xb[st][j][m] = __builtin_bit_cast(
+            bf16x8, make_uint4(in ? v.x : 0u, in ? v.y : 0u, in ? v.z : 0u, in ? v.w : 0u));
+      }
+    }
+  }
+
+  build_tables(a, L);
+  const int n_u = __builtin_amdgcn_readfirstlane(L.n_u);
+  const int n_dev = __builtin_amdgcn_readfirstlane(L.n_dev);
+  Tables* tab = static_cast<Tables*>(a.workspace);
+  uint16_t* h = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.workspace) + kTableBytes);
+  if (blockIdx.x == 0) {
+    if (tid == 0) tab->n_u = n_u;
+    if (tid < n_u) {
+      tab->row[tid] = L.row[tid];
+      tab->mask[tid] = L.mask[tid];
+      tab->base[tid] = L.base[tid];
+    }
+  }
+
+  // this workgroup's run of items (list entry, 8 rows of I)
+  const int per = I / 8;
+  const int hb = n_dev < n_u ? min(kHostBlocks, (int)gridDim.x - 1) : 0;
+  const bool on_host = (int)blockIdx.x < hb;
+  const int64_t n = (int64_t)(on_host ? n_u - n_dev : n_dev) * per;
+  const int blocks = on_host ? hb : (int)gridDim.x - hb;
+  const int blk = on_host ? (int)blockIdx.x : (int)blockIdx.x - hb;
+  const int first = on_host ? n_dev * per : 0;
+  const int g0 = first + (int)(n * blk / blocks), g1 = first + (int)(n * (blk + 1) / blocks);
+  if (g0 >= g1) return;  // the whole workgroup
+  const int steps = (g1 - g0 + nsub - 1) / nsub;
+
+  const size_t wrb = H / 2, srb = H / 32;
+  Slot<CPW> ring[R];
+  // Past the run's end a load reads the first rows of a device bank (the same
+  // for every wavefront, so they stay in the L2) to keep the stream
+  // unconditional.
+  auto issue = [&](Slot<CPW>& o, int step) {
+    const int it = g0 + step * nsub + sub;
+    const bool live = step < steps && it < g1 && active;
+    const int li = live ? it / per : 0;
+    const int code = __builtin_amdgcn_readfirstlane(L.row[L.list[li]]);
+    const int i0 = live ? (it - li * per) * 8 : 0;
+    const bool hot = live ? code >= 0 : (a.hot.n_rows > 0 && !a.hot.host) || a.cold.n_rows == 0;
+    const FewBank& b = hot ? a.hot : a.cold;
+    const size_t row = live ? (size_t)(uint32_t)(code >= 0 ? code : -1 - code) : 0;
+    const size_t r0 = row * 2 * (size_t)I + i0, r1 = r0 + I;
+    const uint8_t* sp = b.s13 + (r0 + (ln.srow & 7)) * srb + (ln.srow >= 8 ? (size_t)I * srb : 0);
+    ln.template load<!TAIL>(o, b.w13 + r0 * wrb, b.w13 + r1 * wrb, sp);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // floats of one (buffer, sub): [group][set][partial][token][row]
+  const int per_sub = 2 * SETS * 2 * ks * 64;
+
+#pragma unroll
+  for (int u = 0; u < R; ++u) issue(ring[u], u);
+
+  for (int s0 = 0;; s0 += R) {
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      const int step = s0 + u;
+      if (step >= steps) return;
+      if (active) {
+        f32x4 acc[2][SETS];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < CPW; ++j) {
+          const float sc[2] = {ln.scale(ring[u], 0, j), ln.scale(ring[u], 1, j)};
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const bf16x8 av = dequant8(word4(ring[u].w[g][j], m), sc[g]);
+#pragma unroll
+              for (int st = 0; st < SETS; ++st)
+                acc[g][st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xb[st][j][m],
+                                                                     acc[g][st], 0, 0, 0);
+            }
+        }
+        // lane (c, q) holds rows 4q .. 4q+3 of column c: keep the diagonal blocks
+        if ((ln.r >= 8) == (ln.q >= 2)) {
+          float* o = red + (size_t)((step & 1) * nsub + sub) * per_sub;
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int st = 0; st < SETS; ++st)
+              *reinterpret_cast<f32x4*>(
+                  o + ((g * SETS + st) * 2 * ks + 2 * slice + (ln.r >= 8)) * 64 +
+                  (ln.r & 7) * 8 + (ln.q & 1) * 4) = acc[g][st];
+        }
+      }
+      issue(ring[u], step + R);
+      lds_barrier();
+      // One wavefront per item, each in turn, adds the partial sums (in their
+      // order) and writes h; the others go on. A buffer is written again two
+      // steps later, past the next step's barrier, which that wavefront reaches
+      // only after its reads.
+      for (int sb = 0; sb < nsub; ++sb) {
+        const int it = g0 + step * nsub + sb;
+        if (it >= g1 || (step * nsub + sb) % kWaves != wv) continue;
+        const float* o = red + (size_t)((step & 1) * nsub + sb) * per_sub + lane;
+        const int li = it / per, i0 = (it - li * per) * 8;
+        const int u_ = L.list[li];
+        const int mask = L.mask[u_], base = L.base[u_];
+#pragma unroll
+        for (int st = 0; st < SETS; ++st) {
+          float g = 0.0f, up = 0.0f;
+          for (int p = 0; p < 2 * ks; ++p) {
+            g += o[(st * 2 * ks + p) * 64];
+            up += o[((SETS + st) * 2 * ks + p) * 64];
+          }
+          const int t = st * 8 + (lane >> 3);
+          if ((mask >> t) & 1) {
+            const int rw = base + __popc(mask & ((1 << t) - 1));
+            h[(size_t)rw * I + i0 + (lane & 7)] =
+                (uint16_t)f32_to_bf16_bits(silu_f32(g) * up * L.wsum[rw]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// ---- down -------------------------------------------------------------------
+//
+// Workgroup b owns 16 columns of out and walks every distinct expert, so the
+// sum over a token's experts stays in its accumulators. A wavefront stages its
+// slice of the h rows (in phases of as many rows as fit; LDS of its own, so no
+// barrier), 16-byte granule g of staged row s at g ^ (s & 7); the columns of
+// tokens that did not pick the expert read a row of zeros, and their results
+// are left out of the sum (an expert with infinite or NaN weights reaches its
+// own tokens only).
+
+constexpr size_t kDownLds = 150 * 1024;  // staged rows, all wavefronts
+
+template <int CPW, int SETS, int R, bool TAIL>
+__global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows) {
+  extern __shared__ __align__(16) unsigned char smem[];  // [waves][max_rows + 1][512 CPW bytes]
+  __shared__ int l_row[kMaxPicks], l_mask[kMaxPicks], l_base[kMaxPicks + 1];
+  const int H = a.H, I = a.I, T = a.T;
+  const Cut cut = cut_of(I);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int ks = cut.ks, nsub = cut.sub;
+  const int slice = wv % ks, sub = wv / ks;
+  Lane<CPW, TAIL> ln;
+  ln.init(lane, slice, I);
+  const Tables* tab = static_cast<const Tables*>(a.workspace);
+  const uint16_t* h =
+      reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(a.workspace) + kTableBytes);
+  const int n_u = __builtin_amdgcn_readfirstlane(tab->n_u);
+  for (int i = tid; i < a.T * a.k; i += blockDim.x) {
+    l_row[i] = i < n_u ? tab->row[i] : 0;
+    l_mask[i] = i < n_u ? tab->mask[i] : 0;
+    if (i < n_u) l_base[i] = tab->base[i];
+    if (i == n_u - 1) l_base[n_u] = tab->base[i] + __popc(tab->mask[i]);
+  }
+  constexpr int kSlice = 512 * CPW;  // bytes of a staged row
+  unsigned char* hs = smem + (size_t)wv * (max_rows + 1) * kSlice;
+  for (int i = lane; i < kSlice / 16; i += 64)
+    *reinterpret_cast<uint4*>(hs + (size_t)max_rows * kSlice + 16 * i) = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+
+  const int o0 = blockIdx.x * 16;
+  const size_t wrb = I / 2, srb = I / 32;
+  Slot<CPW> ring[R];
+  auto issue = [&](Slot<CPW>& o, int v) {
+    const int u = v * nsub + sub;
+    const bool live = u < n_u;
+    const int code = __builtin_amdgcn_readfirstlane(l_row[live ? u : 0]);
+    const bool hot = live ? code >= 0 : (a.hot.n_rows > 0 && !a.hot.host) || a.cold.n_rows == 0;
+    const FewBank& b = hot ? a.hot : a.cold;
+    const size_t row = live ? (size_t)(uint32_t)(code >= 0 ? code : -1 - code) : 0;
+    const size_t r0 = row * H + (live ? o0 : 0);
+    ln.template load<false>(o, b.w2 + r0 * wrb, b.w2 + (r0 + 8) * wrb,
+                            b.s2 + (r0 + ln.srow) * srb);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  f32x4 acc[2][SETS];
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+#pragma unroll
+    for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  if (n_u > 0) {
+#pragma unroll
+    for (int u = 0; u < R; ++u) issue(ring[u], u);
+  }
+  const int steps = sub < n_u ? (n_u - sub + nsub - 1) / nsub : 0;
+  int ph0 = 0, ph_end = 0;  // first staged h row; first expert past the phase
+  // h rows of the experts from u on, as many whole experts as fit
+  auto stage = [&](int u) {
+    ph0 = __builtin_amdgcn_readfirstlane(l_base[u]);
+    ph_end = u;
+    while (ph_end < n_u && __builtin_amdgcn_readfirstlane(l_base[ph_end + 1]) - ph0 <= max_rows)
+      ++ph_end;
+    const int nr = __builtin_amdgcn_readfirstlane(l_base[ph_end]) - ph0;
+    constexpr int kG = kSlice / 16;          // granules per row: 32, 64 or 128
+    constexpr int kB = 8;                    // granules per lane per batch
+    for (int i0 = 0; i0 < nr * kG; i0 += 64 * kB) {
+      uint4 v[kB];
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        const int i = min(i0 + b * 64 + lane, nr * kG - 1);
+        const int s = i / kG, g = i % kG;
+        const int e = slice * CPW * kChunkElems + g * 8;
+        const uint4 w =
+            *reinterpret_cast<const uint4*>(h + (size_t)(ph0 + s) * I + (e < I ? e : 0));
+        v[b] = e < I ? w : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        const int i = min(i0 + b * 64 + lane, nr * kG - 1);
+        const int s = i / kG, g = i % kG;
+        *reinterpret_cast<uint4*>(hs + (size_t)s * kSlice + 16 * (g ^ (s & 7))) = v[b];
+      }
+    }
+  };
+
+  for (int s0 = 0; s0 < steps; s0 += R) {
+#pragma unroll
+    for (int v = 0; v < R; ++v) {
+      const int step = s0 + v;
+      if (step >= steps) break;
+      const int u = step * nsub + sub;
+      if (u >= ph_end) stage(u);
+      const int mask = l_mask[u], base = l_base[u] - ph0;
+      f32x4 d[2][SETS];
+      const unsigned char* hp[SETS];  // this column's staged row
+      int sw[SETS];
+      bool has[SETS];
+#pragma unroll
+      for (int st = 0; st < SETS; ++st) {
+        const int t = st * 8 + (ln.r & 7);
+        has[st] = (mask >> t) & 1;
+        const int s = has[st] ? base + __popc(mask & ((1 << t) - 1)) : max_rows;
+        hp[st] = hs + (size_t)s * kSlice;
+        sw[st] = has[st] ? s & 7 : 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) d[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int j = 0; j < CPW; ++j) {
+        const float sc[2] = {ln.scale(ring[v], 0, j), ln.scale(ring[v], 1, j)};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          bf16x8 bv[SETS];
+#pragma unroll
+          for (int st = 0; st < SETS; ++st) {
+            const int g = 32 * j + (ln.r >= 8 ? 16 : 0) + 4 * ln.q + m;
+            bv[st] = *reinterpret_cast<const bf16x8*>(hp[st] + 16 * (g ^ sw[st]));
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const bf16x8 av = dequant8(word4(ring[v].w[g][j], m), sc[g]);
+#pragma unroll
+            for (int st = 0; st < SETS; ++st)
+              d[g][st] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv[st], d[g][st], 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int st = 0; st < SETS; ++st)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[g][st][e] += has[st] ? d[g][st][e] : 0.0f;
+      issue(ring[v], step + R);
+    }
+  }
+
+  // sum of the wavefronts' partial sums, in their order, and the one rounding
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);  // [wave][half][set][token][16]
+  if ((ln.r >= 8) == (ln.q >= 2)) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int st = 0; st < SETS; ++st)
+        *reinterpret_cast<f32x4*>(red + (((wv * 2 + (ln.r >= 8)) * SETS + st) * 8 + (ln.r & 7)) * 16 +
+                                  8 * g + 4 * (ln.q & 1)) = acc[g][st];
+  }
+  __syncthreads();
+  const int waves = blockDim.x >> 6;
+  for (int i = tid; i < T * 16; i += blockDim.x) {
+    const int t = i / 16, o = i % 16;
+    float s = 0.0f;
+    for (int p = 0; p < 2 * waves; ++p) s += red[((p * SETS + t / 8) * 8 + (t & 7)) * 16 + o];
+    a.out[(size_t)t * H + o0 + o] = (uint16_t)f32_to_bf16_bits(s);
+  }
+}
+
+template <int CPW, int SETS, int R, bool TAIL>
+hipError_t go_gate_up(const FewArgs& a, hipStream_t stream) {
+  const Cut c = cut_of(a.H);
+  const size_t lds = (size_t)2 * c.sub * 2 * SETS * 2 * c.ks * 64 * sizeof(float);
+  hipLaunchKernelGGL((few_gate_up<CPW, SETS, R, TAIL>), dim3(device_cus()), dim3(kThreads), lds,
+                     stream, a);
+  return hipGetLastError();
+}
+
+template <int CPW, int SETS, int R, bool TAIL>
+hipError_t go_down(const FewArgs& a, hipStream_t stream) {
+  const Cut c = cut_of(a.I);
+  const int waves = c.ks * c.sub;
+  const size_t per_row = (size_t)waves * 512 * CPW;
+  const int max_rows = (int)std::min<size_t>(kDownLds / per_row - 1, (size_t)a.T * a.k);
+  const size_t lds = std::max((size_t)(max_rows + 1) * per_row,
+                              (size_t)waves * 2 * SETS * 8 * 16 * sizeof(float));
+  hipLaunchKernelGGL((few_down<CPW, SETS, R, TAIL>), dim3(a.H / 16), dim3(64 * waves), lds,
+                     stream, a, max_rows);
+  return hipGetLastError();
+}
+
+// R: ring slots of 32 CPW + ... registers each; see the launch rule below.
+template <int CPW, int R, bool TAIL>
+hipError_t gate_up_sets(const FewArgs& a, hipStream_t s) {
+  return a.T <= 8 ? go_gate_up<CPW, 1, R, TAIL>(a, s) : go_gate_up<CPW, 2, R, TAIL>(a, s);
+}
+template <int CPW, int R, bool TAIL>
+hipError_t down_sets(const FewArgs& a, hipStream_t s) {
+  return a.T <= 8 ? go_down<CPW, 1, R, TAIL>(a, s) : go_down<CPW, 2, R, TAIL>(a, s);
+}
+
+}  // namespace
+
+bool layer_few_fits(int T, int k, int H, int I) {
+  return T <= MOE_FEW_MAX_TOKENS && k <= MOE_MAX_TOPK && H <= kMaxH && I <= kMaxI;
+}
+
+size_t layer_few_workspace_bytes(int T, int k, int I) {
+  return kTableBytes + (size_t)T * k * I * sizeof(uint16_t);
+}
+
+hipError_t launch_layer_few(const FewArgs& a, hipStream_t s) {
+  const Cut cg = cut_of(a.H), cd = cut_of(a.I);
+  const bool tg = a.H % (kChunkElems * cg.cpw * cg.ks) != 0;
+  const bool td = a.I % (kChunkElems * cd.cpw * cd.ks) != 0;
+  hipError_t e;
+  if (cg.cpw == 1)
+    e = tg ? gate_up_sets<1, 4, true>(a, s) : gate_up_sets<1, 4, false>(a, s);
+  else if (cg.cpw == 2)
+    e = tg ? gate_up_sets<2, 4, true>(a, s) : gate_up_sets<2, 4, false>(a, s);
+  else
+    e = tg ? gate_up_sets<4, 2, true>(a, s) : gate_up_sets<4, 2, false>(a, s);
+  if (e != hipSuccess) return e;
+  if (cd.cpw == 1) return td ? down_sets<1, 4, true>(a, s) : down_sets<1, 4, false>(a, s);
+  return td ? down_sets<2, 4, true>(a, s) : down_sets<2, 4, false>(a, s);
+}
+
+}  // namespace moe

@@ -328,6 +328,80 @@ int moe_swap_rows(const moe_bank *hot, const moe_bank *cold, int hot_row, int co
                   int32_t *hot_owner, int32_t *cold_owner, void *staging, size_t staging_bytes,
                   int H, int I, void *stream);
 
+/* Element types of the entry points that take more than bf16. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F16 1
+#define MOE_DTYPE_F32 2
+
+/* moe_topk_gate weights: softmax over the picked experts, or over all of the
+ * token's unmasked experts (the picks' shares of it, which then add up to less
+ * than 1). */
+#define MOE_GATE_NORM_PICKS 0
+#define MOE_GATE_NORM_ALL 1
+
+/*
+ * moe_topk_gate -- router logits to the top-k ids and weights that the split
+ * and the finalize take.
+ *
+ * For each token t: the k largest of logits[t][0 .. E) in descending order,
+ * equal ones (the two zeros are equal) by ascending expert id, into
+ * topk_ids[t][0 .. k), and their softmax weights into topk_w[t][0 .. k):
+ * exp(l - max) over its sum, in fp32. A logit of -inf or NaN masks its expert,
+ * which is never picked and has no share. Places for which no expert is left
+ * get id -1 and weight 0 (moe_route_split counts such picks as invalid;
+ * moe_layer_few_mxfp4 leaves them out of the sum). Where the largest logit is
+ * +inf, the infinite ones share the weight equally.
+ *
+ * logits: device, element type `dtype`, row t at logits + t * ld elements, ld
+ * >= E, aligned to its element size. 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <=
+ * min(E, MOE_MAX_TOPK). topk_ids: device int32 [T][k]. topk_w: device fp32
+ * [T][k]. Launches one kernel; nothing when T == 0. May be captured.
+ */
+int moe_topk_gate(const void *logits, int dtype, int64_t ld, int T, int E, int k, int norm,
+                  int32_t *topk_ids, float *topk_w, void *stream);
+
+/* Limits of moe_layer_few_mxfp4: tokens, hidden size H, intermediate size I. */
+#define MOE_FEW_MAX_TOKENS 16
+#define MOE_FEW_MAX_H 8192
+#define MOE_FEW_MAX_I 4096
+
+/* Bytes of the device workspace moe_layer_few_mxfp4 needs; 0 when an argument
+ * is <= 0 or past the limits above. */
+size_t moe_layer_few_workspace_bytes(int T, int k, int H, int I);
+
+/*
+ * moe_layer_few_mxfp4 -- the whole layer for at most MOE_FEW_MAX_TOKENS tokens
+ * in two launches: the split by the row map, both banks' expert FFN and the
+ * weighted sum over each token's picks.
+ *
+ * out[t] = bf16( sum over j of topk_w[t][j] * y(t, topk_ids[t][j]) ), with y
+ * as in moe_expert_ffn_mxfp4. The router weight multiplies the SwiGLU output
+ * before that is rounded to bf16, and the down products of a token's experts
+ * are summed in fp32 and rounded once, so the result is as accurate as that of
+ * moe_route_split, moe_expert_ffn_mxfp4 on both banks and moe_finalize, but
+ * not the same bits. Every sum has one order, given by the shapes and the order
+ * of the picks, so the bits do not depend on which bank holds an expert (a
+ * swap between steps, or an all-hot run, changes nothing).
+ *
+ * A pick whose id is outside [0, E) or whose row is outside its bank adds
+ * nothing and is counted in *n_invalid; a token without valid picks gets zeros.
+ * An id may repeat within a token. counts_layer, count_tmax: as for
+ * moe_route_split (NULL: no counting).
+ *
+ * hot, cold: banks as for moe_expert_ffn_mxfp4, each tensor 16-byte aligned;
+ * a bank without rows may have NULL tensors. row_map: device int32 [E]. x:
+ * device bf16 [T][H]. topk_ids: device int32 [T][k]. topk_w: device fp32
+ * [T][k]. n_invalid: device int32 [1]. workspace: device,
+ * moe_layer_few_workspace_bytes(T, k, H, I) bytes; calls that overlap need one
+ * each. out: device bf16 [T][H]; must not overlap x. x, workspace and out
+ * 16-byte aligned. MOE_ENOTSUP past the limits above. Launches nothing, and
+ * leaves *n_invalid as it was, when T == 0. May be captured.
+ */
+int moe_layer_few_mxfp4(const moe_bank *hot, const moe_bank *cold, const int32_t *row_map, int E,
+                        const uint16_t *x, const int32_t *topk_ids, const float *topk_w, int T,
+                        int k, int H, int I, int32_t *counts_layer, int count_tmax,
+                        int32_t *n_invalid, void *workspace, uint16_t *out, void *stream);
+
 /* Message for the last error returned on this thread ("" if none). */
 const char *moe_last_error(void);
 
