@@ -28,6 +28,7 @@
 // The order of every sum is fixed by the shapes and the picks' order alone, not
 // by the banks: a step gives the same bits wherever its experts are.
 #include <algorithm>
+#include <type_traits>
 
 #include "layer_ops.h"
 #include "mxfp4_common.h"
@@ -36,6 +37,8 @@ namespace moe {
 namespace {
 
 using namespace mx;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxPicks = MOE_FEW_MAX_TOKENS * MOE_MAX_TOPK;  // 512
 constexpr int kWaves = 8;
@@ -76,10 +79,19 @@ __device__ __forceinline__ void lds_barrier() {
 
 // One ring slot: the weights of 16 rows (two groups of 8) over the wavefront's
 // chunks, and the slice's scale bytes of row lane/4 (quarter lane%4 of them).
-template <int CPW>
+template <int CPW, bool TAIL>
 struct Slot {
   uint4 w[2][CPW];
-  uint32_t s[(CPW + 1) / 2];
+  // as loaded (widening a loaded half here would wait for it)
+  static constexpr bool kHalves = TAIL || CPW == 1;
+  std::conditional_t<kHalves, uint16_t, uint32_t> s[kHalves ? CPW : CPW / 2];
+  // the slice's scale bytes 4d .. 4d+3 of this lane's piece
+  __device__ __forceinline__ uint32_t word(int d) const {
+    if constexpr (kHalves && CPW > 1)
+      return (uint32_t)s[2 * d] | ((uint32_t)s[2 * d + 1] << 16);
+    else
+      return s[d];
+  }
 };
 
 // The lane's place in the weight rows of a slice: rows of K/2 bytes, K/32
@@ -113,10 +125,12 @@ struct Lane {
     }
   }
 
-  // g0, g1: the two groups' first weight rows; sp: this lane's scale row.
+  // g0, g1: the two groups' first weight rows; sb: the item's scale rows, of
+  // which this lane's starts at so.
   template <bool STREAM>
-  __device__ __forceinline__ void load(Slot<CPW>& o, const uint8_t* g0, const uint8_t* g1,
-                                       const uint8_t* sp) const {
+  __device__ __forceinline__ void load(Slot<CPW, TAIL>& o, const uint8_t* g0, const uint8_t* g1,
+                                       const uint8_t* sb, uint32_t so) const {
+    const uint8_t* sp = sb + so;
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {
       if constexpr (STREAM) {
@@ -127,14 +141,11 @@ struct Lane {
         o.w[1][j] = *reinterpret_cast<const uint4*>(g1 + woff[j]);
       }
     }
+    // nothing here looks at a loaded value: that would wait for it
     if constexpr (TAIL || CPW == 1) {
-      uint32_t h[CPW];
 #pragma unroll
       for (int i = 0; i < CPW; ++i)
-        h[i] = *reinterpret_cast<const uint16_t*>(sp + soff[TAIL ? i : 0]);
-#pragma unroll
-      for (int i = 0; i < (CPW + 1) / 2; ++i)
-        o.s[i] = h[2 * i] | (2 * i + 1 < CPW ? h[2 * i + 1 < CPW ? 2 * i + 1 : 0] << 16 : 0u);
+        o.s[i] = *reinterpret_cast<const uint16_t*>(sp + soff[TAIL ? i : 0]);
     } else {
       // K is a multiple of 256 * CPW: the row's scale bytes and this piece of
       // them are 2 * CPW-byte aligned within the tensor
@@ -150,16 +161,16 @@ struct Lane {
   }
 
   // This lane's scale for group g, chunk j: byte 8j + piece of row (r & 7) + 8g.
-  __device__ __forceinline__ float scale(const Slot<CPW>& o, int g, int j) const {
+  __device__ __forceinline__ float scale(const Slot<CPW, TAIL>& o, int g, int j) const {
     const int b = 8 * j + q + (r >= 8 ? 4 : 0);
     const int src = 32 * g + 4 * (r & 7) + b / (2 * CPW), byte = b % (2 * CPW);
     uint32_t v;
     if constexpr (CPW == 4) {
-      const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.s[0]);
-      const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.s[1]);
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.word(0));
+      const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.word(1));
       v = byte >= 4 ? hi : lo;
     } else {
-      v = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.s[0]);
+      v = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.word(0));
     }
     v = (v >> (8 * (byte & 3))) & 0xffu;
     return e8m0_to_f32(in[j] ? v : 127u);
@@ -336,81 +347,111 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
     }
   }
 
-  // this workgroup's run of items (list entry, 8 rows of I)
+  // this workgroup's run of items (list entry, 8 rows of I): [g0, g1)
   const int per = I / 8;
   const int hb = n_dev < n_u ? min(kHostBlocks, (int)gridDim.x - 1) : 0;
   const bool on_host = (int)blockIdx.x < hb;
-  const int64_t n = (int64_t)(on_host ? n_u - n_dev : n_dev) * per;
-  const int blocks = on_host ? hb : (int)gridDim.x - hb;
-  const int blk = on_host ? (int)blockIdx.x : (int)blockIdx.x - hb;
+  const uint32_t n = (uint32_t)(on_host ? n_u - n_dev : n_dev) * per;  // < 2^19
+  const uint32_t blocks = on_host ? hb : gridDim.x - hb;
+  const uint32_t blk = on_host ? blockIdx.x : blockIdx.x - hb;
   const int first = on_host ? n_dev * per : 0;
   const int g0 = first + (int)(n * blk / blocks), g1 = first + (int)(n * (blk + 1) / blocks);
   if (g0 >= g1) return;  // the whole workgroup
   const int steps = (g1 - g0 + nsub - 1) / nsub;
 
   const size_t wrb = H / 2, srb = H / 32;
-  Slot<CPW> ring[R];
-  // Past the run's end a load reads the first rows of a device bank (the same
-  // for every wavefront, so they stay in the L2) to keep the stream
-  // unconditional.
-  auto issue = [&](Slot<CPW>& o, int step) {
-    const int it = g0 + step * nsub + sub;
-    const bool live = step < steps && it < g1 && active;
-    const int li = live ? it / per : 0;
-    const int code = __builtin_amdgcn_readfirstlane(L.row[L.list[li]]);
-    const int i0 = live ? (it - li * per) * 8 : 0;
-    const bool hot = live ? code >= 0 : (a.hot.n_rows > 0 && !a.hot.host) || a.cold.n_rows == 0;
-    const FewBank& b = hot ? a.hot : a.cold;
-    const size_t row = live ? (size_t)(uint32_t)(code >= 0 ? code : -1 - code) : 0;
-    const size_t r0 = row * 2 * (size_t)I + i0, r1 = r0 + I;
-    const uint8_t* sp = b.s13 + (r0 + (ln.srow & 7)) * srb + (ln.srow >= 8 ? (size_t)I * srb : 0);
-    ln.template load<!TAIL>(o, b.w13 + r0 * wrb, b.w13 + r1 * wrb, sp);
+  // this lane's scale row of an item, from its first gate row
+  const uint32_t srow_off = ((ln.srow & 7) + (ln.srow >= 8 ? (uint32_t)I : 0u)) * (uint32_t)srb;
+  // The prefetch cursor: this wavefront's next item, its place in its expert
+  // and its first gate row. Past the run's end it stays on the first rows of a
+  // device bank (the same for every wavefront, so they stay in the L2), which
+  // keeps the stream unconditional.
+  const uint8_t *cw, *cs;
+  int c_it = g0 + sub, c_li, c_ib;
+  auto enter = [&]() {  // expert c_li, rows 8 c_ib
+    const int code = __builtin_amdgcn_readfirstlane(L.row[L.list[c_li]]);
+    const FewBank& b = code >= 0 ? a.hot : a.cold;
+    const size_t r0 = (size_t)(uint32_t)(code >= 0 ? code : -1 - code) * 2 * I + 8 * c_ib;
+    cw = b.w13 + r0 * wrb;
+    cs = b.s13 + r0 * srb;
+  };
+  auto park = [&]() {
+    const bool hot = (a.hot.n_rows > 0 && !a.hot.host) || a.cold.n_rows == 0;
+    cw = hot ? a.hot.w13 : a.cold.w13;
+    cs = hot ? a.hot.s13 : a.cold.s13;
+  };
+  c_li = c_it / per;
+  c_ib = c_it - c_li * per;
+  if (c_it < g1 && active)
+    enter();
+  else
+    park();
+  auto advance = [&]() {
+    c_it += nsub;
+    c_ib += nsub;
+    if (c_it >= g1 || !active) {
+      park();
+    } else if (c_ib >= per) {
+      do {
+        c_ib -= per;
+        ++c_li;
+      } while (c_ib >= per);
+      enter();
+    } else {
+      cw += (size_t)(8 * nsub) * wrb;
+      cs += (size_t)(8 * nsub) * srb;
+    }
+  };
+  Slot<CPW, TAIL> ring[R];
+  auto issue = [&](Slot<CPW, TAIL>& o) {
+    ln.template load<!TAIL>(o, cw, cw + (size_t)I * wrb, cs, srow_off);
     __builtin_amdgcn_sched_barrier(0);
+    advance();
   };
   // floats of one (buffer, sub): [group][set][partial][token][row]
   const int per_sub = 2 * SETS * 2 * ks * 64;
+  const bool diag = (ln.r >= 8) == (ln.q >= 2) && active;
+  const int red_off = (2 * slice + (ln.r >= 8)) * 64 + (ln.r & 7) * 8 + (ln.q & 1) * 4;
 
 #pragma unroll
-  for (int u = 0; u < R; ++u) issue(ring[u], u);
+  for (int u = 0; u < R; ++u) issue(ring[u]);
 
-  for (int s0 = 0;; s0 += R) {
+  // Whole turns of the ring (steps past the run's end multiply parked weights
+  // and store nothing): leaving the loop inside a turn made the compiler wait
+  // for nearly every load in flight once per turn.
+  for (int s0 = 0; s0 < steps; s0 += R) {
 #pragma unroll
     for (int u = 0; u < R; ++u) {
       const int step = s0 + u;
-      if (step >= steps) return;
-      if (active) {
-        f32x4 acc[2][SETS];
+      f32x4 acc[2][SETS];
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < CPW; ++j) {
+        const float sc[2] = {ln.scale(ring[u], 0, j), ln.scale(ring[u], 1, j)};
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const bf16x8 av = dequant8(word4(ring[u].w[g][j], m), sc[g]);
+#pragma unroll
+            for (int st = 0; st < SETS; ++st)
+              acc[g][st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xb[st][j][m], acc[g][st],
+                                                                   0, 0, 0);
+          }
+      }
+      issue(ring[u]);
+      // lane (c, q) holds rows 4q .. 4q+3 of column c: keep the diagonal blocks
+      if (diag) {
+        float* o = red + (size_t)((step & 1) * nsub + sub) * per_sub + red_off;
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < CPW; ++j) {
-          const float sc[2] = {ln.scale(ring[u], 0, j), ln.scale(ring[u], 1, j)};
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const bf16x8 av = dequant8(word4(ring[u].w[g][j], m), sc[g]);
-#pragma unroll
-              for (int st = 0; st < SETS; ++st)
-                acc[g][st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xb[st][j][m],
-                                                                     acc[g][st], 0, 0, 0);
-            }
-        }
-        // lane (c, q) holds rows 4q .. 4q+3 of column c: keep the diagonal blocks
-        if ((ln.r >= 8) == (ln.q >= 2)) {
-          float* o = red + (size_t)((step & 1) * nsub + sub) * per_sub;
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int st = 0; st < SETS; ++st)
-              *reinterpret_cast<f32x4*>(
-                  o + ((g * SETS + st) * 2 * ks + 2 * slice + (ln.r >= 8)) * 64 +
-                  (ln.r & 7) * 8 + (ln.q & 1) * 4) = acc[g][st];
-        }
+          for (int st = 0; st < SETS; ++st)
+            *reinterpret_cast<f32x4*>(o + (g * SETS + st) * 2 * ks * 64) = acc[g][st];
       }
-      issue(ring[u], step + R);
       lds_barrier();
       // One wavefront per item, each in turn, adds the partial sums (in their
       // order) and writes h; the others go on. A buffer is written again two
@@ -426,9 +467,15 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
 #pragma unroll
         for (int st = 0; st < SETS; ++st) {
           float g = 0.0f, up = 0.0f;
-          for (int p = 0; p < 2 * ks; ++p) {
+          auto add = [&](int p) {
             g += o[(st * 2 * ks + p) * 64];
             up += o[((SETS + st) * 2 * ks + p) * 64];
+          };
+          if (ks == kWaves) {
+#pragma unroll
+            for (int p = 0; p < 2 * kWaves; ++p) add(p);
+          } else {
+            for (int p = 0; p < 2 * ks; ++p) add(p);
           }
           const int t = st * 8 + (lane >> 3);
           if ((mask >> t) & 1) {
@@ -484,17 +531,19 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
 
   const int o0 = blockIdx.x * 16;
   const size_t wrb = I / 2, srb = I / 32;
-  Slot<CPW> ring[R];
-  auto issue = [&](Slot<CPW>& o, int v) {
+  const uint32_t srow_off = (uint32_t)ln.srow * (uint32_t)srb;
+  Slot<CPW, TAIL> ring[R];
+  // past the last expert: the first rows of a device bank (see few_gate_up)
+  auto issue = [&](Slot<CPW, TAIL>& o, int v) {
     const int u = v * nsub + sub;
     const bool live = u < n_u;
     const int code = __builtin_amdgcn_readfirstlane(l_row[live ? u : 0]);
     const bool hot = live ? code >= 0 : (a.hot.n_rows > 0 && !a.hot.host) || a.cold.n_rows == 0;
-    const FewBank& b = hot ? a.hot : a.cold;
-    const size_t row = live ? (size_t)(uint32_t)(code >= 0 ? code : -1 - code) : 0;
-    const size_t r0 = row * H + (live ? o0 : 0);
-    ln.template load<false>(o, b.w2 + r0 * wrb, b.w2 + (r0 + 8) * wrb,
-                            b.s2 + (r0 + ln.srow) * srb);
+    const uint8_t* w2 = hot ? a.hot.w2 : a.cold.w2;
+    const uint8_t* s2 = hot ? a.hot.s2 : a.cold.s2;
+    const uint32_t row = live ? (uint32_t)(code >= 0 ? code : -1 - code) : 0u;
+    const size_t r0 = (size_t)row * H + (live ? o0 : 0);
+    ln.template load<false>(o, w2 + r0 * wrb, w2 + (r0 + 8) * wrb, s2 + r0 * srb, srow_off);
     __builtin_amdgcn_sched_barrier(0);
   };
   f32x4 acc[2][SETS];
@@ -516,36 +565,49 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
     while (ph_end < n_u && __builtin_amdgcn_readfirstlane(l_base[ph_end + 1]) - ph0 <= max_rows)
       ++ph_end;
     const int nr = __builtin_amdgcn_readfirstlane(l_base[ph_end]) - ph0;
-    constexpr int kG = kSlice / 16;          // granules per row: 32, 64 or 128
-    constexpr int kB = 8;                    // granules per lane per batch
+    constexpr int kG = kSlice / 16;  // granules per row: 32, 64 or 128
+    constexpr int kB = 8;            // granules per lane per batch
     for (int i0 = 0; i0 < nr * kG; i0 += 64 * kB) {
-      uint4 v[kB];
+      u32x4 v[kB];
+      uint32_t off[kB];
+      int dst[kB];
+      uint32_t past = 0;  // bit b: granule b lies past the end of the axis
 #pragma unroll
       for (int b = 0; b < kB; ++b) {
         const int i = min(i0 + b * 64 + lane, nr * kG - 1);
         const int s = i / kG, g = i % kG;
         const int e = slice * CPW * kChunkElems + g * 8;
-        const uint4 w =
-            *reinterpret_cast<const uint4*>(h + (size_t)(ph0 + s) * I + (e < I ? e : 0));
-        v[b] = e < I ? w : make_uint4(0, 0, 0, 0);
+        past |= (e < I ? 0u : 1u) << b;
+        off[b] = ((uint32_t)(ph0 + s) * (uint32_t)I + (uint32_t)(e < I ? e : 0)) * 2u;
+        dst[b] = s * kSlice + 16 * (g ^ (s & 7));
       }
+      // Loads and their wait in one block: as ordinary loads under this branch
+      // they made the compiler wait for every weight in flight at each expert.
+      asm volatile(
+          "global_load_dwordx4 %0, %8, %16\n\tglobal_load_dwordx4 %1, %9, %16\n\t"
+          "global_load_dwordx4 %2, %10, %16\n\tglobal_load_dwordx4 %3, %11, %16\n\t"
+          "global_load_dwordx4 %4, %12, %16\n\tglobal_load_dwordx4 %5, %13, %16\n\t"
+          "global_load_dwordx4 %6, %14, %16\n\tglobal_load_dwordx4 %7, %15, %16\n\t"
+          "s_waitcnt vmcnt(0)"
+          : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]),
+            "=&v"(v[6]), "=&v"(v[7])
+          : "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "v"(off[4]), "v"(off[5]),
+            "v"(off[6]), "v"(off[7]), "s"(h)
+          : "memory");
 #pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        const int i = min(i0 + b * 64 + lane, nr * kG - 1);
-        const int s = i / kG, g = i % kG;
-        *reinterpret_cast<uint4*>(hs + (size_t)s * kSlice + 16 * (g ^ (s & 7))) = v[b];
-      }
+      for (int b = 0; b < kB; ++b)
+        *reinterpret_cast<u32x4*>(hs + dst[b]) = (past >> b) & 1u ? u32x4{0, 0, 0, 0} : v[b];
     }
   };
 
-  for (int s0 = 0; s0 < steps; s0 += R) {
+  for (int s0 = 0; s0 < steps; s0 += R) {  // whole turns of the ring, as above
 #pragma unroll
     for (int v = 0; v < R; ++v) {
       const int step = s0 + v;
-      if (step >= steps) break;
-      const int u = step * nsub + sub;
-      if (u >= ph_end) stage(u);
-      const int mask = l_mask[u], base = l_base[u] - ph0;
+      const bool live = step < steps;
+      const int u = live ? step * nsub + sub : 0;
+      if (live && u >= ph_end) stage(u);
+      const int mask = live ? l_mask[u] : 0, base = l_base[u] - ph0;
       f32x4 d[2][SETS];
       const unsigned char* hp[SETS];  // this column's staged row
       int sw[SETS];
@@ -662,12 +724,12 @@ hipError_t launch_layer_few(const FewArgs& a, hipStream_t s) {
   if (cg.cpw == 1)
     e = tg ? gate_up_sets<1, 4, true>(a, s) : gate_up_sets<1, 4, false>(a, s);
   else if (cg.cpw == 2)
-    e = tg ? gate_up_sets<2, 4, true>(a, s) : gate_up_sets<2, 4, false>(a, s);
+    e = tg ? gate_up_sets<2, 3, true>(a, s) : gate_up_sets<2, 3, false>(a, s);
   else
     e = tg ? gate_up_sets<4, 2, true>(a, s) : gate_up_sets<4, 2, false>(a, s);
   if (e != hipSuccess) return e;
   if (cd.cpw == 1) return td ? down_sets<1, 4, true>(a, s) : down_sets<1, 4, false>(a, s);
-  return td ? down_sets<2, 4, true>(a, s) : down_sets<2, 4, false>(a, s);
+  return td ? down_sets<2, 3, true>(a, s) : down_sets<2, 3, false>(a, s);
 }
 
 }  // namespace moe
