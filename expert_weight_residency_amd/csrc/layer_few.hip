@@ -62,10 +62,24 @@ constexpr size_t kTableBytes = (sizeof(Tables) + 255) / 256 * 256;
 struct Cut {
   int nchunk, cpw, ks, sub;
 };
-__host__ __device__ inline Cut cut_of(int K) {
+// Gate/up: as many wavefronts per row as there are (its partial sums go through
+// LDS for every item anyway, and short slices keep the x operands few).
+__host__ __device__ inline Cut gate_up_cut(int H) {
   Cut c;
-  c.nchunk = (K + kChunkElems - 1) / kChunkElems;
+  c.nchunk = (H + kChunkElems - 1) / kChunkElems;
   c.cpw = c.nchunk <= 8 ? 1 : (c.nchunk <= 16 ? 2 : 4);
+  c.ks = (c.nchunk + c.cpw - 1) / c.cpw;
+  c.sub = kWaves / c.ks;
+  return c;
+}
+// Down: at most 4 wavefronts per row and the rest on other experts, so that the
+// SIMDs have equal shares and an expert's fixed cost is paid by few wavefronts
+// (7 tokens at I = 2880: 6 wavefronts of 2 chunks 56 us, 2 x 4 of 3 chunks
+// 47.7 us).
+__host__ __device__ inline Cut down_cut(int I) {
+  Cut c;
+  c.nchunk = (I + kChunkElems - 1) / kChunkElems;
+  c.cpw = (c.nchunk + 3) / 4;
   c.ks = (c.nchunk + c.cpw - 1) / c.cpw;
   c.sub = kWaves / c.ks;
   return c;
@@ -78,57 +92,54 @@ __device__ __forceinline__ void lds_barrier() {
 }
 
 // One ring slot: the weights of 16 rows (two groups of 8) over the wavefront's
-// chunks, and the slice's scale bytes of row lane/4 (quarter lane%4 of them).
-template <int CPW, bool TAIL>
+// chunks and their scale bytes, as loaded (nothing looks at a loaded value
+// before its step: widening a half word at the load would wait for it). Lane l
+// loads scale bytes of row l / 4. WIDE (gate/up, whole slices): 2 CPW
+// consecutive bytes of the slice in one load; otherwise two bytes of each chunk.
+template <int CPW, bool WIDE>
 struct Slot {
   uint4 w[2][CPW];
-  // as loaded (widening a loaded half here would wait for it)
-  static constexpr bool kHalves = TAIL || CPW == 1;
-  std::conditional_t<kHalves, uint16_t, uint32_t> s[kHalves ? CPW : CPW / 2];
-  // the slice's scale bytes 4d .. 4d+3 of this lane's piece
-  __device__ __forceinline__ uint32_t word(int d) const {
-    if constexpr (kHalves && CPW > 1)
-      return (uint32_t)s[2 * d] | ((uint32_t)s[2 * d + 1] << 16);
-    else
-      return s[d];
-  }
+  std::conditional_t<WIDE, uint32_t, uint16_t> s[WIDE ? CPW / 2 : CPW];
 };
 
 // The lane's place in the weight rows of a slice: rows of K/2 bytes, K/32
 // scale bytes. Pieces (32 elements, 16 bytes, 1 scale byte) past the end of the
 // axis are read at the row's start instead; their scale becomes 1 and their
 // activations are zero.
-template <int CPW, bool TAIL>
+template <int CPW, bool WIDE>
 struct Lane {
-  uint32_t woff[CPW];       // weight bytes, within a group of 8 rows
-  uint32_t soff[TAIL ? CPW : 1];  // scale bytes, within this lane's row
+  uint32_t woff[CPW];              // weight bytes, within a group of 8 rows
+  uint32_t soff[WIDE ? 1 : CPW];   // scale bytes, within this lane's row
   bool in[CPW];
-  int r, q, srow;
+  int r, q, srow, piece;
 
   __device__ __forceinline__ void init(int lane, int slice, int K) {
     r = lane & 15;
     q = lane >> 4;
     srow = lane >> 2;
-    const int nblk = K / 32, piece = q + (r >= 8 ? 4 : 0);
+    piece = q + (r >= 8 ? 4 : 0);
+    const int nblk = K / 32;  // even
 #pragma unroll
     for (int j = 0; j < CPW; ++j) {
       const int b = (slice * CPW + j) * 8 + piece;
-      in[j] = !TAIL || b < nblk;
+      in[j] = WIDE || b < nblk;
       woff[j] = (uint32_t)(r & 7) * (uint32_t)(K / 2) + 16u * (uint32_t)(in[j] ? b : 0);
     }
-    const int s0 = slice * CPW * 8 + (lane & 3) * 2 * CPW;
-    if constexpr (TAIL) {
-#pragma unroll
-      for (int i = 0; i < CPW; ++i) soff[i] = s0 + 2 * i < nblk ? s0 + 2 * i : 0;
+    if constexpr (WIDE) {
+      soff[0] = slice * CPW * 8 + (lane & 3) * 2 * CPW;
     } else {
-      soff[0] = s0;
+#pragma unroll
+      for (int j = 0; j < CPW; ++j) {
+        const int b = (slice * CPW + j) * 8 + 2 * (lane & 3);
+        soff[j] = b < nblk ? b : 0;
+      }
     }
   }
 
   // g0, g1: the two groups' first weight rows; sb: the item's scale rows, of
   // which this lane's starts at so.
   template <bool STREAM>
-  __device__ __forceinline__ void load(Slot<CPW, TAIL>& o, const uint8_t* g0, const uint8_t* g1,
+  __device__ __forceinline__ void load(Slot<CPW, WIDE>& o, const uint8_t* g0, const uint8_t* g1,
                                        const uint8_t* sb, uint32_t so) const {
     const uint8_t* sp = sb + so;
 #pragma unroll
@@ -141,39 +152,53 @@ struct Lane {
         o.w[1][j] = *reinterpret_cast<const uint4*>(g1 + woff[j]);
       }
     }
-    // nothing here looks at a loaded value: that would wait for it
-    if constexpr (TAIL || CPW == 1) {
+    if constexpr (!WIDE) {
 #pragma unroll
-      for (int i = 0; i < CPW; ++i)
-        o.s[i] = *reinterpret_cast<const uint16_t*>(sp + soff[TAIL ? i : 0]);
+      for (int j = 0; j < CPW; ++j) o.s[j] = *reinterpret_cast<const uint16_t*>(sp + soff[j]);
+    } else if constexpr (CPW == 2) {
+      o.s[0] = *reinterpret_cast<const uint32_t*>(sp + soff[0]);
     } else {
-      // K is a multiple of 256 * CPW: the row's scale bytes and this piece of
-      // them are 2 * CPW-byte aligned within the tensor
-      
-      if constexpr (CPW == 2) {
-        o.s[0] = *reinterpret_cast<const uint32_t*>(sp + soff[0]);
-      } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(sp + soff[0]);
-        o.s[0] = v.x;
-        o.s[1] = v.y;
-      }
+      const uint2 v = *reinterpret_cast<const uint2*>(sp + soff[0]);
+      o.s[0] = v.x;
+      o.s[1] = v.y;
     }
   }
 
-  // This lane's scale for group g, chunk j: byte 8j + piece of row (r & 7) + 8g.
-  __device__ __forceinline__ float scale(const Slot<CPW, TAIL>& o, int g, int j) const {
-    const int b = 8 * j + q + (r >= 8 ? 4 : 0);
-    const int src = 32 * g + 4 * (r & 7) + b / (2 * CPW), byte = b % (2 * CPW);
-    uint32_t v;
-    if constexpr (CPW == 4) {
-      const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.word(0));
-      const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.word(1));
-      v = byte >= 4 ? hi : lo;
+  // This lane's scales of group g: the E8M0 byte of its piece of chunk j, of row
+  // (r & 7) + 8g, turned into the exponent field of the conversion's fp32 scale
+  // operand. The instruction reads that field only (checked for all 256 bytes
+  // and any sign and mantissa: the same results as the exact power of two, its
+  // subnormal and NaN included), so a rotation replaces e8m0_to_f32's selects.
+  __device__ __forceinline__ void scales(const Slot<CPW, WIDE>& o, int g, float (&sc)[CPW]) const {
+    const int row = 32 * g + 4 * (r & 7);
+    auto fetch = [&](int src, uint32_t v) {
+      return (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)v);
+    };
+    auto expo = [&](uint32_t v, int byte, bool ok) {
+      const uint32_t e = __builtin_rotateright32(v, (uint32_t)(8 * byte + 9) & 31u);
+      return __uint_as_float(ok ? e : 0x3f800000u);
+    };
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int j = 0; j < CPW; ++j) {
+        const int b = 8 * j + piece, src = row + b / (2 * CPW), byte = b % (2 * CPW);
+        uint32_t v = fetch(src, o.s[0]);
+        if constexpr (CPW == 4) {
+          const uint32_t hi = fetch(src, o.s[1]);
+          v = byte >= 4 ? hi : v;
+        }
+        sc[j] = expo(v, byte & 3, true);
+      }
     } else {
-      v = (uint32_t)__builtin_amdgcn_ds_bpermute(src * 4, (int)o.word(0));
+#pragma unroll
+      for (int j = 0; j < CPW; j += 2) {
+        const uint32_t pair =
+            (uint32_t)o.s[j] | (j + 1 < CPW ? (uint32_t)o.s[j + 1 < CPW ? j + 1 : j] << 16 : 0u);
+        const uint32_t v = fetch(row + (piece >> 1), pair);
+        sc[j] = expo(v, piece & 1, in[j]);
+        if (j + 1 < CPW) sc[j + 1] = expo(v, 2 + (piece & 1), in[j + 1 < CPW ? j + 1 : j]);
+      }
     }
-    v = (v >> (8 * (byte & 3))) & 0xffu;
-    return e8m0_to_f32(in[j] ? v : 127u);
   }
 };
 
@@ -298,18 +323,18 @@ __device__ void build_tables(const FewArgs& a, Shared& L) {
 // beside them.
 constexpr int kHostBlocks = 8;
 
-template <int CPW, int SETS, int R, bool TAIL>
+template <int CPW, int SETS, int R, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
   extern __shared__ __align__(16) float red[];  // [2][SUB][2 groups][SETS][2 KS][8][8]
   __shared__ __align__(16) Shared L;
   const int H = a.H, I = a.I, T = a.T;
-  const Cut cut = cut_of(H);
+  const Cut cut = gate_up_cut(H);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ks = cut.ks, nsub = cut.sub;
   const int slice = wv % ks, sub = wv / ks;
   const bool active = sub < nsub;
-  Lane<CPW, TAIL> ln;
+  Lane<CPW, WIDE> ln;
   ln.init(lane, slice, H);
 
   // this wavefront's slice of x as B operands: column c holds token c (first
@@ -402,9 +427,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
       cs += (size_t)(8 * nsub) * srb;
     }
   };
-  Slot<CPW, TAIL> ring[R];
-  auto issue = [&](Slot<CPW, TAIL>& o) {
-    ln.template load<!TAIL>(o, cw, cw + (size_t)I * wrb, cs, srow_off);
+  Slot<CPW, WIDE> ring[R];
+  auto issue = [&](Slot<CPW, WIDE>& o) {
+    ln.template load<WIDE>(o, cw, cw + (size_t)I * wrb, cs, srow_off);
     __builtin_amdgcn_sched_barrier(0);
     advance();
   };
@@ -428,14 +453,16 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
       for (int g = 0; g < 2; ++g)
 #pragma unroll
         for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
+      float sc[2][CPW];
+      ln.scales(ring[u], 0, sc[0]);
+      ln.scales(ring[u], 1, sc[1]);
 #pragma unroll
       for (int j = 0; j < CPW; ++j) {
-        const float sc[2] = {ln.scale(ring[u], 0, j), ln.scale(ring[u], 1, j)};
 #pragma unroll
         for (int m = 0; m < 4; ++m)
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const bf16x8 av = dequant8(word4(ring[u].w[g][j], m), sc[g]);
+            const bf16x8 av = dequant8(word4(ring[u].w[g][j], m), sc[g][j]);
 #pragma unroll
             for (int st = 0; st < SETS; ++st)
               acc[g][st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xb[st][j][m], acc[g][st],
@@ -492,50 +519,58 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
 // ---- down -------------------------------------------------------------------
 //
 // Workgroup b owns 16 columns of out and walks every distinct expert, so the
-// sum over a token's experts stays in its accumulators. A wavefront stages its
-// slice of the h rows (in phases of as many rows as fit; LDS of its own, so no
-// barrier), 16-byte granule g of staged row s at g ^ (s & 7); the columns of
-// tokens that did not pick the expert read a row of zeros, and their results
-// are left out of the sum (an expert with infinite or NaN weights reaches its
-// own tokens only).
+// sum over a token's experts stays in its accumulators. The wavefronts of a row
+// take every SUB-th expert. The h rows are staged in LDS in phases of as many
+// whole experts as fit, 16-byte granule g of staged row s at g ^ (s & 7); the
+// columns of tokens that did not pick the expert read a row of zeros, and their
+// results are left out of the sum (an expert with infinite or NaN weights
+// reaches its own tokens only). An expert's weights are
+// requested as soon as those of the wavefront's last one are multiplied; more in
+// flight was no faster (two experts 50.2 us, three 51.8 against 47.7 at 7
+// tokens): rows of 1440 bytes share lines, which the L2 then drops between
+// their two reads. B operands straight from memory instead of staged rows cost
+// 16 more loads per expert and wavefront (49.4 us at 7 tokens, 112 against 96 at
+// 16).
 
-constexpr size_t kDownLds = 150 * 1024;  // staged rows, all wavefronts
+constexpr size_t kDownLds = 150 * 1024;  // staged rows and the row of zeros
 
-template <int CPW, int SETS, int R, bool TAIL>
+template <int CPW, int SETS>
 __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows) {
-  extern __shared__ __align__(16) unsigned char smem[];  // [waves][max_rows + 1][512 CPW bytes]
+  extern __shared__ __align__(16) unsigned char hs[];  // [max_rows + 1][512 CPW KS bytes]
   __shared__ int l_row[kMaxPicks], l_mask[kMaxPicks], l_base[kMaxPicks + 1];
   const int H = a.H, I = a.I, T = a.T;
-  const Cut cut = cut_of(I);
-  const int tid = threadIdx.x, lane = tid & 63;
+  const Cut cut = down_cut(I);
+  const int tid = threadIdx.x, lane = tid & 63, threads = blockDim.x;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ks = cut.ks, nsub = cut.sub;
   const int slice = wv % ks, sub = wv / ks;
-  Lane<CPW, TAIL> ln;
+  Lane<CPW, false> ln;
   ln.init(lane, slice, I);
   const Tables* tab = static_cast<const Tables*>(a.workspace);
   const uint16_t* h =
       reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(a.workspace) + kTableBytes);
   const int n_u = __builtin_amdgcn_readfirstlane(tab->n_u);
-  for (int i = tid; i < a.T * a.k; i += blockDim.x) {
-    l_row[i] = i < n_u ? tab->row[i] : 0;
-    l_mask[i] = i < n_u ? tab->mask[i] : 0;
-    if (i < n_u) l_base[i] = tab->base[i];
-    if (i == n_u - 1) l_base[n_u] = tab->base[i] + __popc(tab->mask[i]);
+  for (int i = tid; i < T * a.k; i += threads) {
+    const int row = tab->row[i], mask = tab->mask[i], base = tab->base[i];
+    if (i < n_u) {
+      l_row[i] = row;
+      l_mask[i] = mask;
+      l_base[i] = base;
+      if (i == n_u - 1) l_base[n_u] = base + __popc(mask);
+    }
   }
-  constexpr int kSlice = 512 * CPW;  // bytes of a staged row
-  unsigned char* hs = smem + (size_t)wv * (max_rows + 1) * kSlice;
-  for (int i = lane; i < kSlice / 16; i += 64)
-    *reinterpret_cast<uint4*>(hs + (size_t)max_rows * kSlice + 16 * i) = make_uint4(0, 0, 0, 0);
+  const int row_bytes = 512 * CPW * ks;  // of a staged row
+  for (int i = tid; i < row_bytes / 16; i += threads)
+    *reinterpret_cast<uint4*>(hs + (size_t)max_rows * row_bytes + 16 * i) = make_uint4(0, 0, 0, 0);
   __syncthreads();
 
   const int o0 = blockIdx.x * 16;
   const size_t wrb = I / 2, srb = I / 32;
   const uint32_t srow_off = (uint32_t)ln.srow * (uint32_t)srb;
-  Slot<CPW, TAIL> ring[R];
-  // past the last expert: the first rows of a device bank (see few_gate_up)
-  auto issue = [&](Slot<CPW, TAIL>& o, int v) {
-    const int u = v * nsub + sub;
+  Slot<CPW, false> next;
+  // the expert u's; past the last expert the first rows of a device bank (see
+  // few_gate_up)
+  auto issue = [&](Slot<CPW, false>& o, int u) {
     const bool live = u < n_u;
     const int code = __builtin_amdgcn_readfirstlane(l_row[live ? u : 0]);
     const bool hot = live ? code >= 0 : (a.hot.n_rows > 0 && !a.hot.host) || a.cold.n_rows == 0;
@@ -552,34 +587,30 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
 #pragma unroll
     for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  if (n_u > 0) {
-#pragma unroll
-    for (int u = 0; u < R; ++u) issue(ring[u], u);
-  }
-  const int steps = sub < n_u ? (n_u - sub + nsub - 1) / nsub : 0;
   int ph0 = 0, ph_end = 0;  // first staged h row; first expert past the phase
-  // h rows of the experts from u on, as many whole experts as fit
-  auto stage = [&](int u) {
-    ph0 = __builtin_amdgcn_readfirstlane(l_base[u]);
-    ph_end = u;
+  // The next phase: every wavefront calls it once per phase, in order.
+  auto next_phase = [&]() {
+    lds_barrier();  // the last phase's rows have been read
+    const int u0 = ph_end;
+    ph0 = __builtin_amdgcn_readfirstlane(l_base[u0]);
     while (ph_end < n_u && __builtin_amdgcn_readfirstlane(l_base[ph_end + 1]) - ph0 <= max_rows)
       ++ph_end;
     const int nr = __builtin_amdgcn_readfirstlane(l_base[ph_end]) - ph0;
-    constexpr int kG = kSlice / 16;  // granules per row: 32, 64 or 128
-    constexpr int kB = 8;            // granules per lane per batch
-    for (int i0 = 0; i0 < nr * kG; i0 += 64 * kB) {
+    const uint32_t per = 32 * CPW * ks, n = nr * per;  // granules
+    constexpr int kB = 8;                              // per thread per batch
+    for (uint32_t i0 = 0; i0 < n; i0 += kB * threads) {
       u32x4 v[kB];
       uint32_t off[kB];
       int dst[kB];
       uint32_t past = 0;  // bit b: granule b lies past the end of the axis
 #pragma unroll
       for (int b = 0; b < kB; ++b) {
-        const int i = min(i0 + b * 64 + lane, nr * kG - 1);
-        const int s = i / kG, g = i % kG;
-        const int e = slice * CPW * kChunkElems + g * 8;
-        past |= (e < I ? 0u : 1u) << b;
-        off[b] = ((uint32_t)(ph0 + s) * (uint32_t)I + (uint32_t)(e < I ? e : 0)) * 2u;
-        dst[b] = s * kSlice + 16 * (g ^ (s & 7));
+        const uint32_t i = min(i0 + b * threads + tid, n - 1);
+        const uint32_t s = i / per, g = i - s * per;
+        const bool in = g * 8 < (uint32_t)I;
+        past |= (in ? 0u : 1u) << b;
+        off[b] = ((ph0 + s) * (uint32_t)I + (in ? g * 8 : 0u)) * 2u;
+        dst[b] = (int)(s * row_bytes + 16 * (g ^ (s & 7)));
       }
       // Loads and their wait in one block: as ordinary loads under this branch
       // they made the compiler wait for every weight in flight at each expert.
@@ -598,64 +629,60 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
       for (int b = 0; b < kB; ++b)
         *reinterpret_cast<u32x4*>(hs + dst[b]) = (past >> b) & 1u ? u32x4{0, 0, 0, 0} : v[b];
     }
+    lds_barrier();
   };
 
-  for (int s0 = 0; s0 < steps; s0 += R) {  // whole turns of the ring, as above
+  if (sub < n_u) issue(next, sub);
+  for (int u = sub; u < n_u; u += nsub) {
+    while (u >= ph_end) next_phase();
+    const int mask = l_mask[u], base = l_base[u] - ph0;
+    f32x4 d[2][SETS];
+    const unsigned char* hp[SETS];  // this column's staged row
+    int sw[SETS];
+    bool has[SETS];
 #pragma unroll
-    for (int v = 0; v < R; ++v) {
-      const int step = s0 + v;
-      const bool live = step < steps;
-      const int u = live ? step * nsub + sub : 0;
-      if (live && u >= ph_end) stage(u);
-      const int mask = live ? l_mask[u] : 0, base = l_base[u] - ph0;
-      f32x4 d[2][SETS];
-      const unsigned char* hp[SETS];  // this column's staged row
-      int sw[SETS];
-      bool has[SETS];
+    for (int st = 0; st < SETS; ++st) {
+      const int t = st * 8 + (ln.r & 7);
+      has[st] = (mask >> t) & 1;
+      const int s = has[st] ? base + __popc(mask & ((1 << t) - 1)) : max_rows;
+      hp[st] = hs + s * row_bytes + 512 * CPW * slice;
+      sw[st] = 16 * ((ln.r >= 8 ? 16 : 0) + ((4 * ln.q) ^ (has[st] ? s & 7 : 0)));
 #pragma unroll
-      for (int st = 0; st < SETS; ++st) {
-        const int t = st * 8 + (ln.r & 7);
-        has[st] = (mask >> t) & 1;
-        const int s = has[st] ? base + __popc(mask & ((1 << t) - 1)) : max_rows;
-        hp[st] = hs + (size_t)s * kSlice;
-        sw[st] = has[st] ? s & 7 : 0;
+      for (int g = 0; g < 2; ++g) d[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    float sc[2][CPW];
+    ln.scales(next, 0, sc[0]);
+    ln.scales(next, 1, sc[1]);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) d[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
+    for (int j = 0; j < CPW; ++j) {
 #pragma unroll
-      for (int j = 0; j < CPW; ++j) {
-        const float sc[2] = {ln.scale(ring[v], 0, j), ln.scale(ring[v], 1, j)};
+      for (int m = 0; m < 4; ++m) {
+        bf16x8 bv[SETS];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          bf16x8 bv[SETS];
+        for (int st = 0; st < SETS; ++st)  // granule 32j + half + (4q + m ^ s & 7)
+          bv[st] = *reinterpret_cast<const bf16x8*>(hp[st] + 512 * j + (sw[st] ^ (16 * m)));
 #pragma unroll
-          for (int st = 0; st < SETS; ++st) {
-            const int g = 32 * j + (ln.r >= 8 ? 16 : 0) + 4 * ln.q + m;
-            bv[st] = *reinterpret_cast<const bf16x8*>(hp[st] + 16 * (g ^ sw[st]));
-          }
+        for (int g = 0; g < 2; ++g) {
+          const bf16x8 av = dequant8(word4(next.w[g][j], m), sc[g][j]);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const bf16x8 av = dequant8(word4(ring[v].w[g][j], m), sc[g]);
-#pragma unroll
-            for (int st = 0; st < SETS; ++st)
-              d[g][st] =
-                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv[st], d[g][st], 0, 0, 0);
-          }
+          for (int st = 0; st < SETS; ++st)
+            d[g][st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, bv[st], d[g][st], 0, 0, 0);
         }
       }
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int st = 0; st < SETS; ++st)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[g][st][e] += has[st] ? d[g][st][e] : 0.0f;
-      issue(ring[v], step + R);
     }
+    issue(next, u + nsub);
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int st = 0; st < SETS; ++st)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[g][st][e] += has[st] ? d[g][st][e] : 0.0f;
   }
+  while (ph_end < n_u) next_phase();
 
   // sum of the wavefronts' partial sums, in their order, and the one rounding
   __syncthreads();
-  float* red = reinterpret_cast<float*>(smem);  // [wave][half][set][token][16]
+  float* red = reinterpret_cast<float*>(hs);  // [wave][half][set][token][16]
   if ((ln.r >= 8) == (ln.q >= 2)) {
 #pragma unroll
     for (int g = 0; g < 2; ++g)
@@ -665,8 +692,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
                                   8 * g + 4 * (ln.q & 1)) = acc[g][st];
   }
   __syncthreads();
-  const int waves = blockDim.x >> 6;
-  for (int i = tid; i < T * 16; i += blockDim.x) {
+  const int waves = threads >> 6;
+  for (int i = tid; i < T * 16; i += threads) {
     const int t = i / 16, o = i % 16;
     float s = 0.0f;
     for (int p = 0; p < 2 * waves; ++p) s += red[((p * SETS + t / 8) * 8 + (t & 7)) * 16 + o];
@@ -674,36 +701,36 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
   }
 }
 
-template <int CPW, int SETS, int R, bool TAIL>
+template <int CPW, int SETS, int R, bool WIDE>
 hipError_t go_gate_up(const FewArgs& a, hipStream_t stream) {
-  const Cut c = cut_of(a.H);
+  const Cut c = gate_up_cut(a.H);
   const size_t lds = (size_t)2 * c.sub * 2 * SETS * 2 * c.ks * 64 * sizeof(float);
-  hipLaunchKernelGGL((few_gate_up<CPW, SETS, R, TAIL>), dim3(device_cus()), dim3(kThreads), lds,
+  hipLaunchKernelGGL((few_gate_up<CPW, SETS, R, WIDE>), dim3(device_cus()), dim3(kThreads), lds,
                      stream, a);
   return hipGetLastError();
 }
 
-template <int CPW, int SETS, int R, bool TAIL>
+template <int CPW, int SETS>
 hipError_t go_down(const FewArgs& a, hipStream_t stream) {
-  const Cut c = cut_of(a.I);
+  const Cut c = down_cut(a.I);
   const int waves = c.ks * c.sub;
-  const size_t per_row = (size_t)waves * 512 * CPW;
-  const int max_rows = (int)std::min<size_t>(kDownLds / per_row - 1, (size_t)a.T * a.k);
-  const size_t lds = std::max((size_t)(max_rows + 1) * per_row,
-                              (size_t)waves * 2 * SETS * 8 * 16 * sizeof(float));
-  hipLaunchKernelGGL((few_down<CPW, SETS, R, TAIL>), dim3(a.H / 16), dim3(64 * waves), lds,
-                     stream, a, max_rows);
+  const size_t row = (size_t)512 * CPW * c.ks;
+  const int max_rows = (int)std::min<size_t>(kDownLds / row - 1, (size_t)a.T * a.k);
+  const size_t lds =
+      std::max((size_t)(max_rows + 1) * row, (size_t)waves * 2 * SETS * 8 * 16 * sizeof(float));
+  hipLaunchKernelGGL((few_down<CPW, SETS>), dim3(a.H / 16), dim3(64 * waves), lds, stream, a,
+                     max_rows);
   return hipGetLastError();
 }
 
-// R: ring slots of 32 CPW + ... registers each; see the launch rule below.
-template <int CPW, int R, bool TAIL>
+// Ring slots: at least 96 KB of weights in flight per CU.
+template <int CPW, int R, bool WIDE>
 hipError_t gate_up_sets(const FewArgs& a, hipStream_t s) {
-  return a.T <= 8 ? go_gate_up<CPW, 1, R, TAIL>(a, s) : go_gate_up<CPW, 2, R, TAIL>(a, s);
+  return a.T <= 8 ? go_gate_up<CPW, 1, R, WIDE>(a, s) : go_gate_up<CPW, 2, R, WIDE>(a, s);
 }
-template <int CPW, int R, bool TAIL>
+template <int CPW>
 hipError_t down_sets(const FewArgs& a, hipStream_t s) {
-  return a.T <= 8 ? go_down<CPW, 1, R, TAIL>(a, s) : go_down<CPW, 2, R, TAIL>(a, s);
+  return a.T <= 8 ? go_down<CPW, 1>(a, s) : go_down<CPW, 2>(a, s);
 }
 
 }  // namespace
@@ -717,19 +744,22 @@ size_t layer_few_workspace_bytes(int T, int k, int I) {
 }
 
 hipError_t launch_layer_few(const FewArgs& a, hipStream_t s) {
-  const Cut cg = cut_of(a.H), cd = cut_of(a.I);
-  const bool tg = a.H % (kChunkElems * cg.cpw * cg.ks) != 0;
-  const bool td = a.I % (kChunkElems * cd.cpw * cd.ks) != 0;
+  const Cut cg = gate_up_cut(a.H), cd = down_cut(a.I);
+  const bool wide = a.H % (kChunkElems * cg.cpw * cg.ks) == 0;  // no slice ends past the axis
   hipError_t e;
   if (cg.cpw == 1)
-    e = tg ? gate_up_sets<1, 4, true>(a, s) : gate_up_sets<1, 4, false>(a, s);
+    e = gate_up_sets<1, 4, false>(a, s);
   else if (cg.cpw == 2)
-    e = tg ? gate_up_sets<2, 3, true>(a, s) : gate_up_sets<2, 3, false>(a, s);
+    e = wide ? gate_up_sets<2, 3, true>(a, s) : gate_up_sets<2, 3, false>(a, s);
   else
-    e = tg ? gate_up_sets<4, 2, true>(a, s) : gate_up_sets<4, 2, false>(a, s);
+    e = wide ? gate_up_sets<4, 2, true>(a, s) : gate_up_sets<4, 2, false>(a, s);
   if (e != hipSuccess) return e;
-  if (cd.cpw == 1) return td ? down_sets<1, 4, true>(a, s) : down_sets<1, 4, false>(a, s);
-  return td ? down_sets<2, 3, true>(a, s) : down_sets<2, 3, false>(a, s);
+  switch (cd.cpw) {
+    case 1: return down_sets<1>(a, s);
+    case 2: return down_sets<2>(a, s);
+    case 3: return down_sets<3>(a, s);
+    default: return down_sets<4>(a, s);
+  }
 }
 
 }  // namespace moe
