@@ -24,7 +24,9 @@ ENTRY_POINTS = ("moe_expert_bytes", "moe_ffn_workspace_bytes", "moe_route_split"
                 "moe_expert_ffn_mxfp4", "moe_expert_gate_up_mxfp4", "moe_expert_down_mxfp4",
                 "moe_stage_rows", "moe_finalize", "moe_usage_counts", "moe_swap_rows",
                 "moe_last_error", "moe_expert_ffn_mxfp4_noalloc", "moe_stage_rows_dma",
-                "moe_topk_gate", "moe_layer_few_workspace_bytes", "moe_layer_few_mxfp4")
+                "moe_topk_gate", "moe_layer_few_workspace_bytes", "moe_layer_few_mxfp4",
+                "moe_quantize_rows_i8", "moe_linear_i8", "moe_ffn_i8_workspace_bytes",
+                "moe_expert_ffn_i8")
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_H, MOE_FEW_MAX_I = 16, 8192, 4096
 # moe_topk_gate weights: softmax over the picks, or over all unmasked experts
@@ -105,6 +107,14 @@ def lib():
         L.moe_layer_few_mxfp4.restype = i32
         L.moe_layer_few_mxfp4.argtypes = [bankp, bankp, vp, i32, vp, vp, vp, i32, i32, i32, i32,
                                           vp, i32, vp, vp, vp, vp]
+        L.moe_quantize_rows_i8.restype = i32
+        L.moe_quantize_rows_i8.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp]
+        L.moe_linear_i8.restype = i32
+        L.moe_linear_i8.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, vp, i32, i64, vp]
+        L.moe_ffn_i8_workspace_bytes.restype = sz
+        L.moe_ffn_i8_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.moe_expert_ffn_i8.restype = i32
+        L.moe_expert_ffn_i8.argtypes = [bankp, MoeSplitC, vp, vp, i32, i32, i32, i32, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -205,6 +215,33 @@ def moe_ffn_workspace_bytes(T: int, k: int, H: int, I: int) -> int:
 BANK_DEVICE, BANK_HOST, BANK_HOST_WEIGHTS = 0, 1, 2
 
 
+def _bank_abi(bank, dtypes) -> MoeBankC:
+    """The C form of a Bank or BankI8 whose weights and scales have the two
+    dtypes (str names); built once per set of tensors (the call path stays
+    cheap on the host)."""
+    key = (bank.w13.data_ptr(), bank.s13.data_ptr(), bank.w2.data_ptr(), bank.s2.data_ptr(),
+           bank.n_rows, bank.on_host)
+    c = bank.__dict__.get("_abi")
+    if c is None or c[0] != key:
+        where = int(bank.on_host)
+        if where not in (BANK_DEVICE, BANK_HOST, BANK_HOST_WEIGHTS):
+            raise MoeError(MOE_EINVAL, f"bank on_host={bank.on_host!r}: expected "
+                           "BANK_DEVICE, BANK_HOST or BANK_HOST_WEIGHTS")
+        for name, t in bank.tensors().items():
+            want = dtypes[0 if name[0] == "w" else 1]
+            if str(t.dtype) != want or not t.is_contiguous():
+                raise _bad(f"bank {name}", f"a contiguous {want[6:]} tensor", t)
+            host = where == BANK_HOST or (where == BANK_HOST_WEIGHTS and name[0] == "w")
+            if host and (t.device.type != "cpu" or not t.is_pinned()):
+                raise _bad(f"bank {name}", f"pinned host memory (on_host={where})", t)
+            if not host and t.device.type != "cuda":
+                raise _bad(f"bank {name}", f"GPU memory (on_host={where})", t)
+        c = (key, MoeBankC(bank.w13.data_ptr(), bank.s13.data_ptr(), bank.w2.data_ptr(),
+                           bank.s2.data_ptr(), bank.n_rows, where))
+        bank.__dict__["_abi"] = c
+    return c[1]
+
+
 @dataclass
 class Bank:
     """One residency bank: uint8 tensors w13 [R,2I,H/2], s13 [R,2I,H/32],
@@ -223,27 +260,7 @@ class Bank:
         return int(self.w13.shape[0])
 
     def abi(self) -> MoeBankC:
-        # built once per set of tensors (the call path stays cheap on the host)
-        key = (self.w13.data_ptr(), self.s13.data_ptr(), self.w2.data_ptr(),
-               self.s2.data_ptr(), self.n_rows, self.on_host)
-        c = self.__dict__.get("_abi")
-        if c is None or c[0] != key:
-            where = int(self.on_host)
-            if where not in (BANK_DEVICE, BANK_HOST, BANK_HOST_WEIGHTS):
-                raise MoeError(MOE_EINVAL, f"bank on_host={self.on_host!r}: expected "
-                               "BANK_DEVICE, BANK_HOST or BANK_HOST_WEIGHTS")
-            for name, t in self.tensors().items():
-                if str(t.dtype) != "torch.uint8" or not t.is_contiguous():
-                    raise _bad(f"bank {name}", "a contiguous uint8 tensor", t)
-                host = where == BANK_HOST or (where == BANK_HOST_WEIGHTS and name[0] == "w")
-                if host and (t.device.type != "cpu" or not t.is_pinned()):
-                    raise _bad(f"bank {name}", f"pinned host memory (on_host={where})", t)
-                if not host and t.device.type != "cuda":
-                    raise _bad(f"bank {name}", f"GPU memory (on_host={where})", t)
-            c = (key, MoeBankC(self.w13.data_ptr(), self.s13.data_ptr(), self.w2.data_ptr(),
-                               self.s2.data_ptr(), self.n_rows, where))
-            self.__dict__["_abi"] = c
-        return c[1]
+        return _bank_abi(self, ("torch.uint8", "torch.uint8"))
 
     def tensors(self) -> dict:
         return {"w13": self.w13, "s13": self.s13, "w2": self.w2, "s2": self.s2}
@@ -529,3 +546,90 @@ def moe_layer_few_mxfp4(hot: Bank, cold: Bank, row_map, x, topk_ids, topk_w, I: 
         _gpu(topk_w, "topk_w", ("torch.float32",)), T, k, H, I,
         _gpu_opt(counts_layer, "counts", i32), count_tmax, _gpu(n_invalid, "n_invalid", i32),
         _gpu(workspace, "workspace"), _gpu(out, "out", _BF16_BITS), _stream(stream)))
+
+
+@dataclass
+class BankI8:
+    """A bank of 8-bit integer experts: int8 tensors w13 [R,2I,H], w2 [R,H,I]
+    and their float32 scales per output channel s13 [R,2I], s2 [R,H]; on_host
+    as in Bank."""
+    w13: object
+    s13: object
+    w2: object
+    s2: object
+    on_host: int = BANK_DEVICE
+
+    @property
+    def n_rows(self) -> int:
+        return int(self.w13.shape[0])
+
+    def abi(self) -> MoeBankC:
+        return _bank_abi(self, ("torch.int8", "torch.float32"))
+
+    def tensors(self) -> dict:
+        return {"w13": self.w13, "s13": self.s13, "w2": self.w2, "s2": self.s2}
+
+
+def moe_quantize_rows_i8(x, q, scale, stream=None) -> None:
+    """x [rows,K] (bfloat16, float16 or float32; rows may be strided) -> q int8
+    [rows,K], scale fp32 [rows]."""
+    p, dtype, rows, K, ld = _rows2d(x, "x")
+    _same_device(("x", x), ("q", q), ("scale", scale))
+    if tuple(q.shape) != (rows, K):
+        raise MoeError(MOE_EINVAL, f"q {tuple(q.shape)}: need {(rows, K)}")
+    _need(scale, "scale", 4 * rows)
+    _check(lib().moe_quantize_rows_i8(p, dtype, ld, rows, K, _gpu(q, "q", ("torch.int8",)),
+                                      _gpu(scale, "scale", ("torch.float32",)), _stream(stream)))
+
+
+def moe_linear_i8(xq, xs, w, ws, y, stream=None) -> None:
+    """xq int8 [M,K] (rows may be strided) with scales xs fp32 [M], times w int8
+    [N,K] with scales ws fp32 [N] -> y [M,N] (bfloat16, float16 or float32; rows
+    may be strided)."""
+    if str(getattr(xq, "dtype", "")) != "torch.int8" or xq.device.type != "cuda" or \
+            xq.dim() != 2 or (xq.shape[1] > 1 and xq.stride(1) != 1) or \
+            (xq.shape[0] > 1 and xq.stride(0) < xq.shape[1]):
+        raise _bad("xq", "a 2-D int8 GPU tensor of contiguous rows", xq)
+    M, K = int(xq.shape[0]), int(xq.shape[1])
+    yp, dtype, my, N, ldy = _rows2d(y, "y")
+    _same_device(("xq", xq), ("xs", xs), ("w", w), ("ws", ws), ("y", y))
+    if my != M or tuple(w.shape) != (N, K):
+        raise MoeError(MOE_EINVAL, f"xq {(M, K)}, w {tuple(w.shape)}, y {(my, N)}: need [M,K], "
+                                   "[N,K], [M,N]")
+    _need(xs, "xs", 4 * M)
+    _need(ws, "ws", 4 * N)
+    _check(lib().moe_linear_i8(xq.data_ptr(), int(xq.stride(0)) if M > 1 else K,
+                               _gpu(xs, "xs", ("torch.float32",)), M, _gpu(w, "w", ("torch.int8",)),
+                               _gpu(ws, "ws", ("torch.float32",)), N, K, yp, dtype, ldy,
+                               _stream(stream)))
+
+
+def moe_ffn_i8_workspace_bytes(T: int, k: int, H: int, I: int) -> int:
+    return int(lib().moe_ffn_i8_workspace_bytes(T, k, H, I))
+
+
+def moe_expert_ffn_i8(bank: BankI8, split: Split, xq, xs, k: int, I: int, workspace, Y,
+                      stream=None) -> None:
+    """The expert FFN over one bank's picks with 8-bit integer experts; xq int8
+    [T,H] and xs fp32 [T] from moe_quantize_rows_i8."""
+    T, H = int(xq.shape[0]), int(xq.shape[1])
+    _same_device(("xq", xq), ("xs", xs), ("bank", bank.w13), ("workspace", workspace), ("Y", Y))
+    if T > 0 and bank.n_rows > 0:
+        R = bank.n_rows
+        for name, n in (("w13", R * 2 * I * H), ("s13", R * 2 * I), ("w2", R * H * I),
+                        ("s2", R * H)):
+            got = int(getattr(bank, name).numel())
+            if got != n:
+                raise MoeError(MOE_EINVAL, f"bank {name}: {got} elements, {R} rows at H={H}, "
+                                           f"I={I} need {n}")
+        if int(split.slots.numel()) < T * k:
+            raise MoeError(MOE_EINVAL, f"split slots: {int(split.slots.numel())} entries, "
+                                       f"need T*k = {T * k}")
+        _need(xs, "xs", 4 * T)
+        _need(workspace, "workspace", moe_ffn_i8_workspace_bytes(T, k, H, I))
+        _need(Y, "Y", 2 * T * k * H)
+    b = bank.abi()
+    _check(lib().moe_expert_ffn_i8(ctypes.byref(b), split.abi(), _gpu(xq, "xq", ("torch.int8",)),
+                                   _gpu(xs, "xs", ("torch.float32",)), T, k, H, I,
+                                   _gpu(workspace, "workspace"), _gpu(Y, "Y", _BF16_BITS),
+                                   _stream(stream)))

@@ -37,6 +37,11 @@ using moe::set_error;
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
 }  // namespace
 
 extern "C" {
@@ -94,9 +99,8 @@ int moe_layer_few_mxfp4(const moe_bank* hot, const moe_bank* cold, const int32_t
                                  "not be NULL");
   if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(out, 16))
     return set_error(MOE_EINVAL, "x, workspace and out must be 16-byte aligned");
-  const uintptr_t xb = reinterpret_cast<uintptr_t>(x), ob = reinterpret_cast<uintptr_t>(out);
   const size_t nb = (size_t)T * H * 2;
-  if (xb < ob + nb && ob < xb + nb) return set_error(MOE_EINVAL, "out must not overlap x");
+  if (overlap(x, nb, out, nb)) return set_error(MOE_EINVAL, "out must not overlap x");
   moe::FewArgs a = {};
   const size_t align[4] = {16, 16, 16, 16};
   const moe_bank* const src[2] = {hot, cold};
@@ -123,6 +127,141 @@ int moe_layer_few_mxfp4(const moe_bank* hot, const moe_bank* cold, const int32_t
   a.out = out;
   const hipError_t e = moe::launch_layer_few(a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return set_error(MOE_EHIP, "few-token layer: %s", hipGetErrorString(e));
+  return moe::succeed();
+}
+
+int moe_quantize_rows_i8(const void* x, int dtype, int64_t ld, int rows, int K, int8_t* q,
+                         float* scale, void* stream) {
+  if (!moe::dtype_known(dtype)) return set_error(MOE_EINVAL, "dtype=%d unknown", dtype);
+  if (rows < 0) return set_error(MOE_EINVAL, "rows=%d must be >= 0", rows);
+  if (K < 1 || K > MOE_I8_MAX_K)
+    return set_error(MOE_EINVAL, "K=%d outside [1, %d]", K, MOE_I8_MAX_K);
+  if (ld < K || ld > (int64_t)1 << 31)
+    return set_error(MOE_EINVAL, "ld=%lld must be in [K=%d, 2^31]", (long long)ld, K);
+  if (rows == 0) return moe::succeed();
+  if (!x || !q || !scale) return set_error(MOE_EINVAL, "x, q and scale must not be NULL");
+  if (!aligned(x, moe::dtype_bytes(dtype)) || !aligned(scale, 4))
+    return set_error(MOE_EINVAL, "x and scale must be aligned to their elements");
+  if (overlap(x, ((size_t)(rows - 1) * ld + K) * moe::dtype_bytes(dtype), q, (size_t)rows * K))
+    return set_error(MOE_EINVAL, "q must not overlap x");
+  const hipError_t e = moe::launch_quantize_rows(x, dtype, ld, rows, K, nullptr, q, scale,
+                                                 static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return set_error(MOE_EHIP, "quantize launch: %s", hipGetErrorString(e));
+  return moe::succeed();
+}
+
+int moe_linear_i8(const int8_t* xq, int64_t ldx, const float* xs, int M, const int8_t* w,
+                  const float* ws, int N, int K, void* y, int dtype, int64_t ldy, void* stream) {
+  if (!moe::dtype_known(dtype)) return set_error(MOE_EINVAL, "dtype=%d unknown", dtype);
+  if (M < 0 || N < 0) return set_error(MOE_EINVAL, "M=%d and N=%d must be >= 0", M, N);
+  if (K < 16 || K % 16 || K > MOE_I8_MAX_K)
+    return set_error(MOE_EINVAL, "K=%d must be a multiple of 16 in [16, %d]", K, MOE_I8_MAX_K);
+  if (ldx < K || ldx % 16 || ldx > (int64_t)1 << 31)
+    return set_error(MOE_EINVAL, "ldx=%lld must be a multiple of 16 in [K=%d, 2^31]",
+                     (long long)ldx, K);
+  if (ldy < N || ldy > (int64_t)1 << 31)
+    return set_error(MOE_EINVAL, "ldy=%lld must be in [N=%d, 2^31]", (long long)ldy, N);
+  if (M == 0 || N == 0) return moe::succeed();
+  if (!xq || !xs || !w || !ws || !y)
+    return set_error(MOE_EINVAL, "xq, xs, w, ws and y must not be NULL");
+  const size_t es = moe::dtype_bytes(dtype);
+  if (!aligned(xq, 16) || !aligned(w, 16) || !aligned(xs, 4) || !aligned(ws, 4) || !aligned(y, es))
+    return set_error(MOE_EINVAL, "xq and w must be 16-byte aligned, xs, ws and y to their elements");
+  const size_t yb = ((size_t)(M - 1) * ldy + N) * es;
+  if (overlap(y, yb, xq, (size_t)(M - 1) * ldx + K) || overlap(y, yb, w, (size_t)N * K) ||
+      overlap(y, yb, xs, (size_t)M * 4) || overlap(y, yb, ws, (size_t)N * 4))
+    return set_error(MOE_EINVAL, "y must not overlap the inputs");
+  moe::I8Args a = {};
+  a.a = xq;
+  a.lda = ldx;
+  a.sa = xs;
+  a.w = w;
+  a.sw = ws;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.y = y;
+  a.dtype = dtype;
+  a.ldy = ldy;
+  const hipError_t e = moe::launch_gemm_i8(a, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return set_error(MOE_EHIP, "8-bit product: %s", hipGetErrorString(e));
+  return moe::succeed();
+}
+
+size_t moe_ffn_i8_workspace_bytes(int T, int k, int H, int I) {
+  if (T <= 0 || k <= 0 || H <= 0 || I <= 0) return 0;
+  return (size_t)T * k * ((size_t)I * 5 + 4);  // h fp32, h in 8 bits, its scale
+}
+
+int moe_expert_ffn_i8(const moe_bank* bank, moe_split split, const int8_t* xq, const float* xs,
+                      int T, int k, int H, int I, void* workspace, uint16_t* Y, void* stream) {
+  if (T < 0) return set_error(MOE_EINVAL, "T=%d must be >= 0", T);
+  if (k < 1 || k > MOE_MAX_TOPK)
+    return set_error(MOE_EINVAL, "k=%d outside [1, %d]", k, MOE_MAX_TOPK);
+  if ((int64_t)T * k > (int64_t)1 << 24) return set_error(MOE_EINVAL, "T*k above 2^24");
+  if (H <= 0 || H % 64 || I <= 0 || I % 64)
+    return set_error(MOE_EINVAL, "H=%d, I=%d must be positive multiples of 64", H, I);
+  if (H > 32768 || I > 32768)
+    return set_error(MOE_ENOTSUP, "H=%d, I=%d: at most 32768 supported", H, I);
+  if (!bank) return set_error(MOE_EINVAL, "bank is NULL");
+  if (bank->n_rows < 0 || bank->n_rows > MOE_MAX_ROWS)
+    return set_error(MOE_EINVAL, "bank rows %d outside [0, %d]", bank->n_rows, MOE_MAX_ROWS);
+  if (T == 0 || bank->n_rows == 0) return moe::succeed();
+  if (!split.n_active || !split.active_rows || !split.row_off || !split.slots)
+    return set_error(MOE_EINVAL, "split has a NULL buffer");
+  if (!xq || !xs || !workspace || !Y)
+    return set_error(MOE_EINVAL, "xq, xs, workspace and Y must not be NULL");
+  if (!aligned(xq, 16) || !aligned(workspace, 16) || !aligned(Y, 16) || !aligned(xs, 4))
+    return set_error(MOE_EINVAL, "xq, workspace and Y must be 16-byte aligned, xs 4-byte");
+  const size_t align[4] = {16, 16, 16, 16};
+  const uint8_t* p[4];
+  int rc = moe::bank_ptrs(bank, align, p);
+  if (rc != MOE_OK) return rc;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t slots = (size_t)T * k;
+  float* h = static_cast<float*>(workspace);
+  int8_t* hq = reinterpret_cast<int8_t*>(h + slots * I);
+  float* hs = reinterpret_cast<float*>(hq + slots * I);
+  moe::I8Args a = {};
+  a.a = xq;
+  a.lda = H;
+  a.sa = xs;
+  a.w = reinterpret_cast<const int8_t*>(p[0]);
+  a.sw = reinterpret_cast<const float*>(p[1]);
+  a.M = (int)slots;
+  a.N = I;
+  a.K = H;
+  a.n_active = split.n_active;
+  a.active_rows = split.active_rows;
+  a.row_off = split.row_off;
+  a.slots = split.slots;
+  a.n_rows = bank->n_rows;
+  a.k = k;
+  a.by_token = 1;
+  a.gate_up = 1;
+  a.host = bank->on_host != MOE_BANK_DEVICE;
+  a.y = h;
+  a.dtype = MOE_DTYPE_F32;
+  a.ldy = I;
+  hipError_t e = moe::launch_gemm_i8(a, s);
+  if (e == hipSuccess)
+    e = moe::launch_quantize_rows(h, MOE_DTYPE_F32, I, (int)slots, I, &split, hq, hs, s);
+  if (e == hipSuccess) {
+    a.a = hq;
+    a.lda = I;
+    a.sa = hs;
+    a.w = reinterpret_cast<const int8_t*>(p[2]);
+    a.sw = reinterpret_cast<const float*>(p[3]);
+    a.N = H;
+    a.K = I;
+    a.by_token = 0;
+    a.gate_up = 0;
+    a.y = Y;
+    a.dtype = MOE_DTYPE_BF16;
+    a.ldy = H;
+    e = moe::launch_gemm_i8(a, s);
+  }
+  if (e != hipSuccess) return set_error(MOE_EHIP, "8-bit expert FFN: %s", hipGetErrorString(e));
   return moe::succeed();
 }
 

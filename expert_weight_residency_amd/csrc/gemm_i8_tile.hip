@@ -1,0 +1,245 @@
+// Products of 8-bit rows with a scale per activation row and per weight row, in
+// tiles: steps with many activation rows per weight matrix.
+//
+//   y[r][n] = sa[r] * sw[n] * sum_k a[r][k] w[n][k]
+//
+// v_mfma_i32_16x16x64_i8 with the weights as A operand (result rows) and the
+// activations as B operand (result columns), so that a lane ends with 4
+// consecutive outputs of one activation row. The integer sums are exact, so no
+// tile shape, split or order changes a bit of the result; the epilogue scales
+// in fp32 and rounds once.
+//
+// Both operands are K-contiguous rows. A step takes 128 bytes of each row of the
+// tile: global-to-LDS copies of 16 bytes per lane, a wavefront's copy covering 8
+// rows x one whole line, into one of S static buffers (distinct objects, named
+// at compile time, so that the compiler need not wait for the copies into one
+// before reading another), S - 1 steps ahead, with one barrier per step.
+// Granule g of row r lies at g ^ (r & 7) (applied to the source address, as the
+// copy writes LDS in lane order), which spreads an operand read over all banks.
+// Granules past the end of K are copied from 16 zero bytes instead.
+#include "gemm_i8.h"
+#include "mxfp4_common.h"
+#include "tile_items.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __align__(16) const uint8_t kZeros[16] = {};
+
+// s_waitcnt immediate: at most n vector-memory operations and no LDS operation
+// outstanding.
+constexpr int vm_lds(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
+
+#define tile_barrier(W)                                    \
+  do {                                                     \
+    __builtin_amdgcn_sched_barrier(0);                     \
+    __builtin_amdgcn_s_waitcnt(W);                         \
+    __builtin_amdgcn_s_barrier();                          \
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup"); \
+    __builtin_amdgcn_sched_barrier(0);                     \
+  } while (0)
+
+
+// TN x TM tile (weight rows x activation rows), WN x WM wavefronts.
+template <int TN, int TM, int WN, int WM, int S, bool GU>
+__global__ __launch_bounds__(64 * WN * WM, WN * WM > 4 ? 2 : 1) void gemm_i8_tile(I8Args a,
+                                                                               int tiles_n) {
+  constexpr int kW = WN * WM, kRows = TN + TM, kCopies = kRows / 8 / kW;
+  static_assert(kRows % (8 * kW) == 0 && TN % (8 * kW) == 0, "whole copies per wavefront");
+  constexpr int NF = TN / WN / 16, MF = TM / WM / 16;  // MFMA tiles per wavefront
+  static_assert(!GU || NF % 2 == 0, "gate and up tiles in pairs");
+  __shared__ __align__(128) uint8_t buf0[kRows * 128];
+  __shared__ __align__(128) uint8_t buf1[kRows * 128];
+  __shared__ __align__(128) uint8_t buf2[S > 2 ? kRows * 128 : 16];
+  __shared__ __align__(128) uint8_t buf3[S > 3 ? kRows * 128 : 16];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int N = a.N, K = a.K;
+
+  // which tile: [m0, m1) of the group's slots, weight rows from n0
+  int m0, m1, n0;
+  const int8_t* w = a.w;
+  const float* sw = a.sw;
+  const int wrows = GU ? 2 * N : N;
+  if (a.slots) {
+    extern __shared__ int tpre[];  // [n_active + 1]
+    __shared__ int wsum[kW];
+    const int na = *a.n_active;
+    tiles::build_tile_prefix<TM, kW>(a.row_off, na, tpre, wsum);
+    if ((int)blockIdx.x >= tpre[na] * tiles_n) return;  // the whole workgroup
+    // items of one expert: weight rows outermost, so that its tiles meet a
+    // block of weights together
+    const int e = tiles::row_of_tile(tpre, na, blockIdx.x / tiles_n);
+    const int local = blockIdx.x - tpre[e] * tiles_n, nt = tpre[e + 1] - tpre[e];
+    const int nb = local / nt, mt = local - nb * nt;
+    m0 = a.row_off[e] + mt * TM;
+    m1 = min(m0 + TM, a.row_off[e + 1]);
+    n0 = nb * (GU ? TN / 2 : TN);
+    const int64_t row = a.active_rows[e];
+    w += row * wrows * (int64_t)K;
+    sw += row * wrows;
+  } else {
+    const int mt = blockIdx.x / tiles_n, nb = blockIdx.x - mt * tiles_n;
+    m0 = mt * TM;
+    m1 = min(m0 + TM, a.M);
+    n0 = nb * TN;
+  }
+  // weight row of tile row r (clamped into the matrix; such outputs are not
+  // stored). Gate/up: 16 gate rows and the same 16 up rows in turn.
+  auto wrow = [&](int r) {
+    if constexpr (GU) return min(n0 + (r >> 5) * 16 + (r & 15), N - 1) + ((r >> 4) & 1) * N;
+    else return min(n0 + r, N - 1);
+  };
+  auto arow = [&](int m) -> int64_t {
+    if (!a.slots) return m;
+    const int s = a.slots[m];
+    return a.by_token ? s / a.k : s;
+  };
+
+  // copies: wavefront wv copies rows 8 (wv + kW i) .. + 7; lane l granule l % 8
+  // of row l / 8, from where the swizzle has it
+  const int gran = (lane & 7) ^ (lane >> 3);
+  const uint8_t* src[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int r = 8 * (wv + kW * i) + (lane >> 3);
+    const int8_t* p = r < TN ? w + (int64_t)wrow(r) * K
+                             : a.a + arow(min(m0 + (r - TN), m1 - 1)) * a.lda;
+    src[i] = reinterpret_cast<const uint8_t*>(p) + 16 * gran;
+  }
+  auto copy = [&](uint8_t* buf, int k0) {
+    const bool in = k0 + 16 * gran < K;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const uint8_t* p = in ? src[i] + k0 : kZeros;
+      // a select, not a branch around two copies
+      asm volatile("" : "+v"(p));
+      __builtin_amdgcn_global_load_lds(p, buf + 1024 * (wv + kW * i), 16, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  i32x4 acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  const int wn = wv % WN, wm = wv / WN, r = lane & 15, q = lane >> 4;
+  auto frag = [&](const uint8_t* buf, int row, int half) {
+    return *reinterpret_cast<const i32x4*>(buf + row * 128 + 16 * ((4 * half + q) ^ (row & 7)));
+  };
+  auto compute = [&](const uint8_t* buf) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      i32x4 bf[MF], af[NF];
+#pragma unroll
+      for (int j = 0; j < MF; ++j) bf[j] = frag(buf, TN + (wm * MF + j) * 16 + r, half);
+#pragma unroll
+      for (int i = 0; i < NF; ++i) af[i] = frag(buf, (wn * NF + i) * 16 + r, half);
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < MF; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
+    }
+  };
+
+  const int steps = (K + 127) / 128;
+  // past the end of K a copy brings zeros, which the products ignore
+  copy(buf0, 0);
+  if constexpr (S > 2) copy(buf1, 128);
+  if constexpr (S > 3) copy(buf2, 256);
+  for (int s = 0; s < steps; s += S) {
+    // each step: its copies (the oldest) have arrived for every wavefront, and
+    // the buffer the last step read is free for the copies S - 1 steps ahead
+    tile_barrier(vm_lds((S - 2) * kCopies));
+    copy(S == 2 ? buf1 : (S == 3 ? buf2 : buf3), (s + S - 1) * 128);
+    compute(buf0);
+    tile_barrier(vm_lds((S - 2) * kCopies));
+    copy(buf0, (s + S) * 128);
+    compute(buf1);
+    if constexpr (S > 2) {
+      tile_barrier(vm_lds((S - 2) * kCopies));
+      copy(buf1, (s + S + 1) * 128);
+      compute(buf2);
+    }
+    if constexpr (S > 3) {
+      tile_barrier(vm_lds((S - 2) * kCopies));
+      copy(buf2, (s + S + 2) * 128);
+      compute(buf3);
+    }
+  }
+
+  __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
+
+  // lane (r, q): outputs 16 i + 4 q + v of activation row 16 j + r
+#pragma unroll
+  for (int j = 0; j < MF; ++j) {
+    const int m = m0 + (wm * MF + j) * 16 + r;
+    if (m >= m1) continue;
+    const float sa = a.sa[arow(m)];
+    const int64_t orow = a.slots ? a.slots[m] : m;
+    if constexpr (GU) {
+#pragma unroll
+      for (int i = 0; i < NF; i += 2) {
+        const int n = n0 + (wn * NF + i) * 8 + 4 * q;
+        if (n >= N) continue;  // N is a multiple of 64
+        const float4 sg = *reinterpret_cast<const float4*>(sw + n);
+        const float4 su = *reinterpret_cast<const float4*>(sw + N + n);
+        float h[4];
+        const float g4[4] = {sg.x, sg.y, sg.z, sg.w}, u4[4] = {su.x, su.y, su.z, su.w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          h[v] = mx::silu_f32((float)acc[i][j][v] * sa * g4[v]) *
+                 ((float)acc[i + 1][j][v] * sa * u4[v]);
+        *reinterpret_cast<float4*>(static_cast<float*>(a.y) + orow * a.ldy + n) =
+            make_float4(h[0], h[1], h[2], h[3]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        const int n = n0 + (wn * NF + i) * 16 + 4 * q;
+        if (n >= N) continue;
+        float y[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          y[v] = (float)acc[i][j][v] * sa * sw[min(n + v, N - 1)];
+        store4(a, orow, n, y);
+      }
+    }
+  }
+}
+
+template <int TN, int TM, int WN, int WM, int S, bool GU>
+hipError_t go(const I8Args& a, hipStream_t stream) {
+  const int per = GU ? TN / 2 : TN;
+  const int64_t tiles_n = (a.N + per - 1) / per;
+  int64_t tiles_m, lds = 0;
+  if (a.slots) {
+    // at most one part-filled tile per active row
+    const int64_t cap = a.n_rows < a.M ? a.n_rows : a.M;
+    tiles_m = cap + a.M / TM;
+    lds = (cap + 1) * sizeof(int);
+  } else {
+    tiles_m = (a.M + TM - 1) / TM;
+  }
+  if (tiles_m * tiles_n >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemm_i8_tile<TN, TM, WN, WM, S, GU>), dim3((unsigned)(tiles_m * tiles_n)),
+                     dim3(64 * WN * WM), lds, stream, a, (int)tiles_n);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_i8_tile(const I8Args& a, hipStream_t s) {
+  if (a.gate_up) return go<128, 64, 4, 2, 4, true>(a, s);
+  if (a.slots) return go<128, 64, 4, 2, 4, false>(a, s);
+  const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  if (big >= device_cus()) return go<256, 256, 2, 4, 2, false>(a, s);
+  return go<64, 64, 2, 2, 4, false>(a, s);
+}
+
+}  // namespace moe

@@ -44,4 +44,33 @@ bool layer_few_fits(int T, int k, int H, int I);
 size_t layer_few_workspace_bytes(int T, int k, int I);
 hipError_t launch_layer_few(const FewArgs& a, hipStream_t stream);
 
+// Rows to 8-bit integers with a scale each (quantize_i8.hip): rows 0 .. rows-1
+// of x, or with a split the slots it lists (rows = T*k then bounds the launch).
+hipError_t launch_quantize_rows(const void* x, int dtype, int64_t ld, int rows, int K,
+                                const moe_split* split, int8_t* q, float* scale,
+                                hipStream_t stream);
+
+// Products of 8-bit rows: y[r][n] = sa[r] * sw[n] * sum_k a[r][k] w[n][k].
+// Dense (split null): rows 0 .. M-1 and one weight matrix. Grouped: the slots
+// of each active row of the split against that row's matrix; activation row
+// slot / k (by_token) or slot, output row slot. With `gate_up` the matrix has 2N
+// rows, gate then up, and y is fp32 silu(gate) * up.
+struct I8Args {
+  const int8_t* a;
+  int64_t lda;
+  const float* sa;
+  const int8_t* w;
+  const float* sw;
+  int M, N, K;  // grouped: M = T * k, a bound on the slots
+  const int32_t *n_active, *active_rows, *row_off, *slots;  // null: dense
+  int n_rows;   // grouped: rows of the bank
+  int k, by_token, gate_up;
+  int host;     // the weights are in pinned host memory
+  void* y;
+  int dtype;
+  int64_t ldy;
+};
+constexpr int kI8MaxK = 131072;  // 128 * 127 * K stays below 2^31
+hipError_t launch_gemm_i8(const I8Args& a, hipStream_t stream);
+
 }  // namespace moe

@@ -402,6 +402,74 @@ int moe_layer_few_mxfp4(const moe_bank *hot, const moe_bank *cold, const int32_t
                         int k, int H, int I, int32_t *counts_layer, int count_tmax,
                         int32_t *n_invalid, void *workspace, uint16_t *out, void *stream);
 
+/*
+ * 8-bit integer products. A row of activations (a token, a slot) carries one
+ * fp32 scale, a row of weights (an output channel) another:
+ *   y[m][n] = xs[m] * ws[n] * sum over k of xq[m][k] * w[n][k],
+ * the sum exact in int32, the scaling in fp32 (the sum times xs, then times
+ * ws), one rounding to y's type. The sums being exact, results depend on no
+ * tile, grid, bank or step size.
+ *
+ * moe_quantize_rows_i8 -- rows to 8-bit integers with one scale each.
+ *
+ * scale[r] = max over k of |x[r][k]| / 127 (fp32) and q[r][k] = the integer
+ * nearest to 127 * x[r][k] / max|x[r]|, ties to the even one, decided exactly;
+ * q lies in [-127, 127]. A row whose scale would be below the smallest normal
+ * fp32 number (an all-zero row among them) becomes zeros with scale 0; a row
+ * with an infinity or a NaN becomes zeros with scale NaN, so that whatever is
+ * computed from it is NaN.
+ *
+ * x: device, element type dtype, row r at x + r * ld elements, ld >= K, aligned
+ * to its element size (rows of whole 16-byte granules are faster). q: device
+ * int8 [rows][K]; must not overlap x. scale: device fp32 [rows]. 1 <= K <=
+ * MOE_I8_MAX_K. Launches one kernel; nothing when rows == 0. May be captured.
+ */
+#define MOE_I8_MAX_K 131072
+int moe_quantize_rows_i8(const void *x, int dtype, int64_t ld, int rows, int K, int8_t *q,
+                         float *scale, void *stream);
+
+/*
+ * moe_linear_i8 -- the dense product, for the layers around the routed one (a
+ * shared expert, projections).
+ *
+ * xq: device int8, M rows of K at xq + m * ldx (ldx >= K). xs: device fp32 [M].
+ * w: device int8 [N][K] (any values). ws: device fp32 [N]. y: device, element
+ * type dtype, row m at y + m * ldy elements (ldy >= N), aligned to its element
+ * size; must not overlap the inputs. K and ldx multiples of 16, K <=
+ * MOE_I8_MAX_K; xq and w 16-byte aligned. Launches one kernel; nothing when M
+ * or N is 0. May be captured.
+ */
+int moe_linear_i8(const int8_t *xq, int64_t ldx, const float *xs, int M, const int8_t *w,
+                  const float *ws, int N, int K, void *y, int dtype, int64_t ldy, void *stream);
+
+/* Bytes of the device workspace moe_expert_ffn_i8 needs: h per slot in fp32 and
+ * in 8 bits, with its scale. 0 when an argument is <= 0. */
+size_t moe_ffn_i8_workspace_bytes(int T, int k, int H, int I);
+
+/*
+ * moe_expert_ffn_i8 -- moe_expert_ffn_mxfp4 for a bank of 8-bit integer
+ * experts.
+ *
+ * For each active row r of `split` and each slot s of that row, with token t =
+ * s / k: g and u = the products of x[t] with w13[r] (rows [0, I) gate, [I, 2I)
+ * up), h = silu(g) * u in fp32, h quantized as one row per slot
+ * (moe_quantize_rows_i8), y = its product with w2[r], Y[s] = bf16(y). Rows are
+ * unweighted, as there; only this bank's slots of Y are written.
+ *
+ * bank: w13 int8 [R][2I][H], s13 fp32 [R][2I], w2 int8 [R][H][I], s2 fp32
+ * [R][H] (one scale per output channel), 16-byte aligned; on_host as in
+ * moe_bank (pinned host tensors are read in place). moe_stage_rows,
+ * moe_stage_rows_dma and moe_swap_rows move MXFP4 banks only. xq, xs: the
+ * step's activations from moe_quantize_rows_i8, int8 [T][H] and fp32 [T]. H
+ * and I positive multiples of 64, at most 32768; T * k <= 2^24. workspace:
+ * device, moe_ffn_i8_workspace_bytes(T, k, H, I) bytes; both bank calls of one
+ * step may share one (each writes only its own slots). Y: device bf16
+ * [T*k][H]. xq, workspace and Y 16-byte aligned. Launches three kernels;
+ * nothing when T == 0 or the bank has no rows. May be captured.
+ */
+int moe_expert_ffn_i8(const moe_bank *bank, moe_split split, const int8_t *xq, const float *xs,
+                      int T, int k, int H, int I, void *workspace, uint16_t *Y, void *stream);
+
 /* Message for the last error returned on this thread ("" if none). */
 const char *moe_last_error(void);
 

@@ -72,3 +72,52 @@ def test_binding_refuses_host_and_odd_tensors():
     with pytest.raises(moe.MoeError):
         moe.moe_topk_gate(l.to(torch.int32), torch.zeros(4, 2, dtype=torch.int32),
                           torch.zeros(4, 2))
+
+
+def test_quantize_refusals(L):
+    def call(x=P, dtype=0, ld=64, rows=4, K=64, q=8 * P, s=P):
+        return L.moe_quantize_rows_i8(x, dtype, ld, rows, K, q, s, None)
+    for kw, text in (({"dtype": 9}, "dtype"), ({"rows": -1}, "rows"), ({"K": 0, "ld": 0}, "K="),
+                     ({"K": 131073, "ld": 131073}, "K="), ({"ld": 63}, "ld="),
+                     ({"x": None}, "NULL"), ({"q": None}, "NULL"), ({"s": None}, "NULL"),
+                     ({"x": P + 1}, "aligned"), ({"s": P + 2}, "aligned"),
+                     ({"q": P + 100}, "overlap")):
+        refused(call(**kw), moe.MOE_EINVAL, text)
+    assert call(rows=0, x=None) == moe.MOE_OK
+
+
+def test_linear_refusals(L):
+    def call(xq=P, ldx=64, xs=P, M=4, w=2 * P, ws=P, N=8, K=64, y=8 * P, dtype=0, ldy=8):
+        return L.moe_linear_i8(xq, ldx, xs, M, w, ws, N, K, y, dtype, ldy, None)
+    for kw, text in (({"dtype": 3}, "dtype"), ({"M": -1}, "M="), ({"N": -1}, "N="),
+                     ({"K": 0}, "K="), ({"K": 24}, "K="), ({"K": 131088, "ldx": 131088}, "K="),
+                     ({"ldx": 48}, "ldx"), ({"ldx": 72}, "ldx"), ({"ldy": 7}, "ldy"),
+                     ({"xq": None}, "NULL"), ({"xs": None}, "NULL"), ({"w": None}, "NULL"),
+                     ({"ws": None}, "NULL"), ({"y": None}, "NULL"), ({"xq": P + 8}, "aligned"),
+                     ({"w": P + 4}, "aligned"), ({"y": 8 * P + 1}, "aligned"),
+                     ({"xs": P + 1}, "aligned"), ({"y": P + 16}, "overlap"),
+                     ({"y": 2 * P + 32}, "overlap")):
+        refused(call(**kw), moe.MOE_EINVAL, text)
+    assert call(M=0, xq=None) == moe.MOE_OK and call(N=0, ldy=0, w=None) == moe.MOE_OK
+
+
+def test_ffn_i8_refusals(L):
+    def call(bank=None, split=P, xq=P, xs=P, T=4, k=2, H=256, I=128, ws=P, Y=P):
+        bank = moe.MoeBankC(P, P, P, P, 4, 0) if bank is None else bank
+        sp = moe.MoeSplitC(split, split, split, split)
+        return L.moe_expert_ffn_i8(ctypes.byref(bank) if bank else None, sp, xq, xs, T, k, H, I, ws,
+                                   Y, None)
+    for kw, text in (({"T": -1}, "T="), ({"k": 0}, "k="), ({"k": 33}, "k="),
+                     ({"T": 2 ** 24}, "T*k"), ({"H": 100}, "multiples"), ({"I": 0}, "multiples"),
+                     ({"bank": 0}, "NULL"), ({"bank": moe.MoeBankC(P, P, P, P, 5000, 0)}, "rows"),
+                     ({"split": 0}, "split"), ({"xq": None}, "NULL"), ({"xs": None}, "NULL"),
+                     ({"ws": None}, "NULL"), ({"Y": None}, "NULL"), ({"xq": P + 8}, "aligned"),
+                     ({"Y": P + 2}, "aligned"), ({"ws": P + 4}, "aligned"),
+                     ({"bank": moe.MoeBankC(P, P + 4, P, P, 4, 0)}, "aligned"),
+                     ({"bank": moe.MoeBankC(P, P, P, P, 4, 7)}, "on_host")):
+        refused(call(**kw), moe.MOE_EINVAL, text)
+    refused(call(H=32832), moe.MOE_ENOTSUP, "supported")
+    assert call(T=0, xq=None) == moe.MOE_OK
+    assert call(bank=moe.MoeBankC(0, 0, 0, 0, 0, 0)) == moe.MOE_OK
+    assert moe.moe_ffn_i8_workspace_bytes(16, 6, 4096, 2880) == 96 * (2880 * 5 + 4)
+    assert moe.moe_ffn_i8_workspace_bytes(16, 0, 4096, 2880) == 0
