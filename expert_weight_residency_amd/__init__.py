@@ -471,42 +471,72 @@ def moe_swap_rows(hot: Bank, cold: Bank, hot_row: int, cold_row: int, expect_hot
 
 # ------------------------------------------------- around the residency split --
 
-_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
+_dt = None
 
 
-def _rows2d(t, name: str):
+def _dtypes():
+    """torch dtype -> element type code of the entry points that take several."""
+    global _dt
+    if _dt is None:
+        import torch
+        _dt = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    return _dt
+
+
+def _current(stream):
+    """(current device index, raw stream): the device the kernels are launched
+    on, and its current stream unless one is given."""
+    import torch
+    dev = torch.cuda.current_device()
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _stream(stream)
+
+
+def _on(dev: int, **tensors) -> None:
+    """Raise MOE_EINVAL unless the GPU tensors among them (None and host
+    tensors aside) sit on device dev."""
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.get_device() != dev:
+            raise MoeError(MOE_EINVAL, f"{name}: on {t.device}, the current device is cuda:{dev}")
+
+
+def _ptr(t, name: str, dtype):
+    """Data pointer of a contiguous GPU tensor of the torch dtype."""
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise _bad(name, f"a contiguous GPU tensor ({dtype})", t)
+    return t.data_ptr()
+
+
+def _rows2d(t, name: str, dtypes):
     """(pointer, dtype code, rows, columns, row stride) of a 2-D GPU tensor
     whose rows are contiguous."""
-    code = _DTYPES.get(str(getattr(t, "dtype", "")))
-    if code is None or t.device.type != "cuda" or t.dim() != 2 or \
-            (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise _bad(name, "a 2-D GPU tensor (bfloat16, float16, float32) of contiguous rows", t)
-    rows, cols = int(t.shape[0]), int(t.shape[1])
-    return t.data_ptr(), code, rows, cols, int(t.stride(0)) if rows > 1 else cols
-
-
-def _same_device(*named) -> None:
-    """Raise MOE_EINVAL unless the GPU tensors sit on the current device (the
-    one the kernels are launched on)."""
-    import torch
-    cur = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and t.device.type == "cuda" and t.device.index != cur:
-            raise MoeError(MOE_EINVAL, f"{name}: on {t.device}, the current device is cuda:{cur}")
+    code = dtypes.get(t.dtype)
+    if code is None or not t.is_cuda or t.dim() != 2:
+        raise _bad(name, f"a 2-D GPU tensor ({', '.join(str(d) for d in dtypes)})", t)
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (cols > 1 and step != 1) or ld < cols:
+        raise _bad(name, "contiguous rows that do not overlap", t)
+    return t.data_ptr(), code, rows, cols, ld
 
 
 def moe_topk_gate(logits, topk_ids, topk_w, norm: int = GATE_NORM_PICKS, stream=None) -> None:
     """logits [T,E] (bfloat16, float16 or float32; rows may be strided) ->
     topk_ids int32 [T,k], topk_w fp32 [T,k] (see the header for masked experts
     and ties)."""
-    p, dtype, T, E, ld = _rows2d(logits, "logits")
-    _same_device(("logits", logits), ("topk_ids", topk_ids), ("topk_w", topk_w))
-    if topk_ids.dim() != 2 or int(topk_ids.shape[0]) != T or topk_w.shape != topk_ids.shape:
+    import torch
+    p, dtype, T, E, ld = _rows2d(logits, "logits", _dtypes())
+    dev, s = _current(stream)
+    _on(dev, logits=logits, topk_ids=topk_ids, topk_w=topk_w)
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T or topk_w.shape != topk_ids.shape:
         raise MoeError(MOE_EINVAL, f"topk_ids {tuple(topk_ids.shape)}, topk_w "
                                    f"{tuple(topk_w.shape)}: need [{T}, k] each")
-    _check(lib().moe_topk_gate(p, dtype, ld, T, E, int(topk_ids.shape[1]), int(norm),
-                               _gpu(topk_ids, "topk_ids", ("torch.int32",)),
-                               _gpu(topk_w, "topk_w", ("torch.float32",)), _stream(stream)))
+    _check(lib().moe_topk_gate(p, dtype, ld, T, E, topk_ids.shape[1], int(norm),
+                               _ptr(topk_ids, "topk_ids", torch.int32),
+                               _ptr(topk_w, "topk_w", torch.float32), s))
 
 
 def moe_layer_few_workspace_bytes(T: int, k: int, H: int, I: int) -> int:
@@ -518,13 +548,14 @@ def moe_layer_few_mxfp4(hot: Bank, cold: Bank, row_map, x, topk_ids, topk_w, I: 
                         stream=None) -> None:
     """The whole layer for at most MOE_FEW_MAX_TOKENS tokens in two launches:
     x bf16 [T,H], topk_ids int32 [T,k], topk_w fp32 [T,k] -> out bf16 [T,H]."""
-    T, H, k, E = int(x.shape[0]), int(x.shape[1]), int(topk_ids.shape[1]), int(row_map.shape[0])
-    if int(topk_ids.shape[0]) != T or topk_w.shape != topk_ids.shape:
+    import torch
+    (T, H), k, E = x.shape, topk_ids.shape[1], row_map.shape[0]
+    if topk_ids.shape[0] != T or topk_w.shape != topk_ids.shape:
         raise MoeError(MOE_EINVAL, f"topk_ids {tuple(topk_ids.shape)}, topk_w "
                                    f"{tuple(topk_w.shape)}: need [{T}, k] each")
-    _same_device(("x", x), ("out", out), ("topk_ids", topk_ids), ("topk_w", topk_w),
-                 ("row_map", row_map), ("workspace", workspace), ("n_invalid", n_invalid),
-                 ("counts", counts_layer), ("hot bank", hot.w13), ("cold bank", cold.w13))
+    dev, s = _current(stream)
+    _on(dev, x=x, out=out, topk_ids=topk_ids, topk_w=topk_w, row_map=row_map, workspace=workspace,
+        n_invalid=n_invalid, counts_layer=counts_layer, hot_bank=hot.w13, cold_bank=cold.w13)
     if T > 0:
         _check_bank(hot, H, I, "hot bank")
         _check_bank(cold, H, I, "cold bank")
@@ -538,14 +569,15 @@ def moe_layer_few_mxfp4(hot: Bank, cold: Bank, row_map, x, topk_ids, topk_w, I: 
         _need(n_invalid, "n_invalid", 4)
         if counts_layer is not None:
             _need(counts_layer, "counts_layer", 4 * E)
-    i32 = ("torch.int32",)
+    i32 = torch.int32
     h, c = hot.abi(), cold.abi()
     _check(lib().moe_layer_few_mxfp4(
-        ctypes.byref(h), ctypes.byref(c), _gpu(row_map, "row_map", i32), E,
-        _gpu(x, "x", _BF16_BITS), _gpu(topk_ids, "topk_ids", i32),
-        _gpu(topk_w, "topk_w", ("torch.float32",)), T, k, H, I,
-        _gpu_opt(counts_layer, "counts", i32), count_tmax, _gpu(n_invalid, "n_invalid", i32),
-        _gpu(workspace, "workspace"), _gpu(out, "out", _BF16_BITS), _stream(stream)))
+        ctypes.byref(h), ctypes.byref(c), _ptr(row_map, "row_map", i32), E,
+        _gpu(x, "x", _BF16_BITS), _ptr(topk_ids, "topk_ids", i32),
+        _ptr(topk_w, "topk_w", torch.float32), T, k, H, I,
+        None if counts_layer is None else _ptr(counts_layer, "counts_layer", i32), count_tmax,
+        _ptr(n_invalid, "n_invalid", i32), _gpu(workspace, "workspace"),
+        _gpu(out, "out", _BF16_BITS), s))
 
 
 @dataclass
@@ -573,35 +605,33 @@ class BankI8:
 def moe_quantize_rows_i8(x, q, scale, stream=None) -> None:
     """x [rows,K] (bfloat16, float16 or float32; rows may be strided) -> q int8
     [rows,K], scale fp32 [rows]."""
-    p, dtype, rows, K, ld = _rows2d(x, "x")
-    _same_device(("x", x), ("q", q), ("scale", scale))
-    if tuple(q.shape) != (rows, K):
-        raise MoeError(MOE_EINVAL, f"q {tuple(q.shape)}: need {(rows, K)}")
-    _need(scale, "scale", 4 * rows)
-    _check(lib().moe_quantize_rows_i8(p, dtype, ld, rows, K, _gpu(q, "q", ("torch.int8",)),
-                                      _gpu(scale, "scale", ("torch.float32",)), _stream(stream)))
+    import torch
+    p, dtype, rows, K, ld = _rows2d(x, "x", _dtypes())
+    dev, s = _current(stream)
+    _on(dev, x=x, q=q, scale=scale)
+    if q.shape != x.shape or scale.numel() < rows:
+        raise MoeError(MOE_EINVAL, f"q {tuple(q.shape)}, scale {tuple(scale.shape)}: need "
+                                   f"{(rows, K)} and {(rows,)}")
+    _check(lib().moe_quantize_rows_i8(p, dtype, ld, rows, K, _ptr(q, "q", torch.int8),
+                                      _ptr(scale, "scale", torch.float32), s))
 
 
 def moe_linear_i8(xq, xs, w, ws, y, stream=None) -> None:
     """xq int8 [M,K] (rows may be strided) with scales xs fp32 [M], times w int8
     [N,K] with scales ws fp32 [N] -> y [M,N] (bfloat16, float16 or float32; rows
     may be strided)."""
-    if str(getattr(xq, "dtype", "")) != "torch.int8" or xq.device.type != "cuda" or \
-            xq.dim() != 2 or (xq.shape[1] > 1 and xq.stride(1) != 1) or \
-            (xq.shape[0] > 1 and xq.stride(0) < xq.shape[1]):
-        raise _bad("xq", "a 2-D int8 GPU tensor of contiguous rows", xq)
-    M, K = int(xq.shape[0]), int(xq.shape[1])
-    yp, dtype, my, N, ldy = _rows2d(y, "y")
-    _same_device(("xq", xq), ("xs", xs), ("w", w), ("ws", ws), ("y", y))
-    if my != M or tuple(w.shape) != (N, K):
-        raise MoeError(MOE_EINVAL, f"xq {(M, K)}, w {tuple(w.shape)}, y {(my, N)}: need [M,K], "
-                                   "[N,K], [M,N]")
-    _need(xs, "xs", 4 * M)
-    _need(ws, "ws", 4 * N)
-    _check(lib().moe_linear_i8(xq.data_ptr(), int(xq.stride(0)) if M > 1 else K,
-                               _gpu(xs, "xs", ("torch.float32",)), M, _gpu(w, "w", ("torch.int8",)),
-                               _gpu(ws, "ws", ("torch.float32",)), N, K, yp, dtype, ldy,
-                               _stream(stream)))
+    import torch
+    xp, _, M, K, ldx = _rows2d(xq, "xq", {torch.int8: 0})
+    yp, dtype, my, N, ldy = _rows2d(y, "y", _dtypes())
+    dev, s = _current(stream)
+    _on(dev, xq=xq, xs=xs, w=w, ws=ws, y=y)
+    if my != M or w.shape != (N, K) or xs.numel() < M or ws.numel() < N:
+        raise MoeError(MOE_EINVAL, f"xq {(M, K)}, xs {tuple(xs.shape)}, w {tuple(w.shape)}, ws "
+                                   f"{tuple(ws.shape)}, y {(my, N)}: need [M,K], [M], [N,K], [N], "
+                                   "[M,N]")
+    f32 = torch.float32
+    _check(lib().moe_linear_i8(xp, ldx, _ptr(xs, "xs", f32), M, _ptr(w, "w", torch.int8),
+                               _ptr(ws, "ws", f32), N, K, yp, dtype, ldy, s))
 
 
 def moe_ffn_i8_workspace_bytes(T: int, k: int, H: int, I: int) -> int:
@@ -612,8 +642,10 @@ def moe_expert_ffn_i8(bank: BankI8, split: Split, xq, xs, k: int, I: int, worksp
                       stream=None) -> None:
     """The expert FFN over one bank's picks with 8-bit integer experts; xq int8
     [T,H] and xs fp32 [T] from moe_quantize_rows_i8."""
-    T, H = int(xq.shape[0]), int(xq.shape[1])
-    _same_device(("xq", xq), ("xs", xs), ("bank", bank.w13), ("workspace", workspace), ("Y", Y))
+    import torch
+    T, H = xq.shape
+    dev, s = _current(stream)
+    _on(dev, xq=xq, xs=xs, bank=bank.w13, slots=split.slots, workspace=workspace, Y=Y)
     if T > 0 and bank.n_rows > 0:
         R = bank.n_rows
         for name, n in (("w13", R * 2 * I * H), ("s13", R * 2 * I), ("w2", R * H * I),
@@ -629,7 +661,6 @@ def moe_expert_ffn_i8(bank: BankI8, split: Split, xq, xs, k: int, I: int, worksp
         _need(workspace, "workspace", moe_ffn_i8_workspace_bytes(T, k, H, I))
         _need(Y, "Y", 2 * T * k * H)
     b = bank.abi()
-    _check(lib().moe_expert_ffn_i8(ctypes.byref(b), split.abi(), _gpu(xq, "xq", ("torch.int8",)),
-                                   _gpu(xs, "xs", ("torch.float32",)), T, k, H, I,
-                                   _gpu(workspace, "workspace"), _gpu(Y, "Y", _BF16_BITS),
-                                   _stream(stream)))
+    _check(lib().moe_expert_ffn_i8(ctypes.byref(b), split.abi(), _ptr(xq, "xq", torch.int8),
+                                   _ptr(xs, "xs", torch.float32), T, k, H, I,
+                                   _gpu(workspace, "workspace"), _gpu(Y, "Y", _BF16_BITS), s))

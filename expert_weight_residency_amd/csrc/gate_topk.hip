@@ -18,11 +18,29 @@ namespace {
 
 constexpr int kWaves = 4;  // tokens per workgroup
 
+// f over all 64 lanes, in every lane: within rows of 16 by DPP (quad
+// permutations, mirrors), then across rows and halves with the lane swaps, all
+// of them VALU operations (the LDS-based shuffles took most of the kernel's
+// time: 5.7 us for 7 tokens, 9.0 for 4096).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
 template <typename F>
 __device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = f(v, (uint32_t)__shfl_xor((int)v, d, 64));
-  return v;
+  v = f(v, dpp<0xb1>(v));   // quad_perm [1,0,3,2]
+  v = f(v, dpp<0x4e>(v));   // quad_perm [2,3,0,1]
+  v = f(v, dpp<0x141>(v));  // row_half_mirror
+  v = f(v, dpp<0x140>(v));  // row_mirror
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = f(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return f(b[0], b[1]);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
 __device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int dtype) {
@@ -76,9 +94,7 @@ __global__ __launch_bounds__(64 * kWaves) void topk_gate(const void* __restrict_
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (key[i]) s += key[i] == m ? 1.0f : expf(key_value(key[i]) - top);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d, 64);
-        all = s;
+        all = wave_sum(s);
       }
     }
     if (lane == j) {
@@ -91,10 +107,7 @@ __global__ __launch_bounds__(64 * kWaves) void topk_gate(const void* __restrict_
   // equal to the maximum: weight exp(0), also for an infinite one
   const float v = my_key ? key_value(my_key) : 0.0f;
   const float p = my_key ? (v == top ? 1.0f : expf(v - top)) : 0.0f;
-  float total = p;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d, 64);
-  if (norm == MOE_GATE_NORM_ALL) total = all;
+  const float total = norm == MOE_GATE_NORM_ALL ? all : wave_sum(p);
   if (lane < k) {
     ids[(int64_t)t * k + lane] = my_id;
     w[(int64_t)t * k + lane] = my_key ? p / total : 0.0f;

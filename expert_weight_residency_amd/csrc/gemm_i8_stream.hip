@@ -218,62 +218,66 @@ __global__ __launch_bounds__(kThreads, 2) void gemm_i8_stream(I8Args a, int ks, 
       const bool live = step < steps;
       if (live && pc.u != cur) enter(pc);
       i32x4 acc[RG][SETS];
-#pragma unroll
-      for (int g = 0; g < RG; ++g)
-#pragma unroll
-        for (int st = 0; st < SETS; ++st) {
-          acc[g][st] = i32x4{0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < CPW; ++j)
-            acc[g][st] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ring[u][g][j], xb[st][j],
-                                                               acc[g][st], 0, 0, 0);
-        }
-      issue(ring[u]);
-      if (diag) {
-        int* o = red + ((step & 1) * nsub + sub) * per_sub + red_off;
+      if (live) {
 #pragma unroll
         for (int g = 0; g < RG; ++g)
 #pragma unroll
-          for (int st = 0; st < SETS; ++st)
-            *reinterpret_cast<i32x4*>(o + (g * SETS + st) * 2 * ks * 64) = acc[g][st];
-      }
-      lds_barrier();
-      // see few_gate_up: one wavefront per item, each in turn
-      for (int sb = 0; sb < nsub && live; ++sb) {
-        const int ib = pc.ib + sb;
-        if (ib >= pc.end || (step * nsub + sb) % kWaves != wv) continue;
-        const int* o = red + ((step & 1) * nsub + sb) * per_sub + lane;
-        const float* sw = l_sw + (ib - sw0) * 8 * RG + (lane & 7);
-        const int nn = 8 * ib + (lane & 7);
+          for (int st = 0; st < SETS; ++st) {
+            acc[g][st] = i32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int st = 0; st < SETS; ++st) {
-          int s[RG];
-#pragma unroll
-          for (int g = 0; g < RG; ++g) s[g] = 0;
-          auto add = [&](int p) {
-#pragma unroll
-            for (int g = 0; g < RG; ++g) s[g] += o[((g * SETS + st) * 2 * ks + p) * 64];
-          };
-          if (ks == kWaves) {
-#pragma unroll
-            for (int p = 0; p < 2 * kWaves; ++p) add(p);
-          } else {
-            for (int p = 0; p < 2 * ks; ++p) add(p);
+            for (int j = 0; j < CPW; ++j)
+              acc[g][st] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ring[u][g][j], xb[st][j],
+                                                                 acc[g][st], 0, 0, 0);
           }
-          const int c = st * 8 + (lane >> 3);
-          const int row = l_row[c];
-          if (row >= 0 && nn < N) {
-            const float sa = l_sa[c];
-            if constexpr (GU) {
-              static_cast<float*>(a.y)[(int64_t)row * a.ldy + nn] =
-                  mx::silu_f32((float)s[0] * sa * sw[0]) * ((float)s[RG - 1] * sa * sw[8]);
+      }
+      issue(ring[u]);
+      if (live) {
+        if (diag) {
+          int* o = red + ((step & 1) * nsub + sub) * per_sub + red_off;
+#pragma unroll
+          for (int g = 0; g < RG; ++g)
+#pragma unroll
+            for (int st = 0; st < SETS; ++st)
+              *reinterpret_cast<i32x4*>(o + (g * SETS + st) * 2 * ks * 64) = acc[g][st];
+        }
+        lds_barrier();
+        // see few_gate_up: one wavefront per item, each in turn
+        for (int sb = 0; sb < nsub; ++sb) {
+          const int ib = pc.ib + sb;
+          if (ib >= pc.end || (step * nsub + sb) % kWaves != wv) continue;
+          const int* o = red + ((step & 1) * nsub + sb) * per_sub + lane;
+          const float* sw = l_sw + (ib - sw0) * 8 * RG + (lane & 7);
+          const int nn = 8 * ib + (lane & 7);
+#pragma unroll
+          for (int st = 0; st < SETS; ++st) {
+            int s[RG];
+#pragma unroll
+            for (int g = 0; g < RG; ++g) s[g] = 0;
+            auto add = [&](int p) {
+#pragma unroll
+              for (int g = 0; g < RG; ++g) s[g] += o[((g * SETS + st) * 2 * ks + p) * 64];
+            };
+            if (ks == kWaves) {
+#pragma unroll
+              for (int p = 0; p < 2 * kWaves; ++p) add(p);
             } else {
-              store1(a, row, nn, (float)s[0] * sa * sw[0]);
+              for (int p = 0; p < 2 * ks; ++p) add(p);
+            }
+            const int c = st * 8 + (lane >> 3);
+            const int row = l_row[c];
+            if (row >= 0 && nn < N) {
+              const float sa = l_sa[c];
+              if constexpr (GU) {
+                static_cast<float*>(a.y)[(int64_t)row * a.ldy + nn] =
+                    mx::silu_f32((float)s[0] * sa * sw[0]) * ((float)s[RG - 1] * sa * sw[8]);
+              } else {
+                store1(a, row, nn, (float)s[0] * sa * sw[0]);
+              }
             }
           }
         }
+        advance(pc);
       }
-      if (live) advance(pc);
     }
   }
 }

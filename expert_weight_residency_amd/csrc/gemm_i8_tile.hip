@@ -43,8 +43,18 @@ constexpr int vm_lds(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
 
 
 // TN x TM tile (weight rows x activation rows), WN x WM wavefronts.
+// Workgroups go round the 8 XCDs in turn, each with its own L2: XCD x takes the
+// x-th eighth of the items, so that neighbours, which share rows, meet in one
+// L2. The item of this workgroup, -1: none.
+constexpr int kXcds = 8;
+__device__ __forceinline__ int xcd_item(int items) {
+  const int per = (items + kXcds - 1) / kXcds, at = blockIdx.x / kXcds;
+  const int item = (blockIdx.x % kXcds) * per + at;
+  return at < per && item < items ? item : -1;
+}
+
 template <int TN, int TM, int WN, int WM, int S, bool GU>
-__global__ __launch_bounds__(64 * WN * WM, WN * WM > 4 ? 2 : 1) void gemm_i8_tile(I8Args a,
+__global__ __launch_bounds__(64 * WN * WM, TN + TM >= 512 ? 2 : WN * WM / 2) void gemm_i8_tile(I8Args a,
                                                                                int tiles_n) {
   constexpr int kW = WN * WM, kRows = TN + TM, kCopies = kRows / 8 / kW;
   static_assert(kRows % (8 * kW) == 0 && TN % (8 * kW) == 0, "whole copies per wavefront");
@@ -69,11 +79,12 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM > 4 ? 2 : 1) void gemm_i8_til
     __shared__ int wsum[kW];
     const int na = *a.n_active;
     tiles::build_tile_prefix<TM, kW>(a.row_off, na, tpre, wsum);
-    if ((int)blockIdx.x >= tpre[na] * tiles_n) return;  // the whole workgroup
+    const int item = xcd_item(tpre[na] * tiles_n);
+    if (item < 0) return;  // the whole workgroup
     // items of one expert: weight rows outermost, so that its tiles meet a
     // block of weights together
-    const int e = tiles::row_of_tile(tpre, na, blockIdx.x / tiles_n);
-    const int local = blockIdx.x - tpre[e] * tiles_n, nt = tpre[e + 1] - tpre[e];
+    const int e = tiles::row_of_tile(tpre, na, item / tiles_n);
+    const int local = item - tpre[e] * tiles_n, nt = tpre[e + 1] - tpre[e];
     const int nb = local / nt, mt = local - nb * nt;
     m0 = a.row_off[e] + mt * TM;
     m1 = min(m0 + TM, a.row_off[e + 1]);
@@ -82,7 +93,9 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM > 4 ? 2 : 1) void gemm_i8_til
     w += row * wrows * (int64_t)K;
     sw += row * wrows;
   } else {
-    const int mt = blockIdx.x / tiles_n, nb = blockIdx.x - mt * tiles_n;
+    const int item = xcd_item((a.M + TM - 1) / TM * tiles_n);
+    if (item < 0) return;
+    const int mt = item / tiles_n, nb = item - mt * tiles_n;
     m0 = mt * TM;
     m1 = min(m0 + TM, a.M);
     n0 = nb * TN;
@@ -226,17 +239,18 @@ hipError_t go(const I8Args& a, hipStream_t stream) {
   } else {
     tiles_m = (a.M + TM - 1) / TM;
   }
-  if (tiles_m * tiles_n >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((gemm_i8_tile<TN, TM, WN, WM, S, GU>), dim3((unsigned)(tiles_m * tiles_n)),
-                     dim3(64 * WN * WM), lds, stream, a, (int)tiles_n);
+  if (tiles_m * tiles_n >= ((int64_t)1 << 31) - kXcds) return hipErrorInvalidValue;
+  const unsigned grid = (unsigned)((tiles_m * tiles_n + kXcds - 1) / kXcds * kXcds);
+  hipLaunchKernelGGL((gemm_i8_tile<TN, TM, WN, WM, S, GU>), dim3(grid), dim3(64 * WN * WM), lds,
+                     stream, a, (int)tiles_n);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gemm_i8_tile(const I8Args& a, hipStream_t s) {
-  if (a.gate_up) return go<128, 64, 4, 2, 4, true>(a, s);
-  if (a.slots) return go<128, 64, 4, 2, 4, false>(a, s);
+  if (a.gate_up) return go<128, 64, 4, 2, 3, true>(a, s);
+  if (a.slots) return go<128, 64, 4, 2, 3, false>(a, s);
   const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   if (big >= device_cus()) return go<256, 256, 2, 4, 2, false>(a, s);
   return go<64, 64, 2, 2, 4, false>(a, s);
