@@ -189,13 +189,16 @@ __global__ __launch_bounds__(64 * WN * WM, TN + TM >= 512 ? 2 : WN * WM / 2) voi
   __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
 
   // lane (r, q): outputs 16 i + 4 q + v of activation row 16 j + r
+  auto rows = [&](auto f) {
 #pragma unroll
-  for (int j = 0; j < MF; ++j) {
-    const int m = m0 + (wm * MF + j) * 16 + r;
-    if (m >= m1) continue;
-    const float sa = a.sa[arow(m)];
-    const int64_t orow = a.slots ? a.slots[m] : m;
-    if constexpr (GU) {
+    for (int j = 0; j < MF; ++j) {
+      const int m = m0 + (wm * MF + j) * 16 + r;
+      if (m >= m1) continue;
+      f(j, a.sa[arow(m)], a.slots ? (int64_t)a.slots[m] : (int64_t)m);
+    }
+  };
+  if constexpr (GU) {
+    rows([&](int j, float sa, int64_t orow) {
 #pragma unroll
       for (int i = 0; i < NF; i += 2) {
         const int n = n0 + (wn * NF + i) * 8 + 4 * q;
@@ -211,19 +214,167 @@ __global__ __launch_bounds__(64 * WN * WM, TN + TM >= 512 ? 2 : WN * WM / 2) voi
         *reinterpret_cast<float4*>(static_cast<float*>(a.y) + orow * a.ldy + n) =
             make_float4(h[0], h[1], h[2], h[3]);
       }
+    });
+  } else {
+    with_output(a, [&](auto type, auto vec) {
+      rows([&](int j, float sa, int64_t orow) {
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          const int n = n0 + (wn * NF + i) * 16 + 4 * q;
+          if (n >= N) continue;
+          float y[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            y[v] = (float)acc[i][j][v] * sa * sw[min(n + v, N - 1)];
+          store4<type(), vec()>(a, orow, n, y);
+        }
+      });
+    });
+  }
+}
+
+// Dense products large enough to fill the card with wide tiles: MFMA-bound, 8
+// wavefronts (2 x 4) of TN/2 x TM/4 outputs, S buffers of 128 bytes per row.
+// The operands of the next half step are read from LDS, spread between the
+// products of this one; the one barrier per step sits between its halves, after
+// the last read of the step's buffer, which then takes the copies for the step
+// S steps on.
+template <int TN, int TM, int S>
+__global__ __launch_bounds__(512, 2) void gemm_i8_big(I8Args a, int tiles_n) {
+  constexpr int WN = 2, WM = 4, kW = 8;
+  constexpr int kRows = TN + TM, kCopies = kRows / 8 / kW;
+  static_assert(kRows % (8 * kW) == 0 && (S == 2 || S == 3), "whole copies per wavefront");
+  constexpr int NF = TN / WN / 16, MF = TM / WM / 16;
+  __shared__ __align__(128) uint8_t buf0[kRows * 128];
+  __shared__ __align__(128) uint8_t buf1[kRows * 128];
+  __shared__ __align__(128) uint8_t buf2[S > 2 ? kRows * 128 : 16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int N = a.N, K = a.K, M = a.M;
+  // items in groups of 8 rows of tiles, column by column, so that an XCD's
+  // share is about square and its L2 meets few rows of either operand
+  const int tiles_m = (M + TM - 1) / TM;
+  const int item = xcd_item(tiles_m * tiles_n);
+  if (item < 0) return;
+  const int group = item / (8 * tiles_n), local = item - group * 8 * tiles_n;
+  const int gm = min(8, tiles_m - 8 * group);
+  const int m0 = (8 * group + local % gm) * TM, n0 = local / gm * TN;
+
+  const int gran = (lane & 7) ^ (lane >> 3);
+  const uint8_t* src[kCopies];
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) {
+    const int r = 8 * (wv + kW * i) + (lane >> 3);
+    const int8_t* p = r < TN ? a.w + (int64_t)min(n0 + r, N - 1) * K
+                             : a.a + (int64_t)min(m0 + (r - TN), M - 1) * a.lda;
+    src[i] = reinterpret_cast<const uint8_t*>(p) + 16 * gran;
+  }
+  auto copy = [&](uint8_t* buf, int k0) {
+    const bool in = k0 + 16 * gran < K;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      const uint8_t* p = in ? src[i] + k0 : kZeros;
+      asm volatile("" : "+v"(p));  // a select, not a branch around two copies
+      __builtin_amdgcn_global_load_lds(p, buf + 1024 * (wv + kW * i), 16, 0, 0);
+    }
+  };
+  i32x4 acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  const int wn = wv % WN, wm = wv / WN, r = lane & 15, q = lane >> 4;
+  struct Frags {
+    i32x4 b[MF], a[NF];
+  };
+  // rows 16 apart keep r & 7, so one swizzled offset per half serves all
+  const int off0 = r * 128 + 16 * (q ^ (r & 7)), off1 = r * 128 + 16 * ((4 + q) ^ (r & 7));
+  auto read = [&](const uint8_t* buf, int half, Frags& f) {
+    const uint8_t* p = buf + (half ? off1 : off0);
+#pragma unroll
+    for (int j = 0; j < MF; ++j)
+      f.b[j] = *reinterpret_cast<const i32x4*>(p + (TN + (wm * MF + j) * 16) * 128);
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+      f.a[i] = *reinterpret_cast<const i32x4*>(p + (wn * NF + i) * 16 * 128);
+  };
+  auto mul = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < MF; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+  };
+  Frags f0, f1;
+  auto spread = [&](bool copies) {
+    constexpr int kOps = NF + MF, kMul = NF * MF;
+#pragma unroll
+    for (int i = 0; i < kOps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (copies && i < kCopies) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kMul / kOps, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, kMul % kOps, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // the step out of `here`, f0 its first half's operands
+  auto step = [&](int k0, uint8_t* here, const uint8_t* next) {
+    read(here, 1, f1);
+    mul(f0);
+    spread(false);
+    tile_barrier(vm_lds((S - 2) * kCopies));  // the next step's copies have arrived
+    copy(here, k0 + 128 * S);
+    read(next, 0, f0);
+    mul(f1);
+    spread(true);
+  };
+  copy(buf0, 0);
+  copy(buf1, 128);
+  if constexpr (S > 2) copy(buf2, 256);
+  tile_barrier(vm_lds((S - 1) * kCopies));
+  read(buf0, 0, f0);
+  for (int k0 = 0; k0 < K; k0 += 128 * S) {
+    step(k0, buf0, buf1);
+    if constexpr (S == 2) {
+      step(k0 + 128, buf1, buf0);
     } else {
+      step(k0 + 128, buf1, buf2);
+      step(k0 + 256, buf2, buf0);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
+  float sw[NF][4];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) sw[i][v] = a.sw[min(n0 + (wn * NF + i) * 16 + 4 * q + v, N - 1)];
+  with_output(a, [&](auto type, auto vec) {
+#pragma unroll
+    for (int j = 0; j < MF; ++j) {
+      const int m = m0 + (wm * MF + j) * 16 + r;
+      if (m >= M) continue;
+      const float sa = a.sa[m];
 #pragma unroll
       for (int i = 0; i < NF; ++i) {
         const int n = n0 + (wn * NF + i) * 16 + 4 * q;
         if (n >= N) continue;
         float y[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          y[v] = (float)acc[i][j][v] * sa * sw[min(n + v, N - 1)];
-        store4(a, orow, n, y);
+        for (int v = 0; v < 4; ++v) y[v] = (float)acc[i][j][v] * sa * sw[i][v];
+        store4<type(), vec()>(a, m, n, y);
       }
     }
-  }
+  });
+}
+
+template <int TN, int TM, int S>
+hipError_t go_big(const I8Args& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.N + TN - 1) / TN, tiles = (int64_t)((a.M + TM - 1) / TM) * tiles_n;
+  if (tiles >= ((int64_t)1 << 31) - kXcds) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((gemm_i8_big<TN, TM, S>),
+                     dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds)), dim3(512), 0, stream, a,
+                     (int)tiles_n);
+  return hipGetLastError();
 }
 
 template <int TN, int TM, int WN, int WM, int S, bool GU>
@@ -251,9 +402,29 @@ hipError_t go(const I8Args& a, hipStream_t stream) {
 hipError_t launch_gemm_i8_tile(const I8Args& a, hipStream_t s) {
   if (a.gate_up) return go<128, 64, 4, 2, 3, true>(a, s);
   if (a.slots) return go<128, 64, 4, 2, 3, false>(a, s);
-  const int64_t big = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (big >= device_cus()) return go<256, 256, 2, 4, 2, false>(a, s);
-  return go<64, 64, 2, 2, 4, false>(a, s);
+  // Wide tiles once they fill the card: the width whose rounds over the CUs cost
+  // least (4096 x 5760 x 4096: 192 wide 102 us, 256 wide 119; 4096 x 4096 x 2880:
+  // 256 wide 60 us, 128 wide 63, 192 wide 81; 8192 x 8192 x 4096: 261, 312, 308).
+  const int cus = device_cus();
+  const int64_t tiles_m = (a.M + 255) / 256;
+  if (tiles_m * ((a.N + 255) / 256) >= cus) {
+    auto cost = [&](int tn) {
+      return (tiles_m * ((a.N + tn - 1) / tn) + cus - 1) / cus * tn;
+    };
+    const int64_t c256 = cost(256), c192 = cost(192), c128 = cost(128);
+    if (c256 <= c192 && c256 <= c128) return go_big<256, 256, 2>(a, s);
+    return c192 <= c128 ? go_big<192, 256, 2>(a, s) : go_big<128, 256, 3>(a, s);
+  }
+  // Smaller ones, us (each with about 6 of launch): 500 x 4096 x 4096 at 128 x
+  // 128 with the operands read ahead 19.9, at 128 x 64 23.2, 64 x 64 23.3; 1001 x
+  // 2048 x 1040 10.9, 9.7, 10.7; 112 x 4096 x 2880 at 64 x 64 10.7, at 32 x 64 8.3.
+  auto tiles = [&](int tn, int tm) {
+    return (int64_t)((a.N + tn - 1) / tn) * ((a.M + tm - 1) / tm);
+  };
+  if (a.K >= 2048 && tiles(128, 128) >= cus / 2) return go_big<128, 128, 3>(a, s);
+  if (tiles(128, 64) >= cus) return go<128, 64, 4, 2, 3, false>(a, s);
+  if (tiles(64, 64) >= cus) return go<64, 64, 2, 2, 3, false>(a, s);
+  return go<32, 64, 2, 2, 4, false>(a, s);
 }
 
 }  // namespace moe
