@@ -319,9 +319,127 @@ __device__ void build_tables(const FewArgs& a, Shared& L) {
   __syncthreads();
 }
 
-// CUs that read experts in host memory; the others stream the device banks
-// beside them.
+// Adds the partial sums of item `it` (o: this lane's, 64 apart; in their order)
+// and writes its 8 values of h for each token that picked the expert. One
+// wavefront.
+template <int SETS>
+__device__ __forceinline__ void write_h(const FewArgs& a, const Shared& L, int it, int ks,
+                                        const float* o, uint16_t* h) {
+  const int lane = threadIdx.x & 63, per = a.I / 8;
+  const int li = it / per, i0 = (it - li * per) * 8;
+  const int u = L.list[li];
+  const int mask = L.mask[u], base = L.base[u];
+#pragma unroll
+  for (int st = 0; st < SETS; ++st) {
+    float g = 0.0f, up = 0.0f;
+    auto add = [&](int p) {
+      g += o[(st * 2 * ks + p) * 64];
+      up += o[((SETS + st) * 2 * ks + p) * 64];
+    };
+    if (ks == kWaves) {
+#pragma unroll
+      for (int p = 0; p < 2 * kWaves; ++p) add(p);
+    } else {
+      for (int p = 0; p < 2 * ks; ++p) add(p);
+    }
+    const int t = st * 8 + (lane >> 3);
+    if ((mask >> t) & 1) {
+      const int rw = base + __popc(mask & ((1 << t) - 1));
+      h[(size_t)rw * a.I + i0 + (lane & 7)] =
+          (uint16_t)f32_to_bf16_bits(silu_f32(g) * up * L.wsum[rw]);
+    }
+  }
+}
+
+// Experts in pinned host memory are read by kHostBlocks workgroups, the others
+// stream the device banks beside them. The host link wants long contiguous
+// reads (see ffn_host.hip): an item's 8 gate and 8 up rows are two contiguous
+// blocks, copied in linear order through registers into LDS while the last item
+// is multiplied out of it, instead of 8 rows x 128 bytes per load (one expert
+// of 12.5 MB beside 35 in HBM: 315 us in place, HOST_US us so).
 constexpr int kHostBlocks = 8;
+constexpr int kHostVecs = kMaxH / 2 / 512;  // 16-byte pieces per thread and item
+
+// Multiplies items [g0, g1) (list entries from n_dev on) of host experts; every
+// product and sum as in the device path below, so the bits are the same.
+template <int CPW, int SETS, bool WIDE>
+__device__ void host_gate_up(const FewArgs& a, const Shared& L, int g0, int g1,
+                             const Lane<CPW, WIDE>& ln, const bf16x8 (&xb)[SETS][CPW][4],
+                             int slice, bool active, int ks, float* red, unsigned char* wl,
+                             uint16_t* h) {
+  const int H = a.H, I = a.I, tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int per = I / 8, wrb = H / 2, srb = H / 32;
+  const int half = wrb / 2, shalf = srb / 2;  // pieces of 8 rows of weights, of scales
+  unsigned char* sl = wl + 16 * wrb;          // the 16 rows' scale bytes
+  u32x4 v[kHostVecs], sv;
+  auto issue = [&](int it) {
+    const int li = it / per, i0 = (it - li * per) * 8;
+    const int code = __builtin_amdgcn_readfirstlane(L.row[L.list[li]]);
+    const FewBank& b = code >= 0 ? a.hot : a.cold;
+    const size_t r0 = (size_t)(uint32_t)(code >= 0 ? code : -1 - code) * 2 * I + i0, r1 = r0 + I;
+    const u32x4* wg = reinterpret_cast<const u32x4*>(b.w13 + r0 * wrb);
+    const u32x4* wu = reinterpret_cast<const u32x4*>(b.w13 + r1 * wrb);
+#pragma unroll
+    for (int n = 0; n < kHostVecs; ++n) {
+      const int p = n * kThreads + tid;
+      if (n * kThreads < 2 * half) {  // uniform
+        const int c = min(p, 2 * half - 1);
+        v[n] = c < half ? wg[c] : wu[c - half];
+      }
+    }
+    const int c = min(tid, 2 * shalf - 1);
+    sv = c < shalf ? reinterpret_cast<const u32x4*>(b.s13 + r0 * srb)[c]
+                   : reinterpret_cast<const u32x4*>(b.s13 + r1 * srb)[c - shalf];
+  };
+  issue(g0);
+  for (int it = g0; it < g1; ++it) {
+#pragma unroll
+    for (int n = 0; n < kHostVecs; ++n)
+      if (n * kThreads < 2 * half)
+        *reinterpret_cast<u32x4*>(wl + 16 * min(n * kThreads + tid, 2 * half - 1)) = v[n];
+    *reinterpret_cast<u32x4*>(sl + 16 * min(tid, 2 * shalf - 1)) = sv;
+    if (it + 1 < g1) issue(it + 1);
+    lds_barrier();
+    f32x4 acc[2][SETS];
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < CPW; ++j) {
+      uint4 w[2];
+      float sc[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        w[g] = *reinterpret_cast<const uint4*>(wl + 8 * g * wrb + ln.woff[j]);
+        const int row = (ln.r & 7) + 8 * g, b = (slice * CPW + j) * 8 + ln.piece;
+        const uint32_t e = sl[row * srb + (ln.in[j] ? b : 0)];
+        sc[g] = __uint_as_float((ln.in[j] ? e : 127u) << 23);  // see Lane::scales
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const bf16x8 av = dequant8(word4(w[g], m), sc[g]);
+#pragma unroll
+          for (int st = 0; st < SETS; ++st)
+            acc[g][st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xb[st][j][m], acc[g][st], 0,
+                                                                 0, 0);
+        }
+    }
+    if (active && (ln.r >= 8) == (ln.q >= 2)) {
+      float* o = red + (2 * slice + (ln.r >= 8)) * 64 + (ln.r & 7) * 8 + (ln.q & 1) * 4;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int st = 0; st < SETS; ++st)
+          *reinterpret_cast<f32x4*>(o + (g * SETS + st) * 2 * ks * 64) = acc[g][st];
+    }
+    lds_barrier();  // the item's weights have been read, its partial sums written
+    if (wv == it % kWaves) write_h<SETS>(a, L, it, ks, red + lane, h);
+  }
+}
 
 template <int CPW, int SETS, int R, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
@@ -382,6 +500,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
   const int first = on_host ? n_dev * per : 0;
   const int g0 = first + (int)(n * blk / blocks), g1 = first + (int)(n * (blk + 1) / blocks);
   if (g0 >= g1) return;  // the whole workgroup
+  if (on_host) {
+    unsigned char* wl = reinterpret_cast<unsigned char*>(red) +
+                        (size_t)2 * nsub * 2 * SETS * 2 * ks * 64 * sizeof(float);
+    host_gate_up<CPW, SETS, WIDE>(a, L, g0, g1, ln, xb, slice, active && sub == 0, ks, red, wl, h);
+    return;
+  }
   const int steps = (g1 - g0 + nsub - 1) / nsub;
 
   const size_t wrb = H / 2, srb = H / 32;
@@ -487,30 +611,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
       for (int sb = 0; sb < nsub; ++sb) {
         const int it = g0 + step * nsub + sb;
         if (it >= g1 || (step * nsub + sb) % kWaves != wv) continue;
-        const float* o = red + (size_t)((step & 1) * nsub + sb) * per_sub + lane;
-        const int li = it / per, i0 = (it - li * per) * 8;
-        const int u_ = L.list[li];
-        const int mask = L.mask[u_], base = L.base[u_];
-#pragma unroll
-        for (int st = 0; st < SETS; ++st) {
-          float g = 0.0f, up = 0.0f;
-          auto add = [&](int p) {
-            g += o[(st * 2 * ks + p) * 64];
-            up += o[((SETS + st) * 2 * ks + p) * 64];
-          };
-          if (ks == kWaves) {
-#pragma unroll
-            for (int p = 0; p < 2 * kWaves; ++p) add(p);
-          } else {
-            for (int p = 0; p < 2 * ks; ++p) add(p);
-          }
-          const int t = st * 8 + (lane >> 3);
-          if ((mask >> t) & 1) {
-            const int rw = base + __popc(mask & ((1 << t) - 1));
-            h[(size_t)rw * I + i0 + (lane & 7)] =
-                (uint16_t)f32_to_bf16_bits(silu_f32(g) * up * L.wsum[rw]);
-          }
-        }
+        write_h<SETS>(a, L, it, ks, red + (size_t)((step & 1) * nsub + sb) * per_sub + lane, h);
       }
     }
   }
@@ -704,7 +805,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
 template <int CPW, int SETS, int R, bool WIDE>
 hipError_t go_gate_up(const FewArgs& a, hipStream_t stream) {
   const Cut c = gate_up_cut(a.H);
-  const size_t lds = (size_t)2 * c.sub * 2 * SETS * 2 * c.ks * 64 * sizeof(float);
+  size_t lds = (size_t)2 * c.sub * 2 * SETS * 2 * c.ks * 64 * sizeof(float);
+  if (a.hot.host || a.cold.host) lds += (size_t)16 * (a.H / 2 + a.H / 32);  // an item's weights
   hipLaunchKernelGGL((few_gate_up<CPW, SETS, R, WIDE>), dim3(device_cus()), dim3(kThreads), lds,
                      stream, a);
   return hipGetLastError();

@@ -106,7 +106,9 @@ def test_against_64_bits(T, k, E, H, I, n_cold):
     check(out, ref, bound)
 
 
-@pytest.mark.parametrize("T,k,E,H,I", [(7, 4, 12, 1024, 576), (16, 3, 10, 320, 1088)])
+@pytest.mark.parametrize("T,k,E,H,I", [(7, 4, 12, 1024, 576), (16, 3, 10, 320, 1088),
+                                       (3, 2, 6, 8192, 128), (9, 2, 6, 4160, 256),
+                                       (5, 4, 7, 64, 64), (7, 3, 7, 4096, 2880)])
 def test_bits_do_not_depend_on_the_banks(T, k, E, H, I):
     rm, arr, ids, w, x = make_step(T, k, E, H, I, 4, 5)
     want, _ = run(arr, rm, ids, w, x, H, I)
