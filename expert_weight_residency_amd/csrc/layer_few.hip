@@ -95,11 +95,13 @@ __device__ __forceinline__ void lds_barrier() {
 // chunks and their scale bytes, as loaded (nothing looks at a loaded value
 // before its step: widening a half word at the load would wait for it). Lane l
 // loads scale bytes of row l / 4. WIDE (gate/up, whole slices): 2 CPW
-// consecutive bytes of the slice in one load; otherwise two bytes of each chunk.
+// consecutive bytes of the slice; otherwise the 8 bytes of one chunk (chunk l % 4
+// of the slice), with CPW = 1 the two bytes l % 4 of the one chunk.
 template <int CPW, bool WIDE>
 struct Slot {
+  static constexpr bool kPairs = !WIDE && CPW == 1;
   uint4 w[2][CPW];
-  std::conditional_t<WIDE, uint32_t, uint16_t> s[WIDE ? CPW / 2 : CPW];
+  std::conditional_t<kPairs, uint16_t, uint32_t> s[kPairs ? 1 : (WIDE ? CPW / 2 : 2)];
 };
 
 // The lane's place in the weight rows of a slice: rows of K/2 bytes, K/32
@@ -109,7 +111,8 @@ struct Slot {
 template <int CPW, bool WIDE>
 struct Lane {
   uint32_t woff[CPW];              // weight bytes, within a group of 8 rows
-  uint32_t soff[WIDE ? 1 : CPW];   // scale bytes, within this lane's row
+  uint32_t soff;                   // scale bytes, within this lane's row
+  int sfirst[CPW];                 // a chunk's first scale byte, within the 8 loaded
   bool in[CPW];
   int r, q, srow, piece;
 
@@ -126,13 +129,16 @@ struct Lane {
       woff[j] = (uint32_t)(r & 7) * (uint32_t)(K / 2) + 16u * (uint32_t)(in[j] ? b : 0);
     }
     if constexpr (WIDE) {
-      soff[0] = slice * CPW * 8 + (lane & 3) * 2 * CPW;
+      soff = slice * CPW * 8 + (lane & 3) * 2 * CPW;
+    } else if constexpr (CPW == 1) {
+      const int b = slice * 8 + 2 * (lane & 3);
+      soff = b < nblk ? b : 0;
     } else {
+      // 8 bytes end at the row's end at the latest (rows are longer than 8)
+      auto start = [&](int c) { return min(8 * c, nblk - 8); };
+      soff = start(slice * CPW + min(lane & 3, CPW - 1));
 #pragma unroll
-      for (int j = 0; j < CPW; ++j) {
-        const int b = (slice * CPW + j) * 8 + 2 * (lane & 3);
-        soff[j] = b < nblk ? b : 0;
-      }
+      for (int j = 0; j < CPW; ++j) sfirst[j] = 8 * (slice * CPW + j) - start(slice * CPW + j);
     }
   }
 
@@ -152,16 +158,13 @@ struct Lane {
         o.w[1][j] = *reinterpret_cast<const uint4*>(g1 + woff[j]);
       }
     }
-    if constexpr (!WIDE) {
-#pragma unroll
-      for (int j = 0; j < CPW; ++j) o.s[j] = *reinterpret_cast<const uint16_t*>(sp + soff[j]);
-    } else if constexpr (CPW == 2) {
-      o.s[0] = *reinterpret_cast<const uint32_t*>(sp + soff[0]);
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(sp + soff[0]);
-      o.s[0] = v.x;
-      o.s[1] = v.y;
-    }
+    load_scales(o, sp);
+  }
+  __device__ __forceinline__ void load_scales(Slot<CPW, WIDE>& o, const uint8_t* sp) const {
+    if constexpr (Slot<CPW, WIDE>::kPairs)
+      o.s[0] = *reinterpret_cast<const uint16_t*>(sp + soff);
+    else
+      __builtin_memcpy(o.s, sp + soff, sizeof o.s);  // even addresses; one load
   }
 
   // This lane's scales of group g: the E8M0 byte of its piece of chunk j, of row
@@ -178,25 +181,21 @@ struct Lane {
       const uint32_t e = __builtin_rotateright32(v, (uint32_t)(8 * byte + 9) & 31u);
       return __uint_as_float(ok ? e : 0x3f800000u);
     };
-    if constexpr (WIDE) {
+    if constexpr (Slot<CPW, WIDE>::kPairs) {
+      sc[0] = expo(fetch(row + (piece >> 1), o.s[0]), piece & 1, in[0]);
+    } else {
 #pragma unroll
       for (int j = 0; j < CPW; ++j) {
-        const int b = 8 * j + piece, src = row + b / (2 * CPW), byte = b % (2 * CPW);
+        // WIDE: byte 8j + piece of the slice; else byte sfirst + piece of lane j's 8
+        constexpr int kPer = WIDE ? 2 * CPW : 8;
+        const int b = WIDE ? 8 * j + piece : sfirst[j] + piece;
+        const int src = row + (WIDE ? b / kPer : j), byte = b % kPer;
         uint32_t v = fetch(src, o.s[0]);
-        if constexpr (CPW == 4) {
+        if constexpr (kPer == 8) {
           const uint32_t hi = fetch(src, o.s[1]);
           v = byte >= 4 ? hi : v;
         }
-        sc[j] = expo(v, byte & 3, true);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < CPW; j += 2) {
-        const uint32_t pair =
-            (uint32_t)o.s[j] | (j + 1 < CPW ? (uint32_t)o.s[j + 1 < CPW ? j + 1 : j] << 16 : 0u);
-        const uint32_t v = fetch(row + (piece >> 1), pair);
-        sc[j] = expo(v, piece & 1, in[j]);
-        if (j + 1 < CPW) sc[j + 1] = expo(v, 2 + (piece & 1), in[j + 1 < CPW ? j + 1 : j]);
+        sc[j] = expo(v, byte & 3, in[j]);
       }
     }
   }
@@ -356,7 +355,7 @@ __device__ __forceinline__ void write_h(const FewArgs& a, const Shared& L, int i
 // reads (see ffn_host.hip): an item's 8 gate and 8 up rows are two contiguous
 // blocks, copied in linear order through registers into LDS while the last item
 // is multiplied out of it, instead of 8 rows x 128 bytes per load (one expert
-// of 12.5 MB beside 35 in HBM: 315 us in place, HOST_US us so).
+// of 12.5 MB beside 35 in HBM: 315 us in place, 230 us so).
 constexpr int kHostBlocks = 8;
 constexpr int kHostVecs = kMaxH / 2 / 512;  // 16-byte pieces per thread and item
 
@@ -632,12 +631,20 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
 // their two reads. B operands straight from memory instead of staged rows cost
 // 16 more loads per expert and wavefront (49.4 us at 7 tokens, 112 against 96 at
 // 16).
+//
+// An expert in host memory: a wavefront's slice of 16 rows x CPW lines is loaded
+// in linear order, so that a load reads CPW consecutive lines of a row, and
+// brought into operand order through LDS of the wavefront's own (one such expert
+// beside 35 in HBM: 181 us with the operand order's loads of 8 rows x one line,
+// 163 us so).
 
 constexpr size_t kDownLds = 150 * 1024;  // staged rows and the row of zeros
 
-template <int CPW, int SETS>
+// LINEAR: host experts through LDS, as above.
+template <int CPW, int SETS, bool LINEAR>
 __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows) {
-  extern __shared__ __align__(16) unsigned char hs[];  // [max_rows + 1][512 CPW KS bytes]
+  // [max_rows + 1][512 CPW KS bytes], then if LINEAR per wavefront [16][128 CPW]
+  extern __shared__ __align__(16) unsigned char hs[];
   __shared__ int l_row[kMaxPicks], l_mask[kMaxPicks], l_base[kMaxPicks + 1];
   const int H = a.H, I = a.I, T = a.T;
   const Cut cut = down_cut(I);
@@ -668,6 +675,15 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
   const int o0 = blockIdx.x * 16;
   const size_t wrb = I / 2, srb = I / 32;
   const uint32_t srow_off = (uint32_t)ln.srow * (uint32_t)srb;
+  // the slice's pieces in linear order: piece i = 64 n + lane of 16 rows x 8 CPW
+  unsigned char* own = hs + (size_t)(max_rows + 1) * row_bytes + wv * 2048 * CPW;
+  uint32_t loff[2][CPW];
+#pragma unroll
+  for (int n = 0; n < 2 * CPW; ++n) {
+    const int i = 64 * n + lane, row = i / (8 * CPW);
+    const uint32_t b = 16u * (uint32_t)(slice * CPW * 8 + i % (8 * CPW));
+    loff[n / CPW][n % CPW] = (uint32_t)row * (uint32_t)wrb + (b < wrb ? b : 0u);
+  }
   Slot<CPW, false> next;
   // the expert u's; past the last expert the first rows of a device bank (see
   // few_gate_up)
@@ -679,7 +695,14 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
     const uint8_t* s2 = hot ? a.hot.s2 : a.cold.s2;
     const uint32_t row = live ? (uint32_t)(code >= 0 ? code : -1 - code) : 0u;
     const size_t r0 = (size_t)row * H + (live ? o0 : 0);
-    ln.template load<false>(o, w2 + r0 * wrb, w2 + (r0 + 8) * wrb, s2 + r0 * srb, srow_off);
+    const bool lin = LINEAR && live && (hot ? a.hot.host : a.cold.host);
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+#pragma unroll
+      for (int j = 0; j < CPW; ++j)
+        o.w[g][j] = *reinterpret_cast<const uint4*>(w2 + (r0 + (lin ? 0 : 8 * g)) * wrb +
+                                                    (lin ? loff[g][j] : ln.woff[j]));
+    ln.load_scales(o, s2 + r0 * srb + srow_off);
     __builtin_amdgcn_sched_barrier(0);
   };
   f32x4 acc[2][SETS];
@@ -751,6 +774,20 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
 #pragma unroll
       for (int g = 0; g < 2; ++g) d[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    if constexpr (LINEAR) {
+      const int code = __builtin_amdgcn_readfirstlane(l_row[u]);
+      if (code >= 0 ? a.hot.host : a.cold.host) {
+#pragma unroll
+        for (int n = 0; n < 2 * CPW; ++n)
+          *reinterpret_cast<uint4*>(own + 16 * (64 * n + lane)) = next.w[n / CPW][n % CPW];
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int j = 0; j < CPW; ++j)
+            next.w[g][j] = *reinterpret_cast<const uint4*>(
+                own + 16 * (((ln.r & 7) + 8 * g) * 8 * CPW + 8 * j + ln.piece));
+      }
+    }
     float sc[2][CPW];
     ln.scales(next, 0, sc[0]);
     ln.scales(next, 1, sc[1]);
@@ -817,11 +854,17 @@ hipError_t go_down(const FewArgs& a, hipStream_t stream) {
   const Cut c = down_cut(a.I);
   const int waves = c.ks * c.sub;
   const size_t row = (size_t)512 * CPW * c.ks;
-  const int max_rows = (int)std::min<size_t>(kDownLds / row - 1, (size_t)a.T * a.k);
-  const size_t lds =
-      std::max((size_t)(max_rows + 1) * row, (size_t)waves * 2 * SETS * 8 * 16 * sizeof(float));
-  hipLaunchKernelGGL((few_down<CPW, SETS>), dim3(a.H / 16), dim3(64 * waves), lds, stream, a,
-                     max_rows);
+  // host experts: room for the wavefronts' linear slices, where the h rows of
+  // one expert still fit beside them
+  const size_t own = (size_t)waves * 2048 * CPW;
+  const bool linear = (a.hot.host || a.cold.host) &&
+                      (size_t)(std::min(a.T, MOE_FEW_MAX_TOKENS) + 1) * row + own <= kDownLds;
+  const size_t room = kDownLds - (linear ? own : 0);
+  const int max_rows = (int)std::min<size_t>(room / row - 1, (size_t)a.T * a.k);
+  const size_t lds = std::max((size_t)(max_rows + 1) * row + (linear ? own : 0),
+                              (size_t)waves * 2 * SETS * 8 * 16 * sizeof(float));
+  auto kern = linear ? few_down<CPW, SETS, true> : few_down<CPW, SETS, false>;
+  hipLaunchKernelGGL(kern, dim3(a.H / 16), dim3(64 * waves), lds, stream, a, max_rows);
   return hipGetLastError();
 }
 
