@@ -16,8 +16,9 @@
 //    8 up rows; 16 down rows), so that one expert already spreads over all CUs.
 //  - Each wavefront holds its slice of the activations in registers (gate/up)
 //    or in LDS of its own (down) and streams weights through a register ring
-//    several items ahead, with one barrier per gate/up item for the sum of the
-//    wavefronts' partial results and none until the end in the down kernel.
+//    some items ahead, with one barrier per two gate/up items for the sum of
+//    the wavefronts' partial results (one barrier per item: 170 us instead of
+//    158 at 16 tokens) and none but the staging's in the down kernel.
 //  - A weight load takes 8 rows x one whole 128-byte line (256 elements). Lanes
 //    r < 8 of the MFMA operand hold the first half of row r's line, lanes r >= 8
 //    the second half of row r - 8's; the B operand holds the tokens' first
@@ -442,7 +443,7 @@ __device__ void host_gate_up(const FewArgs& a, const Shared& L, int g0, int g1,
 
 template <int CPW, int SETS, int R, bool WIDE>
 __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
-  extern __shared__ __align__(16) float red[];  // [2][SUB][2 groups][SETS][2 KS][8][8]
+  extern __shared__ __align__(16) float red[];  // [4][SUB][2 groups][SETS][2 KS][8][8]
   __shared__ __align__(16) Shared L;
   const int H = a.H, I = a.I, T = a.T;
   const Cut cut = gate_up_cut(H);
@@ -501,7 +502,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
   if (g0 >= g1) return;  // the whole workgroup
   if (on_host) {
     unsigned char* wl = reinterpret_cast<unsigned char*>(red) +
-                        (size_t)2 * nsub * 2 * SETS * 2 * ks * 64 * sizeof(float);
+                        (size_t)4 * nsub * 2 * SETS * 2 * ks * 64 * sizeof(float);
     host_gate_up<CPW, SETS, WIDE>(a, L, g0, g1, ln, xb, slice, active && sub == 0, ks, red, wl, h);
     return;
   }
@@ -564,53 +565,58 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up(FewArgs a) {
 #pragma unroll
   for (int u = 0; u < R; ++u) issue(ring[u]);
 
-  // Whole turns of the ring (steps past the run's end multiply parked weights
-  // and store nothing): leaving the loop inside a turn made the compiler wait
-  // for nearly every load in flight once per turn.
+  // Whole turns of the ring: leaving the loop inside a turn made the compiler
+  // wait for nearly every load in flight once per turn.
+  static_assert(R % 2 == 0, "steps in pairs");
   for (int s0 = 0; s0 < steps; s0 += R) {
 #pragma unroll
     for (int u = 0; u < R; ++u) {
       const int step = s0 + u;
+      const bool live = step < steps;
       f32x4 acc[2][SETS];
+      if (live) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
-      float sc[2][CPW];
-      ln.scales(ring[u], 0, sc[0]);
-      ln.scales(ring[u], 1, sc[1]);
+          for (int st = 0; st < SETS; ++st) acc[g][st] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float sc[2][CPW];
+        ln.scales(ring[u], 0, sc[0]);
+        ln.scales(ring[u], 1, sc[1]);
 #pragma unroll
-      for (int j = 0; j < CPW; ++j) {
+        for (int j = 0; j < CPW; ++j) {
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+          for (int m = 0; m < 4; ++m)
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const bf16x8 av = dequant8(word4(ring[u].w[g][j], m), sc[g][j]);
+            for (int g = 0; g < 2; ++g) {
+              const bf16x8 av = dequant8(word4(ring[u].w[g][j], m), sc[g][j]);
 #pragma unroll
-            for (int st = 0; st < SETS; ++st)
-              acc[g][st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xb[st][j][m], acc[g][st],
-                                                                   0, 0, 0);
-          }
+              for (int st = 0; st < SETS; ++st)
+                acc[g][st] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av, xb[st][j][m],
+                                                                     acc[g][st], 0, 0, 0);
+            }
+        }
       }
       issue(ring[u]);
       // lane (c, q) holds rows 4q .. 4q+3 of column c: keep the diagonal blocks
-      if (diag) {
-        float* o = red + (size_t)((step & 1) * nsub + sub) * per_sub + red_off;
+      if (live && diag) {
+        float* o = red + (size_t)((step & 3) * nsub + sub) * per_sub + red_off;
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
           for (int st = 0; st < SETS; ++st)
             *reinterpret_cast<f32x4*>(o + (g * SETS + st) * 2 * ks * 64) = acc[g][st];
       }
+      if ((u & 1) == 0 || step - 1 >= steps) continue;
+      // Every second step: one wavefront per item, each in turn, adds the
+      // partial sums (in their order) and writes h; the others go on. A buffer is
+      // written again four steps later, past the next barrier, which that
+      // wavefront reaches only after its reads.
       lds_barrier();
-      // One wavefront per item, each in turn, adds the partial sums (in their
-      // order) and writes h; the others go on. A buffer is written again two
-      // steps later, past the next step's barrier, which that wavefront reaches
-      // only after its reads.
-      for (int sb = 0; sb < nsub; ++sb) {
-        const int it = g0 + step * nsub + sb;
-        if (it >= g1 || (step * nsub + sb) % kWaves != wv) continue;
-        write_h<SETS>(a, L, it, ks, red + (size_t)((step & 1) * nsub + sb) * per_sub + lane, h);
+      for (int n = 0; n < 2 * nsub; ++n) {
+        const int st = step - 1 + (n >= nsub), sb = n >= nsub ? n - nsub : n;
+        const int it = g0 + st * nsub + sb;
+        if (st >= steps || it >= g1 || (it - g0) % kWaves != wv) continue;
+        write_h<SETS>(a, L, it, ks, red + (size_t)((st & 3) * nsub + sb) * per_sub + lane, h);
       }
     }
   }
@@ -842,7 +848,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_down(FewArgs a, int max_rows)
 template <int CPW, int SETS, int R, bool WIDE>
 hipError_t go_gate_up(const FewArgs& a, hipStream_t stream) {
   const Cut c = gate_up_cut(a.H);
-  size_t lds = (size_t)2 * c.sub * 2 * SETS * 2 * c.ks * 64 * sizeof(float);
+  size_t lds = (size_t)4 * c.sub * 2 * SETS * 2 * c.ks * 64 * sizeof(float);
   if (a.hot.host || a.cold.host) lds += (size_t)16 * (a.H / 2 + a.H / 32);  // an item's weights
   hipLaunchKernelGGL((few_gate_up<CPW, SETS, R, WIDE>), dim3(device_cus()), dim3(kThreads), lds,
                      stream, a);
@@ -868,7 +874,8 @@ hipError_t go_down(const FewArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Ring slots: at least 96 KB of weights in flight per CU.
+// R ring slots, 32 CPW KB of weights each and CU. At H = 4096 (CPW = 2), 2 slots
+// take 21.3, 78.4 and 158 us for 1, 7 and 16 tokens, 4 slots 24.2, 83.1 and 154.
 template <int CPW, int R, bool WIDE>
 hipError_t gate_up_sets(const FewArgs& a, hipStream_t s) {
   return a.T <= 8 ? go_gate_up<CPW, 1, R, WIDE>(a, s) : go_gate_up<CPW, 2, R, WIDE>(a, s);
@@ -895,7 +902,7 @@ hipError_t launch_layer_few(const FewArgs& a, hipStream_t s) {
   if (cg.cpw == 1)
     e = gate_up_sets<1, 4, false>(a, s);
   else if (cg.cpw == 2)
-    e = wide ? gate_up_sets<2, 3, true>(a, s) : gate_up_sets<2, 3, false>(a, s);
+    e = wide ? gate_up_sets<2, 2, true>(a, s) : gate_up_sets<2, 2, false>(a, s);
   else
     e = wide ? gate_up_sets<4, 2, true>(a, s) : gate_up_sets<4, 2, false>(a, s);
   if (e != hipSuccess) return e;
