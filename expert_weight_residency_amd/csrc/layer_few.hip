@@ -5,7 +5,7 @@
 //            Wdown[e] . bf16(w[t][e] * silu(Wgate[e] . x[t]) * (Wup[e] . x[t]))
 //
 // The router weight multiplies h before its one rounding to bf16 (the MFMA
-// operand type; an error of at most 2^-9 of each h, as the split path has), so
+// operand type; an error of at most 2^-8 of each h, as the split path has), so
 // that the down products of a token's experts add up in one fp32 accumulator
 // and no row per pick is written: the second kernel ends in `out`.
 //
@@ -15,7 +15,7 @@
 //    elements each), and a work item is only 8 rows of the product (8 gate and
 //    8 up rows; 16 down rows), so that one expert already spreads over all CUs.
 //  - Each wavefront holds its slice of the activations in registers (gate/up)
-//    or in LDS of its own (down) and streams weights through a register ring
+//    or in LDS (down) and streams weights through a register ring
 //    some items ahead, with one barrier per two gate/up items for the sum of
 //    the wavefronts' partial results (one barrier per item: 170 us instead of
 //    158 at 16 tokens) and none but the staging's in the down kernel.

@@ -11,6 +11,11 @@ call may run on a second stream (and, with a stage, its gate/up GEMM beside
 the copy of the down tensors): the calls write disjoint slots, so the result
 does not depend on the overlap. Nothing here computes; it only sequences the
 library's kernels.
+
+Two further forms of the same step: forward_few, the whole layer in two
+launches for at most MOE_FEW_MAX_TOKENS tokens, and forward on a pair of 8-bit
+integer banks (BankI8). route turns router logits into the ids and weights that
+all of them take.
 """
 from __future__ import annotations
 
@@ -18,9 +23,12 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (STAGE_ALL, STAGE_DOWN, STAGE_GATE_UP, Bank, Split, moe_expert_down_mxfp4,
-               moe_expert_ffn_mxfp4, moe_expert_gate_up_mxfp4, moe_ffn_workspace_bytes,
-               moe_finalize, moe_route_split, moe_stage_rows, moe_stage_rows_dma)
+from . import (GATE_NORM_PICKS, MOE_EINVAL, STAGE_ALL, STAGE_DOWN, STAGE_GATE_UP, Bank, BankI8,
+               MoeError, Split, moe_expert_down_mxfp4, moe_expert_ffn_i8, moe_expert_ffn_mxfp4,
+               moe_expert_gate_up_mxfp4, moe_ffn_i8_workspace_bytes, moe_ffn_workspace_bytes,
+               moe_finalize, moe_layer_few_mxfp4, moe_layer_few_workspace_bytes,
+               moe_quantize_rows_i8, moe_route_split, moe_stage_rows, moe_stage_rows_dma,
+               moe_topk_gate)
 
 
 @dataclass
@@ -31,15 +39,23 @@ class LayerBuffers:
     workspace: torch.Tensor
     Y: torch.Tensor
     out: torch.Tensor
+    xq: torch.Tensor | None = None  # 8-bit banks: the step's activations
+    xs: torch.Tensor | None = None  # and their scales
 
     @classmethod
-    def allocate(cls, T: int, k: int, H: int, I: int, n_hot: int, n_cold: int, device="cuda"):
-        ws = max(moe_ffn_workspace_bytes(T, k, H, I), 16)
+    def allocate(cls, T: int, k: int, H: int, I: int, n_hot: int, n_cold: int, device="cuda",
+                 i8: bool = False):
+        """Buffers for steps of T tokens (forward, and forward_few where T allows
+        it); i8: for a pair of BankI8."""
+        ws = moe_ffn_i8_workspace_bytes(T, k, H, I) if i8 else max(
+            moe_ffn_workspace_bytes(T, k, H, I), moe_layer_few_workspace_bytes(T, k, H, I))
         return cls(Split.empty(n_hot, T, k, device), Split.empty(n_cold, T, k, device),
                    torch.zeros(1, dtype=torch.int32, device=device),
-                   torch.empty(ws, dtype=torch.uint8, device=device),
+                   torch.empty(max(ws, 16), dtype=torch.uint8, device=device),
                    torch.empty((max(T * k, 1), H), dtype=torch.int16, device=device),
-                   torch.empty((max(T, 1), H), dtype=torch.int16, device=device))
+                   torch.empty((max(T, 1), H), dtype=torch.int16, device=device),
+                   torch.empty((max(T, 1), H), dtype=torch.int8, device=device) if i8 else None,
+                   torch.empty(max(T, 1), dtype=torch.float32, device=device) if i8 else None)
 
 
 class ColdStage:
@@ -125,8 +141,47 @@ class ResidencyLayer:
                  stage: ColdStage | None = None):
         """With `stage`, the cold bank's active rows are copied to it in one
         contiguous stream per row and the cold FFN reads them from HBM."""
+        self.i8 = isinstance(hot, BankI8)
+        if self.i8 != isinstance(cold, BankI8):
+            raise MoeError(MOE_EINVAL, "hot and cold must be of one kind (Bank or BankI8)")
+        if self.i8 and stage is not None:
+            raise MoeError(MOE_EINVAL, "the cold stage holds MXFP4 rows: none for 8-bit banks")
         self.hot, self.cold, self.row_map, self.H, self.I = hot, cold, row_map, H, I
         self.stage = stage
+
+    def route(self, logits, topk_ids, topk_w, norm: int = GATE_NORM_PICKS, stream=None):
+        """Router logits [T,E] -> topk_ids, topk_w (moe_topk_gate)."""
+        if int(logits.shape[1]) != int(self.row_map.shape[0]):
+            raise MoeError(MOE_EINVAL, f"logits of {int(logits.shape[1])} experts, the row map "
+                                       f"has {int(self.row_map.shape[0])}")
+        moe_topk_gate(logits, topk_ids, topk_w, norm=norm, stream=stream)
+
+    def forward_few(self, x, topk_ids, topk_w, bufs: LayerBuffers, counts_layer=None,
+                    count_tmax: int = 256, stream=None):
+        """forward in two launches (moe_layer_few_mxfp4): the same value within
+        its roundings, not the same bits. Padding tokens may carry ids of -1."""
+        T = int(x.shape[0])
+        moe_layer_few_mxfp4(self.hot, self.cold, self.row_map, x, topk_ids, topk_w, self.I,
+                            bufs.workspace, bufs.out[:T], bufs.n_invalid, counts_layer,
+                            count_tmax, stream=stream)
+        return bufs.out
+
+    def _forward_i8(self, x, topk_w, k, bufs, s, cold_stream, hot_stream):
+        T = int(x.shape[0])
+        xq, xs = bufs.xq[:T], bufs.xs[:T]
+        xb = x.view(torch.bfloat16) if x.dtype == torch.int16 else x
+        moe_quantize_rows_i8(xb, xq, xs, stream=s)
+        side = {id(self.hot): hot_stream, id(self.cold): None if hot_stream else cold_stream}
+        for bank, split in ((self.cold, bufs.cold_split), (self.hot, bufs.hot_split)):
+            on = side[id(bank)] or s
+            if on is not s:
+                on.wait_stream(s)
+            moe_expert_ffn_i8(bank, split, xq, xs, k, self.I, bufs.workspace, bufs.Y, stream=on)
+        for on in side.values():
+            if on is not None:
+                s.wait_stream(on)
+        moe_finalize(bufs.Y, topk_w, bufs.out, stream=s)
+        return bufs.out
 
     def _cold_ffn(self, x, k, bufs, stream, overlap=False):
         return enqueue_cold_ffn(self.cold, bufs.cold_split, x, k, self.H, self.I, bufs,
@@ -144,6 +199,8 @@ class ResidencyLayer:
         s = stream if stream is not None else torch.cuda.current_stream()
         moe_route_split(topk_ids, self.row_map, self.hot.n_rows, self.cold.n_rows, bufs.hot_split,
                         bufs.cold_split, bufs.n_invalid, counts_layer, count_tmax, stream=s)
+        if self.i8:
+            return self._forward_i8(x, topk_w, k, bufs, s, cold_stream, hot_stream)
         if hot_stream is not None:
             hot_stream.wait_stream(s)
             moe_expert_ffn_mxfp4(self.hot, bufs.hot_split, x, k, self.I, bufs.workspace, bufs.Y,

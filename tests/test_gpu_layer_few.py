@@ -244,3 +244,63 @@ def test_two_calls_at_once_on_two_streams():
     torch.cuda.synchronize()
     for _, _, out, _ in calls:
         assert torch.equal(out.cpu().view(torch.int16), want.view(torch.int16))
+
+
+def test_residency_layer_runs_gate_few_and_i8():
+    """ResidencyLayer: router logits through route, then forward_few, forward and
+    (with 8-bit banks) the int8 forward on one or two streams."""
+    from expert_weight_residency_amd.layer import LayerBuffers, ResidencyLayer
+    T, k, E, H, I = 7, 3, 12, 512, 320
+    rm, arr, _, _, x = make_step(T, k, E, H, I, 4, 41)
+    rmd = torch.from_numpy(rm.astype(np.int32)).cuda()
+    logits = torch.randn(T, E, generator=torch.Generator().manual_seed(1))
+    layer = ResidencyLayer(device_bank(arr["hot"]), pinned_bank(arr["cold"]), rmd, H, I)
+    bufs = LayerBuffers.allocate(T, k, H, I, E - 4, 4)
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    xd = x.cuda()
+    layer.route(logits.cuda(), ids, w)
+    layer.forward_few(xd, ids, w, bufs)
+    torch.cuda.synchronize()
+    few = bufs.out[:T].cpu().view(torch.bfloat16)
+    ref, bound, _ = layer_ref.layer(arr, row_of(rm, E - 4, 4), x, ids.cpu(), w.cpu(), H, I)
+    check(few, ref, bound)
+    layer.forward(xd, ids, w, bufs)
+    torch.cuda.synchronize()
+    full = bufs.out[:T].cpu().view(torch.bfloat16).double()
+    assert float((full - few.double()).norm() / full.norm()) <= 2 * REL_L2
+
+    g = torch.Generator().manual_seed(2)
+    rows = {"w13": torch.randint(-127, 128, (E, 2 * I, H), dtype=torch.int8, generator=g),
+            "s13": torch.rand(E, 2 * I, generator=g) / (73 * H ** 0.5),
+            "w2": torch.randint(-127, 128, (E, H, I), dtype=torch.int8, generator=g),
+            "s2": torch.rand(E, H, generator=g) / (73 * I ** 0.5)}
+    # row of an expert in either bank
+    hot = {n: torch.empty_like(v[:E - 4]) for n, v in rows.items()}
+    cold = {n: torch.empty_like(v[:4]).pin_memory() for n, v in rows.items()}
+    for e in range(E):
+        for n in rows:
+            (hot if rm[e] >= 0 else cold)[n][rm[e] if rm[e] >= 0 else -1 - rm[e]] = rows[n][e]
+    mk = lambda b, where, on: moe.BankI8(*(where(b[n]) for n in ("w13", "s13", "w2", "s2")), on)  # noqa: E731
+    i8 = ResidencyLayer(mk(hot, lambda t: t.cuda(), moe.BANK_DEVICE),
+                        mk(cold, lambda t: t, moe.BANK_HOST), rmd, H, I)
+    b8 = LayerBuffers.allocate(T, k, H, I, E - 4, 4, i8=True)
+    outs = []
+    for kw in ({}, {"cold_stream": torch.cuda.Stream()}, {"hot_stream": torch.cuda.Stream()}):
+        b8.out.zero_()
+        i8.forward(xd, ids, w, b8, **kw)
+        torch.cuda.synchronize()
+        outs.append(b8.out[:T].clone())
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    # against the product of the unquantised activations: each of x and h is off
+    # by at most half a step of 1/127 of its row's maximum, about 0.6 % in norm
+    # for these rows (sqrt(1/12) / 127 * max/rms, max/rms below 4), taken four times
+    want = torch.zeros(T, H, dtype=torch.float64)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            gu = (rows["w13"][e].double() * rows["s13"][e].double()[:, None]) @ x[t].double()
+            h = layer_ref.swiglu(gu[:I], gu[I:])
+            want[t] += float(w[t, j]) * (rows["w2"][e].double() * rows["s2"][e].double()[:, None]) @ h
+    got = outs[0].cpu().view(torch.bfloat16).double()
+    assert float((got - want).norm() / want.norm()) <= 4 * 2 ** 0.5 * (1 / 12) ** 0.5 / 127 * 4

@@ -121,3 +121,20 @@ def test_ffn_i8_refusals(L):
     assert call(bank=moe.MoeBankC(0, 0, 0, 0, 0, 0)) == moe.MOE_OK
     assert moe.moe_ffn_i8_workspace_bytes(16, 6, 4096, 2880) == 96 * (2880 * 5 + 4)
     assert moe.moe_ffn_i8_workspace_bytes(16, 0, 4096, 2880) == 0
+
+
+def test_residency_layer_refuses_mixed_and_staged_i8():
+    from expert_weight_residency_amd.layer import ResidencyLayer
+    z = torch.zeros(1, 64, 64, dtype=torch.int8)
+    s = torch.zeros(1, 64)
+    i8 = moe.BankI8(z, s, z, s)
+    u = torch.zeros(1, 64, 64, dtype=torch.uint8)
+    fp4 = moe.Bank(u, u, u, u)
+    rm = torch.zeros(2, dtype=torch.int32)
+    for hot, cold, stage in ((i8, fp4, None), (fp4, i8, None), (i8, i8, object())):
+        with pytest.raises(moe.MoeError) as e:
+            ResidencyLayer(hot, cold, rm, 64, 64, stage=stage)
+        assert e.value.code == moe.MOE_EINVAL
+    layer = ResidencyLayer(fp4, fp4, rm, 64, 64)
+    with pytest.raises(moe.MoeError):
+        layer.route(torch.zeros(1, 3), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 1))
