@@ -490,6 +490,8 @@ def _current(stream):
     dev = torch.cuda.current_device()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise MoeError(MOE_EINVAL, f"stream: of {stream.device}, the current device is cuda:{dev}")
     return dev, _stream(stream)
 
 
@@ -555,7 +557,9 @@ def moe_layer_few_mxfp4(hot: Bank, cold: Bank, row_map, x, topk_ids, topk_w, I: 
                                    f"{tuple(topk_w.shape)}: need [{T}, k] each")
     dev, s = _current(stream)
     _on(dev, x=x, out=out, topk_ids=topk_ids, topk_w=topk_w, row_map=row_map, workspace=workspace,
-        n_invalid=n_invalid, counts_layer=counts_layer, hot_bank=hot.w13, cold_bank=cold.w13)
+        n_invalid=n_invalid, counts_layer=counts_layer)
+    _on(dev, **hot.tensors())
+    _on(dev, **cold.tensors())
     if T > 0:
         _check_bank(hot, H, I, "hot bank")
         _check_bank(cold, H, I, "cold bank")
@@ -645,7 +649,8 @@ def moe_expert_ffn_i8(bank: BankI8, split: Split, xq, xs, k: int, I: int, worksp
     import torch
     T, H = xq.shape
     dev, s = _current(stream)
-    _on(dev, xq=xq, xs=xs, bank=bank.w13, slots=split.slots, workspace=workspace, Y=Y)
+    _on(dev, xq=xq, xs=xs, slots=split.slots, workspace=workspace, Y=Y)
+    _on(dev, **bank.tensors())
     if T > 0 and bank.n_rows > 0:
         R = bank.n_rows
         for name, n in (("w13", R * 2 * I * H), ("s13", R * 2 * I), ("w2", R * H * I),

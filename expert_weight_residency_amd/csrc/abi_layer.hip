@@ -56,7 +56,7 @@ int moe_topk_gate(const void* logits, int dtype, int64_t ld, int T, int E, int k
     return set_error(MOE_EINVAL, "E=%d outside [1, %d]", E, MOE_MAX_EXPERTS);
   if (k < 1 || k > MOE_MAX_TOPK || k > E)
     return set_error(MOE_EINVAL, "k=%d outside [1, min(E=%d, %d)]", k, E, MOE_MAX_TOPK);
-  if ((int64_t)T * k >= (int64_t)1 << 31) return set_error(MOE_EINVAL, "T*k too large");
+  if (T > 1 << 25) return set_error(MOE_EINVAL, "T=%d above 2^25", T);
   if (ld < E || ld > (int64_t)1 << 31)
     return set_error(MOE_EINVAL, "ld=%lld must be in [E=%d, 2^31]", (long long)ld, E);
   if (T == 0) return moe::succeed();
@@ -64,6 +64,10 @@ int moe_topk_gate(const void* logits, int dtype, int64_t ld, int T, int E, int k
     return set_error(MOE_EINVAL, "logits, topk_ids and topk_w must not be NULL");
   if (!aligned(logits, moe::dtype_bytes(dtype)) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
     return set_error(MOE_EINVAL, "logits, topk_ids and topk_w must be aligned to their elements");
+  const size_t in = ((size_t)(T - 1) * ld + E) * moe::dtype_bytes(dtype), ob = (size_t)T * k * 4;
+  if (overlap(topk_ids, ob, logits, in) || overlap(topk_w, ob, logits, in) ||
+      overlap(topk_ids, ob, topk_w, ob))
+    return set_error(MOE_EINVAL, "topk_ids and topk_w must not overlap logits or each other");
   const hipError_t e = moe::launch_topk_gate(logits, dtype, ld, T, E, k, norm, topk_ids, topk_w,
                                              static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return set_error(MOE_EHIP, "gate launch: %s", hipGetErrorString(e));
@@ -100,7 +104,9 @@ int moe_layer_few_mxfp4(const moe_bank* hot, const moe_bank* cold, const int32_t
   if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(out, 16))
     return set_error(MOE_EINVAL, "x, workspace and out must be 16-byte aligned");
   const size_t nb = (size_t)T * H * 2;
-  if (overlap(x, nb, out, nb)) return set_error(MOE_EINVAL, "out must not overlap x");
+  const size_t wb = moe::layer_few_workspace_bytes(T, k, I);
+  if (overlap(x, nb, out, nb) || overlap(x, nb, workspace, wb) || overlap(out, nb, workspace, wb))
+    return set_error(MOE_EINVAL, "x, workspace and out must not overlap");
   moe::FewArgs a = {};
   const size_t align[4] = {16, 16, 16, 16};
   const moe_bank* const src[2] = {hot, cold};
@@ -133,7 +139,8 @@ int moe_layer_few_mxfp4(const moe_bank* hot, const moe_bank* cold, const int32_t
 int moe_quantize_rows_i8(const void* x, int dtype, int64_t ld, int rows, int K, int8_t* q,
                          float* scale, void* stream) {
   if (!moe::dtype_known(dtype)) return set_error(MOE_EINVAL, "dtype=%d unknown", dtype);
-  if (rows < 0) return set_error(MOE_EINVAL, "rows=%d must be >= 0", rows);
+  if (rows < 0 || rows > MOE_I8_MAX_ROWS)
+    return set_error(MOE_EINVAL, "rows=%d outside [0, %d]", rows, MOE_I8_MAX_ROWS);
   if (K < 1 || K > MOE_I8_MAX_K)
     return set_error(MOE_EINVAL, "K=%d outside [1, %d]", K, MOE_I8_MAX_K);
   if (ld < K || ld > (int64_t)1 << 31)
@@ -142,8 +149,10 @@ int moe_quantize_rows_i8(const void* x, int dtype, int64_t ld, int rows, int K, 
   if (!x || !q || !scale) return set_error(MOE_EINVAL, "x, q and scale must not be NULL");
   if (!aligned(x, moe::dtype_bytes(dtype)) || !aligned(scale, 4))
     return set_error(MOE_EINVAL, "x and scale must be aligned to their elements");
-  if (overlap(x, ((size_t)(rows - 1) * ld + K) * moe::dtype_bytes(dtype), q, (size_t)rows * K))
-    return set_error(MOE_EINVAL, "q must not overlap x");
+  const size_t xb = ((size_t)(rows - 1) * ld + K) * moe::dtype_bytes(dtype), qb = (size_t)rows * K;
+  if (overlap(x, xb, q, qb) || overlap(x, xb, scale, (size_t)rows * 4) ||
+      overlap(q, qb, scale, (size_t)rows * 4))
+    return set_error(MOE_EINVAL, "x, q and scale must not overlap");
   const hipError_t e = moe::launch_quantize_rows(x, dtype, ld, rows, K, nullptr, q, scale,
                                                  static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return set_error(MOE_EHIP, "quantize launch: %s", hipGetErrorString(e));
@@ -153,7 +162,8 @@ int moe_quantize_rows_i8(const void* x, int dtype, int64_t ld, int rows, int K, 
 int moe_linear_i8(const int8_t* xq, int64_t ldx, const float* xs, int M, const int8_t* w,
                   const float* ws, int N, int K, void* y, int dtype, int64_t ldy, void* stream) {
   if (!moe::dtype_known(dtype)) return set_error(MOE_EINVAL, "dtype=%d unknown", dtype);
-  if (M < 0 || N < 0) return set_error(MOE_EINVAL, "M=%d and N=%d must be >= 0", M, N);
+  if (M < 0 || N < 0 || M > MOE_I8_MAX_ROWS || N > MOE_I8_MAX_ROWS)
+    return set_error(MOE_EINVAL, "M=%d, N=%d outside [0, %d]", M, N, MOE_I8_MAX_ROWS);
   if (K < 16 || K % 16 || K > MOE_I8_MAX_K)
     return set_error(MOE_EINVAL, "K=%d must be a multiple of 16 in [16, %d]", K, MOE_I8_MAX_K);
   if (ldx < K || ldx % 16 || ldx > (int64_t)1 << 31)
@@ -183,6 +193,8 @@ int moe_linear_i8(const int8_t* xq, int64_t ldx, const float* xs, int M, const i
   a.y = y;
   a.dtype = dtype;
   a.ldy = ldy;
+  if (!moe::gemm_i8_fits(a))
+    return set_error(MOE_ENOTSUP, "M=%d, N=%d: more tiles than one launch takes", M, N);
   const hipError_t e = moe::launch_gemm_i8(a, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return set_error(MOE_EHIP, "8-bit product: %s", hipGetErrorString(e));
   return moe::succeed();
@@ -198,7 +210,8 @@ int moe_expert_ffn_i8(const moe_bank* bank, moe_split split, const int8_t* xq, c
   if (T < 0) return set_error(MOE_EINVAL, "T=%d must be >= 0", T);
   if (k < 1 || k > MOE_MAX_TOPK)
     return set_error(MOE_EINVAL, "k=%d outside [1, %d]", k, MOE_MAX_TOPK);
-  if ((int64_t)T * k > (int64_t)1 << 24) return set_error(MOE_EINVAL, "T*k above 2^24");
+  if ((int64_t)T * k > MOE_I8_MAX_ROWS)
+    return set_error(MOE_EINVAL, "T*k above %d", MOE_I8_MAX_ROWS);
   if (H <= 0 || H % 64 || I <= 0 || I % 64)
     return set_error(MOE_EINVAL, "H=%d, I=%d must be positive multiples of 64", H, I);
   if (H > 32768 || I > 32768)
@@ -243,24 +256,26 @@ int moe_expert_ffn_i8(const moe_bank* bank, moe_split split, const int8_t* xq, c
   a.y = h;
   a.dtype = MOE_DTYPE_F32;
   a.ldy = I;
+  moe::I8Args d = a;  // the down product
+  d.a = hq;
+  d.lda = I;
+  d.sa = hs;
+  d.w = reinterpret_cast<const int8_t*>(p[2]);
+  d.sw = reinterpret_cast<const float*>(p[3]);
+  d.N = H;
+  d.K = I;
+  d.by_token = 0;
+  d.gate_up = 0;
+  d.y = Y;
+  d.dtype = MOE_DTYPE_BF16;
+  d.ldy = H;
+  if (!moe::gemm_i8_fits(a) || !moe::gemm_i8_fits(d))
+    return set_error(MOE_ENOTSUP, "T*k=%zu at H=%d, I=%d: more tiles than one launch takes", slots,
+                     H, I);
   hipError_t e = moe::launch_gemm_i8(a, s);
   if (e == hipSuccess)
     e = moe::launch_quantize_rows(h, MOE_DTYPE_F32, I, (int)slots, I, &split, hq, hs, s);
-  if (e == hipSuccess) {
-    a.a = hq;
-    a.lda = I;
-    a.sa = hs;
-    a.w = reinterpret_cast<const int8_t*>(p[2]);
-    a.sw = reinterpret_cast<const float*>(p[3]);
-    a.N = H;
-    a.K = I;
-    a.by_token = 0;
-    a.gate_up = 0;
-    a.y = Y;
-    a.dtype = MOE_DTYPE_BF16;
-    a.ldy = H;
-    e = moe::launch_gemm_i8(a, s);
-  }
+  if (e == hipSuccess) e = moe::launch_gemm_i8(d, s);
   if (e != hipSuccess) return set_error(MOE_EHIP, "8-bit expert FFN: %s", hipGetErrorString(e));
   return moe::succeed();
 }

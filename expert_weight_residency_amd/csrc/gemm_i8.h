@@ -8,6 +8,7 @@
 namespace moe {
 
 hipError_t launch_gemm_i8_tile(const I8Args& a, hipStream_t stream);
+bool gemm_i8_tile_fits(const I8Args& a);
 hipError_t launch_gemm_i8_stream(const I8Args& a, hipStream_t stream);
 bool gemm_i8_use_stream(const I8Args& a);
 

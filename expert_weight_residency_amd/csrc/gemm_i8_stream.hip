@@ -19,6 +19,11 @@
 // run of items is contiguous over (unit, weight rows), so it reloads the
 // activations and the scales once or twice. A group with more rows takes
 // further units, which stream its weights again.
+//
+// Measured (H 4096, I 2880, 16 tokens of top-6 over 384 experts, about 69 of them
+// met): gate/up 270-278 us, 5.9 TB/s of its 1.63 GB; down, whose 2880-byte rows
+// are not whole lines, 139-142 us, 5.8 TB/s. One row times 5760 x 4096: 11.1 us,
+// 2.1 TB/s, launch and first round trip being half of it.
 #include <algorithm>
 
 #include "gemm_i8.h"
@@ -341,6 +346,8 @@ hipError_t launch_gemm_i8_stream(const I8Args& a, hipStream_t s) {
     default: return pick<8>(a, c, s);
   }
 }
+
+bool gemm_i8_fits(const I8Args& a) { return gemm_i8_use_stream(a) || gemm_i8_tile_fits(a); }
 
 hipError_t launch_gemm_i8(const I8Args& a, hipStream_t s) {
   return gemm_i8_use_stream(a) ? launch_gemm_i8_stream(a, s) : launch_gemm_i8_tile(a, s);

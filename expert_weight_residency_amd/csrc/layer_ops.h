@@ -70,7 +70,9 @@ struct I8Args {
   int dtype;
   int64_t ldy;
 };
-constexpr int kI8MaxK = 131072;  // 128 * 127 * K stays below 2^31
+// Whether the launch stays below 2^32 work items (checked before anything of a
+// call is enqueued).
+bool gemm_i8_fits(const I8Args& a);
 hipError_t launch_gemm_i8(const I8Args& a, hipStream_t stream);
 
 }  // namespace moe

@@ -10,8 +10,10 @@
 //
 // One workgroup per row (a wavefront for rows of at most 512 elements), the row
 // held in registers between the maximum and the rounding (up to 8192 elements;
-// longer rows are read twice, the second time from the L2). Bound by the reads
-// of x: see the figures in the design notes' table.
+// longer rows are read twice, the second time from the L2). Bound by its traffic
+// at prefill sizes (4096 rows of 4096 bf16: 15.5 us, 50 MB at 3.2 TB/s; 24576
+// rows of 2880 fp32: 69 us, 354 MB at 5.1 TB/s), by one round trip to memory for a
+// few rows (3.1 us for one).
 #include "layer_ops.h"
 
 namespace moe {

@@ -23,7 +23,7 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (GATE_NORM_PICKS, MOE_EINVAL, STAGE_ALL, STAGE_DOWN, STAGE_GATE_UP, Bank, BankI8,
+from . import (GATE_NORM_PICKS, MOE_EINVAL, MOE_FEW_MAX_TOKENS, STAGE_ALL, STAGE_DOWN, STAGE_GATE_UP, Bank, BankI8,
                MoeError, Split, moe_expert_down_mxfp4, moe_expert_ffn_i8, moe_expert_ffn_mxfp4,
                moe_expert_gate_up_mxfp4, moe_ffn_i8_workspace_bytes, moe_ffn_workspace_bytes,
                moe_finalize, moe_layer_few_mxfp4, moe_layer_few_workspace_bytes,
@@ -45,10 +45,11 @@ class LayerBuffers:
     @classmethod
     def allocate(cls, T: int, k: int, H: int, I: int, n_hot: int, n_cold: int, device="cuda",
                  i8: bool = False):
-        """Buffers for steps of T tokens (forward, and forward_few where T allows
-        it); i8: for a pair of BankI8."""
+        """Buffers for steps of up to T tokens (forward, and forward_few of as many
+        as it takes); i8: for a pair of BankI8."""
         ws = moe_ffn_i8_workspace_bytes(T, k, H, I) if i8 else max(
-            moe_ffn_workspace_bytes(T, k, H, I), moe_layer_few_workspace_bytes(T, k, H, I))
+            moe_ffn_workspace_bytes(T, k, H, I),
+            moe_layer_few_workspace_bytes(min(T, MOE_FEW_MAX_TOKENS), k, H, I))
         return cls(Split.empty(n_hot, T, k, device), Split.empty(n_cold, T, k, device),
                    torch.zeros(1, dtype=torch.int32, device=device),
                    torch.empty(max(ws, 16), dtype=torch.uint8, device=device),
@@ -168,6 +169,8 @@ class ResidencyLayer:
 
     def _forward_i8(self, x, topk_w, k, bufs, s, cold_stream, hot_stream):
         T = int(x.shape[0])
+        if bufs.xq is None:
+            raise MoeError(MOE_EINVAL, "8-bit banks need LayerBuffers.allocate(..., i8=True)")
         xq, xs = bufs.xq[:T], bufs.xs[:T]
         xb = x.view(torch.bfloat16) if x.dtype == torch.int16 else x
         moe_quantize_rows_i8(xb, xq, xs, stream=s)

@@ -348,14 +348,15 @@ int moe_swap_rows(const moe_bank *hot, const moe_bank *cold, int hot_row, int co
  * topk_ids[t][0 .. k), and their softmax weights into topk_w[t][0 .. k):
  * exp(l - max) over its sum, in fp32. A logit of -inf or NaN masks its expert,
  * which is never picked and has no share. Places for which no expert is left
- * get id -1 and weight 0 (moe_route_split counts such picks as invalid;
- * moe_layer_few_mxfp4 leaves them out of the sum). Where the largest logit is
+ * get id -1 and weight 0 (moe_layer_few_mxfp4 leaves them out of the sum; for
+ * moe_route_split they are invalid picks, whose tokens' output is undefined). Where the largest logit is
  * +inf, the infinite ones share the weight equally.
  *
  * logits: device, element type `dtype`, row t at logits + t * ld elements, ld
  * >= E, aligned to its element size. 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <=
  * min(E, MOE_MAX_TOPK). topk_ids: device int32 [T][k]. topk_w: device fp32
- * [T][k]. Launches one kernel; nothing when T == 0. May be captured.
+ * [T][k]; neither may overlap logits. T <= 2^25. Launches one kernel; nothing
+ * when T == 0. May be captured.
  */
 int moe_topk_gate(const void *logits, int dtype, int64_t ld, int T, int E, int k, int norm,
                   int32_t *topk_ids, float *topk_w, void *stream);
@@ -393,8 +394,8 @@ size_t moe_layer_few_workspace_bytes(int T, int k, int H, int I);
  * device bf16 [T][H]. topk_ids: device int32 [T][k]. topk_w: device fp32
  * [T][k]. n_invalid: device int32 [1]. workspace: device,
  * moe_layer_few_workspace_bytes(T, k, H, I) bytes; calls that overlap need one
- * each. out: device bf16 [T][H]; must not overlap x. x, workspace and out
- * 16-byte aligned. MOE_ENOTSUP past the limits above. Launches nothing, and
+ * each. out: device bf16 [T][H]. x, workspace and out 16-byte aligned, none
+ * overlapping another. MOE_ENOTSUP past the limits above. Launches nothing, and
  * leaves *n_invalid as it was, when T == 0. May be captured.
  */
 int moe_layer_few_mxfp4(const moe_bank *hot, const moe_bank *cold, const int32_t *row_map, int E,
@@ -421,10 +422,13 @@ int moe_layer_few_mxfp4(const moe_bank *hot, const moe_bank *cold, const int32_t
  *
  * x: device, element type dtype, row r at x + r * ld elements, ld >= K, aligned
  * to its element size (rows of whole 16-byte granules are faster). q: device
- * int8 [rows][K]; must not overlap x. scale: device fp32 [rows]. 1 <= K <=
- * MOE_I8_MAX_K. Launches one kernel; nothing when rows == 0. May be captured.
+ * int8 [rows][K]. scale: device fp32 [rows]. x, q and scale must not overlap.
+ * rows <= MOE_I8_MAX_ROWS, 1 <= K <= MOE_I8_MAX_K (up to which a sum of any
+ * 8-bit values stays in int32). Launches one kernel; nothing when rows == 0. May
+ * be captured.
  */
-#define MOE_I8_MAX_K 131072
+#define MOE_I8_MAX_K 131056
+#define MOE_I8_MAX_ROWS (1 << 23)
 int moe_quantize_rows_i8(const void *x, int dtype, int64_t ld, int rows, int K, int8_t *q,
                          float *scale, void *stream);
 
@@ -433,11 +437,12 @@ int moe_quantize_rows_i8(const void *x, int dtype, int64_t ld, int rows, int K, 
  * shared expert, projections).
  *
  * xq: device int8, M rows of K at xq + m * ldx (ldx >= K). xs: device fp32 [M].
- * w: device int8 [N][K] (any values). ws: device fp32 [N]. y: device, element
+ * w: device int8 [N][K]. ws: device fp32 [N]. y: device, element
  * type dtype, row m at y + m * ldy elements (ldy >= N), aligned to its element
  * size; must not overlap the inputs. K and ldx multiples of 16, K <=
- * MOE_I8_MAX_K; xq and w 16-byte aligned. Launches one kernel; nothing when M
- * or N is 0. May be captured.
+ * MOE_I8_MAX_K; M, N <= MOE_I8_MAX_ROWS; xq and w 16-byte aligned. MOE_ENOTSUP
+ * for a product of more tiles than one launch takes (M * N past about 2^35).
+ * Launches one kernel; nothing when M or N is 0. May be captured.
  */
 int moe_linear_i8(const int8_t *xq, int64_t ldx, const float *xs, int M, const int8_t *w,
                   const float *ws, int N, int K, void *y, int dtype, int64_t ldy, void *stream);
@@ -461,7 +466,8 @@ size_t moe_ffn_i8_workspace_bytes(int T, int k, int H, int I);
  * moe_bank (pinned host tensors are read in place). moe_stage_rows,
  * moe_stage_rows_dma and moe_swap_rows move MXFP4 banks only. xq, xs: the
  * step's activations from moe_quantize_rows_i8, int8 [T][H] and fp32 [T]. H
- * and I positive multiples of 64, at most 32768; T * k <= 2^24. workspace:
+ * and I positive multiples of 64, at most 32768; T * k <= MOE_I8_MAX_ROWS
+ * (MOE_ENOTSUP past what one launch takes). workspace:
  * device, moe_ffn_i8_workspace_bytes(T, k, H, I) bytes; both bank calls of one
  * step may share one (each writes only its own slots). Y: device bf16
  * [T*k][H]. xq, workspace and Y 16-byte aligned. Launches three kernels;

@@ -123,7 +123,7 @@ def check_linear(y, xq, xs, w, ws):
 LINEAR = [(1, 1, 16), (1, 7, 32), (1, 5760, 4096), (3, 100, 2880), (8, 64, 1024), (9, 63, 1040),
           (16, 333, 4096), (16, 40, 8192), (2, 24, 8208), (17, 65, 128), (64, 64, 64),
           (100, 130, 272), (257, 511, 1040), (33, 4096, 2880), (1001, 2047, 1040),
-          (4095, 4100, 144), (300, 257, 16), (5, 3, 131072)]
+          (4095, 4100, 144), (300, 257, 16), (5, 3, 131056)]
 
 
 @pytest.mark.parametrize("M,N,K", LINEAR)
@@ -134,7 +134,7 @@ def test_linear(M, N, K):
         moe.moe_linear_i8(xq.cuda(), xs.cuda(), w.cuda(), ws.cuda(), y[:M])
         torch.cuda.synchronize()
         assert (y[M] == 7.0).all()
-        if dtype == torch.float16 and K == 131072:
+        if dtype == torch.float16 and K == 131056:
             continue  # sums past its range
         check_linear(y[:M], xq, xs, w, ws)
 
@@ -152,6 +152,19 @@ def test_linear_strides(M):
         torch.cuda.synchronize()
         check_linear(y, xq, xs, w, ws)
         assert (big[:, :off] == 7.0).all() and (big[:, off + N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_linear_largest_sums(M):
+    """Rows of -128 over the longest axis: sums of 2^31 - 2^18, just inside int32."""
+    N, K = 70, 131056
+    one = torch.ones(max(M, N), device="cuda")
+    xq = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    y = torch.empty(M, N, device="cuda")
+    moe.moe_linear_i8(xq, one[:M], w, one[:N], y)
+    torch.cuda.synchronize()
+    assert (y == float(2 ** 14 * K)).all()  # 2^18 * (2^13 - 1): exact in fp32
 
 
 def test_quantize_then_linear():

@@ -108,7 +108,8 @@ def test_against_64_bits(T, k, E, H, I, n_cold):
 
 @pytest.mark.parametrize("T,k,E,H,I", [(7, 4, 12, 1024, 576), (16, 3, 10, 320, 1088),
                                        (3, 2, 6, 8192, 128), (9, 2, 6, 4160, 256),
-                                       (5, 4, 7, 64, 64), (7, 3, 7, 4096, 2880)])
+                                       (5, 4, 7, 64, 64), (7, 3, 7, 4096, 2880),
+                                       (9, 2, 6, 8192, 64), (16, 3, 6, 64, 4096)])
 def test_bits_do_not_depend_on_the_banks(T, k, E, H, I):
     rm, arr, ids, w, x = make_step(T, k, E, H, I, 4, 5)
     want, _ = run(arr, rm, ids, w, x, H, I)
@@ -304,3 +305,33 @@ def test_residency_layer_runs_gate_few_and_i8():
             want[t] += float(w[t, j]) * (rows["w2"][e].double() * rows["s2"][e].double()[:, None]) @ h
     got = outs[0].cpu().view(torch.bfloat16).double()
     assert float((got - want).norm() / want.norm()) <= 4 * 2 ** 0.5 * (1 / 12) ** 0.5 / 127 * 4
+
+
+def test_every_scale_byte():
+    """Scale bytes 1 .. 252 (products down to the subnormals, up to the type's
+    range): the step's tokens see each byte in both products, the activations
+    and weights scaled so that h and out stay finite."""
+    T, k, H, I = 4, 1, 512, 512
+    for lo, hi in ((1, 40), (100, 150), (215, 252)):
+        E = 4
+        rng = np.random.default_rng(lo)
+        arr = {"hot": {"w13": rng.integers(0, 256, (E, 2 * I, H // 2), dtype=np.uint8),
+                       "s13": rng.integers(lo, hi + 1, (E, 2 * I, H // 32)).astype(np.uint8),
+                       "w2": rng.integers(0, 256, (E, H, I // 2), dtype=np.uint8),
+                       "s2": np.full((E, H, I // 32), 100, np.uint8)}}
+        arr["cold"] = {n: v[:0] for n, v in arr["hot"].items()}
+        # gate and up of order one at most, whatever the bytes
+        x = torch.randn(T, H, generator=torch.Generator().manual_seed(lo))
+        x = (x * 2.0 ** (127 - hi - 8)).to(torch.bfloat16) if hi > 127 else x.to(torch.bfloat16)
+        ids = torch.arange(T, dtype=torch.int32)[:, None]
+        w = torch.ones(T, 1)
+        rm = np.arange(E)
+        out, _ = run(arr, rm, ids, w, x, H, I)
+        ref, bound, _ = layer_ref.layer(arr, row_of(rm, E, 0), x, ids, w, H, I)
+        # tiny h flush nowhere, but bf16 itself ends at 2^-133: half of its last
+        # step for h, times the down row, and for out
+        w2 = torch.stack([layer_ref.mxfp4(arr["hot"]["w2"][e], arr["hot"]["s2"][e]).abs().sum(dim=1)
+                          for e in range(E)])
+        bound = bound + 2.0 ** -133 * w2 + 2.0 ** -133
+        off = (out.double() - ref).abs()
+        assert bool((off <= bound).all()), (lo, float((off / bound).max()))

@@ -20,14 +20,16 @@ def refused(rc, code, text):
 
 
 def test_gate_refusals(L):
-    def call(logits=P, dtype=2, ld=384, T=4, E=384, k=6, norm=0, ids=P, w=P):
+    def call(logits=P, dtype=2, ld=384, T=4, E=384, k=6, norm=0, ids=4 * P, w=8 * P):
         return L.moe_topk_gate(logits, dtype, ld, T, E, k, norm, ids, w, None)
     for kw, text in (({"dtype": 3}, "dtype"), ({"dtype": -1}, "dtype"), ({"norm": 2}, "norm"),
                      ({"T": -1}, "T="), ({"E": 0, "ld": 0}, "E="), ({"E": 4097, "ld": 5000}, "E="),
                      ({"k": 0}, "k="), ({"k": 33}, "k="), ({"E": 4, "k": 5}, "k="),
-                     ({"ld": 383}, "ld="), ({"ld": 2 ** 32}, "ld="), ({"T": 2 ** 30}, "T*k"),
+                     ({"ld": 383}, "ld="), ({"ld": 2 ** 32}, "ld="), ({"T": 2 ** 25 + 1}, "T="),
                      ({"logits": None}, "NULL"), ({"ids": None}, "NULL"), ({"w": None}, "NULL"),
                      ({"logits": P + 2}, "aligned"), ({"ids": P + 2}, "aligned"),
+                     ({"ids": P + 64}, "overlap"), ({"w": P + 6100}, "overlap"),
+                     ({"w": 4 * P + 92}, "overlap"),
                      ({"logits": P + 1, "dtype": 0}, "aligned")):
         refused(call(**kw), moe.MOE_EINVAL, text)
     assert call(T=0, logits=None, ids=None, w=None) == moe.MOE_OK
@@ -39,7 +41,7 @@ def test_few_refusals(L):
         return moe.MoeBankC(p, p, p, p, n, on)
 
     def call(hot=None, cold=None, rm=P, E=8, x=P, ids=P, w=P, T=4, k=2, H=256, I=128, ninv=P,
-             ws=P, out=2 * P, null=False):
+             ws=8 * P, out=2 * P, null=False):
         hot, cold = hot or bank(), cold or bank()
         h = None if null else ctypes.byref(hot)
         return L.moe_layer_few_mxfp4(h, ctypes.byref(cold), rm, E, x, ids, w, T, k, H, I, None,
@@ -52,6 +54,7 @@ def test_few_refusals(L):
                      ({"ninv": None}, "NULL"), ({"ws": None}, "NULL"), ({"out": None}, "NULL"),
                      ({"x": P + 8}, "aligned"), ({"ws": P + 8}, "aligned"),
                      ({"out": P}, "overlap"), ({"out": P + 4 * 256 * 2 - 16}, "overlap"),
+                     ({"ws": P}, "overlap"), ({"ws": 2 * P - 64}, "overlap"),
                      ({"hot": bank(on=3)}, "on_host"), ({"hot": bank(p=0)}, "NULL"),
                      ({"cold": bank(p=P + 8)}, "aligned")):
         refused(call(**kw), moe.MOE_EINVAL, text)
@@ -75,13 +78,14 @@ def test_binding_refuses_host_and_odd_tensors():
 
 
 def test_quantize_refusals(L):
-    def call(x=P, dtype=0, ld=64, rows=4, K=64, q=8 * P, s=P):
+    def call(x=P, dtype=0, ld=64, rows=4, K=64, q=8 * P, s=4 * P):
         return L.moe_quantize_rows_i8(x, dtype, ld, rows, K, q, s, None)
-    for kw, text in (({"dtype": 9}, "dtype"), ({"rows": -1}, "rows"), ({"K": 0, "ld": 0}, "K="),
+    for kw, text in (({"dtype": 9}, "dtype"), ({"rows": -1}, "rows"), ({"rows": 2 ** 23 + 1}, "rows"), ({"K": 0, "ld": 0}, "K="),
                      ({"K": 131073, "ld": 131073}, "K="), ({"ld": 63}, "ld="),
                      ({"x": None}, "NULL"), ({"q": None}, "NULL"), ({"s": None}, "NULL"),
                      ({"x": P + 1}, "aligned"), ({"s": P + 2}, "aligned"),
-                     ({"q": P + 100}, "overlap")):
+                     ({"q": P + 100}, "overlap"), ({"s": P + 8}, "overlap"),
+                     ({"s": 8 * P + 16}, "overlap")):
         refused(call(**kw), moe.MOE_EINVAL, text)
     assert call(rows=0, x=None) == moe.MOE_OK
 
@@ -90,6 +94,7 @@ def test_linear_refusals(L):
     def call(xq=P, ldx=64, xs=P, M=4, w=2 * P, ws=P, N=8, K=64, y=8 * P, dtype=0, ldy=8):
         return L.moe_linear_i8(xq, ldx, xs, M, w, ws, N, K, y, dtype, ldy, None)
     for kw, text in (({"dtype": 3}, "dtype"), ({"M": -1}, "M="), ({"N": -1}, "N="),
+                     ({"M": 2 ** 23 + 1}, "M="), ({"N": 2 ** 23 + 1, "ldy": 2 ** 24}, "N="),
                      ({"K": 0}, "K="), ({"K": 24}, "K="), ({"K": 131088, "ldx": 131088}, "K="),
                      ({"ldx": 48}, "ldx"), ({"ldx": 72}, "ldx"), ({"ldy": 7}, "ldy"),
                      ({"xq": None}, "NULL"), ({"xs": None}, "NULL"), ({"w": None}, "NULL"),
@@ -98,6 +103,8 @@ def test_linear_refusals(L):
                      ({"xs": P + 1}, "aligned"), ({"y": P + 16}, "overlap"),
                      ({"y": 2 * P + 32}, "overlap")):
         refused(call(**kw), moe.MOE_EINVAL, text)
+    refused(call(M=2 ** 21, N=2 ** 21, ldy=2 ** 21, K=16, xq=2 ** 44, w=2 ** 45, y=2 ** 50),
+            moe.MOE_ENOTSUP, "tiles")
     assert call(M=0, xq=None) == moe.MOE_OK and call(N=0, ldy=0, w=None) == moe.MOE_OK
 
 
@@ -108,7 +115,7 @@ def test_ffn_i8_refusals(L):
         return L.moe_expert_ffn_i8(ctypes.byref(bank) if bank else None, sp, xq, xs, T, k, H, I, ws,
                                    Y, None)
     for kw, text in (({"T": -1}, "T="), ({"k": 0}, "k="), ({"k": 33}, "k="),
-                     ({"T": 2 ** 24}, "T*k"), ({"H": 100}, "multiples"), ({"I": 0}, "multiples"),
+                     ({"T": 2 ** 22 + 1}, "T*k"), ({"H": 100}, "multiples"), ({"I": 0}, "multiples"),
                      ({"bank": 0}, "NULL"), ({"bank": moe.MoeBankC(P, P, P, P, 5000, 0)}, "rows"),
                      ({"split": 0}, "split"), ({"xq": None}, "NULL"), ({"xs": None}, "NULL"),
                      ({"ws": None}, "NULL"), ({"Y": None}, "NULL"), ({"xq": P + 8}, "aligned"),
@@ -117,6 +124,7 @@ def test_ffn_i8_refusals(L):
                      ({"bank": moe.MoeBankC(P, P, P, P, 4, 7)}, "on_host")):
         refused(call(**kw), moe.MOE_EINVAL, text)
     refused(call(H=32832), moe.MOE_ENOTSUP, "supported")
+    refused(call(T=2 ** 22, H=32768, I=32768), moe.MOE_ENOTSUP, "tiles")
     assert call(T=0, xq=None) == moe.MOE_OK
     assert call(bank=moe.MoeBankC(0, 0, 0, 0, 0, 0)) == moe.MOE_OK
     assert moe.moe_ffn_i8_workspace_bytes(16, 6, 4096, 2880) == 96 * (2880 * 5 + 4)
@@ -138,3 +146,38 @@ def test_residency_layer_refuses_mixed_and_staged_i8():
     layer = ResidencyLayer(fp4, fp4, rm, 64, 64)
     with pytest.raises(moe.MoeError):
         layer.route(torch.zeros(1, 3), torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 1))
+
+
+def test_tensors_on_another_device_are_refused():
+    class On:  # what the check looks at of a tensor
+        def __init__(self, dev):
+            self.dev = dev
+        is_cuda = True
+        device = "cuda:1"
+
+        def get_device(self):
+            return self.dev
+    moe._on(0, a=On(0), b=None, c=torch.zeros(1))
+    with pytest.raises(moe.MoeError) as e:
+        moe._on(0, a=On(0), b=On(1))
+    assert e.value.code == moe.MOE_EINVAL and "b: on cuda:1" in str(e.value)
+
+
+def test_streams_of_another_device_are_refused(monkeypatch):
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(moe.MoeError) as e:
+        moe._current(Stream())
+    assert e.value.code == moe.MOE_EINVAL and "stream" in str(e.value)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert moe._current(Stream())[0] == 1
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 40, 300])
+def test_buffers_serve_few_token_steps_of_any_size(T):
+    from expert_weight_residency_amd.layer import LayerBuffers
+    k, H, I = 2, 256, 64  # tables larger than a token's h rows
+    bufs = LayerBuffers.allocate(T, k, H, I, 4, 4, device="cpu")
+    for t in range(1, min(T, 16) + 1):
+        assert bufs.workspace.numel() >= moe.moe_layer_few_workspace_bytes(t, k, H, I)
