@@ -490,8 +490,9 @@ def _current(stream):
     dev = torch.cuda.current_device()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
-    if stream.device.index != dev:
-        raise MoeError(MOE_EINVAL, f"stream: of {stream.device}, the current device is cuda:{dev}")
+    on = getattr(stream, "device", None)  # None: a raw handle
+    if on is not None and on.index != dev:
+        raise MoeError(MOE_EINVAL, f"stream: of {on}, the current device is cuda:{dev}")
     return dev, _stream(stream)
 
 

@@ -172,6 +172,7 @@ def test_streams_of_another_device_are_refused(monkeypatch):
     assert e.value.code == moe.MOE_EINVAL and "stream" in str(e.value)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     assert moe._current(Stream())[0] == 1
+    assert moe._current(77) == (1, 77)  # a raw handle
 
 
 @pytest.mark.parametrize("T", [1, 16, 17, 40, 300])
