@@ -434,7 +434,8 @@ hipError_t launch_gemm_i8_tile(const I8Args& a, hipStream_t s) {
   }
   // Smaller ones, us (each with about 6 of launch): 500 x 4096 x 4096 at 128 x
   // 128 with the operands read ahead 19.9, at 128 x 64 23.2, 64 x 64 23.3; 1001 x
-  // 2048 x 1040 10.9, 9.7, 10.7; 112 x 4096 x 2880 at 64 x 64 10.7, at 32 x 64 8.3.
+  // 2048 x 1040 10.9, 9.7, 10.7; 112 x 4096 x 2880 at 64 x 64 10.7, at 32 x 64 8.3
+  // (5, 6 or 8 buffers instead of 4: 8.6, 8.5, 8.8).
   auto tiles = [&](int tn, int tm) {
     return (int64_t)((a.N + tn - 1) / tn) * ((a.M + tm - 1) / tm);
   };
