@@ -8,6 +8,11 @@
 // fused multiply-adds per output starting from +0.0f, one round-to-nearest-even
 // cast, one 16-byte store. The layer is tiny next to the expert FFN; the
 // kernel is bound by reading Y once.
+//
+// A pick of weight 0 adds nothing, whatever its row holds: the rows of invalid
+// picks are written by no bank, and the router's gate leaves such picks (id -1,
+// weight 0) where a token has fewer unmasked experts than k. Stale finite bits
+// are harmless in the chain (0 times them); infinities and NaN are replaced by 0.
 #include "internal.h"
 
 namespace moe {
@@ -27,7 +32,14 @@ __global__ __launch_bounds__(256) void finalize_kernel(const uint16_t* __restric
   for (int j = 0; j < k; ++j) {
     const float wj = w[(int64_t)t * k + j];
     const uint4 v = *reinterpret_cast<const uint4*>(Y + ((int64_t)t * k + j) * H + o);
-    const uint32_t d[4] = {v.x, v.y, v.z, v.w};
+    uint32_t d[4] = {v.x, v.y, v.z, v.w};
+    if (wj == 0.0f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((d[e] & 0x7f80u) == 0x7f80u) d[e] &= 0xffff0000u;
+        if ((d[e] & 0x7f800000u) == 0x7f800000u) d[e] &= 0xffffu;
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       acc[2 * e] = __builtin_fmaf(wj, bf16_bits_to_f32(d[e] & 0xffffu), acc[2 * e]);

@@ -124,8 +124,9 @@ size_t moe_ffn_workspace_bytes(int T, int k, int H, int I);
  * For every pick s = t*k + j with id = topk_ids[s] in [0, E): m = row_map[id];
  * m >= 0 routes the pick to hot row m, m < 0 to cold row -1-m. Picks whose id
  * is outside [0, E) or whose row is outside its bank are routed to neither
- * bank and counted in *n_invalid (the output of that token is then undefined:
- * a caller error). Each bank's output lists its active rows in ascending row
+ * bank and counted in *n_invalid (with a weight other than 0 the output of that
+ * token is then undefined: a caller error; with weight 0 the pick adds nothing,
+ * see moe_finalize). Each bank's output lists its active rows in ascending row
  * order and, per row, its slots in ascending s, so the result is unique.
  * ("vLLM: Pin Hot Experts", section "Results, September 17": split each token's
  * ids by residency; "We Built the Counter", section 2: the split kernel.)
@@ -348,9 +349,10 @@ int moe_swap_rows(const moe_bank *hot, const moe_bank *cold, int hot_row, int co
  * topk_ids[t][0 .. k), and their softmax weights into topk_w[t][0 .. k):
  * exp(l - max) over its sum, in fp32. A logit of -inf or NaN masks its expert,
  * which is never picked and has no share. Places for which no expert is left
- * get id -1 and weight 0 (moe_layer_few_mxfp4 leaves them out of the sum; for
- * moe_route_split they are invalid picks, whose tokens' output is undefined). Where the largest logit is
- * +inf, the infinite ones share the weight equally.
+ * get id -1 and weight 0: both forms of the layer count them as invalid and
+ * leave them out of the sum (moe_layer_few_mxfp4 by the id, moe_finalize by the
+ * weight), and a token with no expert left gets zeros. Where the largest logit
+ * is +inf, the infinite ones share the weight equally.
  *
  * logits: device, element type `dtype`, row t at logits + t * ld elements, ld
  * >= E, aligned to its element size. 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <=

@@ -163,3 +163,100 @@ def test_graph_replays():
         torch.cuda.synchronize()
         wi, ww = gate(l, k, moe.GATE_NORM_PICKS)
         assert np.array_equal(ids.cpu().numpy(), wi) and np.array_equal(w.cpu().double().numpy(), ww)
+
+
+def masked_step(T, E, k, seed):
+    """Logits with every kind of masked row among ordinary ones."""
+    l = torch.randn(T, E, generator=torch.Generator().manual_seed(seed))
+    l[0] = -math.inf               # no expert left
+    l[1, 1:] = math.nan            # one
+    l[T - 2, k - 1:] = -math.inf   # one fewer than the picks
+    return l
+
+
+STALE = [0, 0x7fc1, 0xff80, 0x4228]  # +0, NaN, -inf, 42 (bf16 bits)
+
+
+@pytest.mark.parametrize("T", [5, 40, 300])
+@pytest.mark.parametrize("kind", ["mxfp4", "i8"])
+def test_masked_picks_add_nothing_on_the_split_path(kind, T):
+    """Gate -> split -> expert FFN -> finalize where tokens have fewer unmasked
+    experts than picks: the rows of Y that no bank writes hold what earlier steps
+    left, and the output does not depend on it."""
+    import layer_ref
+    import synth
+    from expert_weight_residency_amd.layer import LayerBuffers, ResidencyLayer
+    from gpu_util import device_bank, host_bank, pinned_bank
+    k, E, H, I = 3, 10, 256, 192
+    rm, ho, co = synth.random_map(E, 4, 3)
+    if kind == "mxfp4":
+        arr = {n: host_bank(o, 3, 0, H, I, scale_lo=118, scale_cnt=4)
+               for n, o in (("hot", ho), ("cold", co))}
+        hot, cold = device_bank(arr["hot"]), pinned_bank(arr["cold"])
+    else:
+        def bank(rows):
+            return moe.BankI8(torch.randint(-127, 128, (rows, 2 * I, H), dtype=torch.int8, generator=g).cuda(),
+                              torch.full((rows, 2 * I), 1 / (73 * H ** 0.5), device="cuda"),
+                              torch.randint(-127, 128, (rows, H, I), dtype=torch.int8, generator=g).cuda(),
+                              torch.full((rows, H), 1 / (73 * I ** 0.5), device="cuda"))
+        g = torch.Generator().manual_seed(4)
+        hot, cold = bank(E - 4), bank(4)
+    x = torch.from_numpy(synth.activations(T, H, 3).view(np.int16)).view(torch.bfloat16)
+    l = masked_step(T, E, k, 5)
+    layer = ResidencyLayer(hot, cold, torch.from_numpy(rm.astype(np.int32)).cuda(), H, I)
+    bufs = LayerBuffers.allocate(T, k, H, I, E - 4, 4, i8=kind == "i8")
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(T, k, device="cuda")
+    layer.route(l.cuda(), ids, w)
+    want = None
+    for bits in STALE:
+        bufs.Y.fill_(bits if bits < 0x8000 else bits - 0x10000)
+        bufs.out.fill_(7)
+        layer.forward(x.cuda(), ids, w, bufs)
+        torch.cuda.synchronize()
+        out = bufs.out[:T].cpu()
+        want = out if want is None else want
+        assert torch.equal(out, want), hex(bits)
+        assert int(bufs.n_invalid) == int((ids < 0).sum()) == k + (k - 1) + 1
+    got = want.view(torch.bfloat16).double()
+    assert (got[0] == 0).all() and got.isfinite().all() and (got[1] != 0).any()
+    if kind == "mxfp4" and T < 256:
+        def row(e):
+            return None if e < 0 else (("hot", int(rm[e])) if rm[e] >= 0 else ("cold", -1 - int(rm[e])))
+        ref, bound, _ = layer_ref.layer(arr, row, x, ids.cpu(), w.cpu(), H, I)
+        # besides the roundings of the bound, each row of Y to bf16: at most
+        # 2^-8 of the row, whose weighted sum over the picks is at most that of
+        # the weights times the largest row
+        rows = bufs.Y[:T * k].cpu().view(torch.bfloat16).double().view(T, k, H).abs()
+        rows = torch.where(ids.cpu()[:, :, None] < 0, 0.0, rows)
+        extra = layer_ref.UBF16 * (1 + layer_ref.UBF16) * (w.cpu().double()[:, :, None] * rows).sum(dim=1)
+        assert bool(((got - ref).abs() <= bound + extra).all())
+
+
+def test_finalize_leaves_out_picks_of_weight_zero():
+    """Bit for bit the chain over the finite rows; rows of infinities and NaN
+    count where their weight is not 0, and only there."""
+    import oracle
+    T, k, H = 9, 5, 264
+    rng = np.random.default_rng(6)
+    Y = oracle.f32_to_bf16(rng.standard_normal((T * k, H)).astype(np.float32))
+    w = rng.random((T, k)).astype(np.float32)
+    special = np.array([0x7f80, 0xff80, 0x7fc0, 0xffff, 0x7f81, 0x8000], np.uint16)
+    for t in range(1, 7):
+        w[t, t % k] = 0.0 if t % 2 else -0.0
+        Y[t * k + t % k] = rng.choice(special, H)
+    w[7, 2] = 0.0                              # a finite row of weight 0
+    Y[8 * k + 1, ::3] = 0x7fc0                 # NaN that counts
+    out = torch.empty(T, H, dtype=torch.int16, device="cuda")
+    moe.moe_finalize(torch.from_numpy(Y.view(np.int16)).cuda(), torch.from_numpy(w).cuda(), out)
+    torch.cuda.synchronize()
+    got = out.cpu().numpy().view(np.uint16)
+    clean = Y.copy()
+    for t in range(1, 7):
+        row = clean[t * k + t % k]
+        row[(row & 0x7f80) == 0x7f80] = 0
+    want = oracle.finalize(clean.reshape(T, k, H), w)
+    assert np.array_equal(got[:8], want[:8])
+    nan = oracle.bf16_to_f32(got[8])
+    assert np.isnan(nan[::3]).all() and np.isfinite(nan[1::3]).all()
+    assert np.array_equal(got[8][1::3], want[8][1::3])
