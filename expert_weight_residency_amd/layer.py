@@ -175,14 +175,17 @@ class ResidencyLayer:
         xq, xs = bufs.xq[:T], bufs.xs[:T]
         xb = x.view(torch.bfloat16) if x.dtype == torch.int16 else x
         moe_quantize_rows_i8(xb, xq, xs, stream=s)
-        side = {id(self.hot): hot_stream, id(self.cold): None if hot_stream else cold_stream}
-        for bank, split in ((self.cold, bufs.cold_split), (self.hot, bufs.hot_split)):
-            on = side[id(bank)] or s
+        cold_on = cold_stream if hot_stream is None and cold_stream is not None else s
+        hot_on = hot_stream if hot_stream is not None else s
+        # the side stream branches off before either bank's kernels
+        for on in (cold_on, hot_on):
             if on is not s:
                 on.wait_stream(s)
+        for bank, split, on in ((self.cold, bufs.cold_split, cold_on),
+                                (self.hot, bufs.hot_split, hot_on)):
             moe_expert_ffn_i8(bank, split, xq, xs, k, self.I, bufs.workspace, bufs.Y, stream=on)
-        for on in side.values():
-            if on is not None:
+        for on in (cold_on, hot_on):
+            if on is not s:
                 s.wait_stream(on)
         moe_finalize(bufs.Y, topk_w, bufs.out, stream=s)
         return bufs.out

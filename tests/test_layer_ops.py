@@ -182,3 +182,58 @@ def test_buffers_serve_few_token_steps_of_any_size(T):
     bufs = LayerBuffers.allocate(T, k, H, I, 4, 4, device="cpu")
     for t in range(1, min(T, 16) + 1):
         assert bufs.workspace.numel() >= moe.moe_layer_few_workspace_bytes(t, k, H, I)
+
+
+class Recorder:
+    """Stands in for the streams and the entry points that ResidencyLayer calls:
+    every operation knows which others it waits for."""
+
+    def __init__(self, monkeypatch):
+        from expert_weight_residency_amd import layer
+        self.after = {}  # operation -> those it follows, directly or not
+        for name in ("moe_route_split", "moe_quantize_rows_i8", "moe_expert_ffn_i8",
+                     "moe_expert_ffn_mxfp4", "moe_finalize"):
+            monkeypatch.setattr(layer, name, lambda *a, _name=name, stream=None, **kw:
+                                self.call(_name, a, stream))
+
+    def call(self, name, args, stream):
+        if name.startswith("moe_expert_ffn"):
+            name = args[0].name
+        self.after[name] = set(stream.done)
+        stream.done.add(name)
+
+    class Stream:
+        def __init__(self):
+            self.done = set()
+
+        def wait_stream(self, other):
+            self.done |= other.done
+
+
+def stub_i8_layer(T, H, I, x_dtype=torch.bfloat16):
+    from expert_weight_residency_amd.layer import LayerBuffers, ResidencyLayer
+
+    def bank(name):
+        b = moe.BankI8(torch.zeros(1, 2 * I, H, dtype=torch.int8), torch.zeros(1, 2 * I),
+                       torch.zeros(1, H, I, dtype=torch.int8), torch.zeros(1, H))
+        b.name = name
+        return b
+    layer = ResidencyLayer(bank("hot"), bank("cold"), torch.tensor([0, -1], dtype=torch.int32), H, I)
+    bufs = LayerBuffers.allocate(T, 1, H, I, 1, 1, device="cpu", i8=True)
+    x = torch.zeros(T, H, dtype=torch.int16).view(x_dtype)
+    return layer, bufs, (x, torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1))
+
+
+@pytest.mark.parametrize("side", [(), ("cold_stream",), ("hot_stream",), ("hot_stream", "cold_stream")])
+def test_i8_banks_run_beside_each_other(monkeypatch, side):
+    """With a side stream neither bank's FFN waits for the other's; both follow
+    the split and the quantisation, and the finalize follows both."""
+    rec = Recorder(monkeypatch)
+    layer, bufs, args = stub_i8_layer(2, 64, 64)
+    s, other = Recorder.Stream(), {n: Recorder.Stream() for n in side}
+    layer.forward(*args, bufs, stream=s, **other)
+    first = {"moe_route_split", "moe_quantize_rows_i8"}
+    assert first <= rec.after["hot"] and first <= rec.after["cold"]
+    assert {"hot", "cold"} <= rec.after["moe_finalize"]
+    if side:
+        assert "cold" not in rec.after["hot"] and "hot" not in rec.after["cold"]
