@@ -173,7 +173,8 @@ class ResidencyLayer:
         if bufs.xq is None:
             raise MoeError(MOE_EINVAL, "8-bit banks need LayerBuffers.allocate(..., i8=True)")
         xq, xs = bufs.xq[:T], bufs.xs[:T]
-        xb = x.view(torch.bfloat16) if x.dtype == torch.int16 else x
+        # bf16 bits in any of the types that the MXFP4 step takes them in
+        xb = x.view(torch.bfloat16) if x.dtype in (torch.int16, torch.uint16) else x
         moe_quantize_rows_i8(xb, xq, xs, stream=s)
         cold_on = cold_stream if hot_stream is None and cold_stream is not None else s
         hot_on = hot_stream if hot_stream is not None else s

@@ -191,6 +191,7 @@ class Recorder:
     def __init__(self, monkeypatch):
         from expert_weight_residency_amd import layer
         self.after = {}  # operation -> those it follows, directly or not
+        self.args = {}
         for name in ("moe_route_split", "moe_quantize_rows_i8", "moe_expert_ffn_i8",
                      "moe_expert_ffn_mxfp4", "moe_finalize"):
             monkeypatch.setattr(layer, name, lambda *a, _name=name, stream=None, **kw:
@@ -199,7 +200,7 @@ class Recorder:
     def call(self, name, args, stream):
         if name.startswith("moe_expert_ffn"):
             name = args[0].name
-        self.after[name] = set(stream.done)
+        self.after[name], self.args[name] = set(stream.done), args
         stream.done.add(name)
 
     class Stream:
@@ -237,3 +238,12 @@ def test_i8_banks_run_beside_each_other(monkeypatch, side):
     assert {"hot", "cold"} <= rec.after["moe_finalize"]
     if side:
         assert "cold" not in rec.after["hot"] and "hot" not in rec.after["cold"]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int16, torch.uint16])
+def test_i8_banks_take_bf16_bits_in_any_type(monkeypatch, dtype):
+    rec = Recorder(monkeypatch)
+    layer, bufs, args = stub_i8_layer(2, 64, 64, dtype)
+    layer.forward(*args, bufs, stream=Recorder.Stream())
+    x = rec.args["moe_quantize_rows_i8"][0]
+    assert x.dtype == torch.bfloat16 and x.data_ptr() == args[0].data_ptr()
