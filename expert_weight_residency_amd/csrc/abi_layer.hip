@@ -272,6 +272,11 @@ int moe_expert_ffn_i8(const moe_bank* bank, moe_split split, const int8_t* xq, c
   if (!moe::gemm_i8_fits(a) || !moe::gemm_i8_fits(d))
     return set_error(MOE_ENOTSUP, "T*k=%zu at H=%d, I=%d: more tiles than one launch takes", slots,
                      H, I);
+  const size_t wb = moe_ffn_i8_workspace_bytes(T, k, H, I), yb = slots * H * 2;
+  if (overlap(Y, yb, workspace, wb) || overlap(Y, yb, xq, (size_t)T * H) ||
+      overlap(Y, yb, xs, (size_t)T * 4) || overlap(workspace, wb, xq, (size_t)T * H) ||
+      overlap(workspace, wb, xs, (size_t)T * 4))
+    return set_error(MOE_EINVAL, "workspace and Y must not overlap xq, xs or each other");
   hipError_t e = moe::launch_gemm_i8(a, s);
   if (e == hipSuccess)
     e = moe::launch_quantize_rows(h, MOE_DTYPE_F32, I, (int)slots, I, &split, hq, hs, s);

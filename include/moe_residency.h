@@ -472,8 +472,9 @@ size_t moe_ffn_i8_workspace_bytes(int T, int k, int H, int I);
  * (MOE_ENOTSUP past what one launch takes). workspace:
  * device, moe_ffn_i8_workspace_bytes(T, k, H, I) bytes; both bank calls of one
  * step may share one (each writes only its own slots). Y: device bf16
- * [T*k][H]. xq, workspace and Y 16-byte aligned. Launches three kernels;
- * nothing when T == 0 or the bank has no rows. May be captured.
+ * [T*k][H]. xq, workspace and Y 16-byte aligned; workspace and Y overlap neither
+ * each other nor xq or xs. Launches three kernels; nothing when T == 0 or the
+ * bank has no rows. May be captured.
  */
 int moe_expert_ffn_i8(const moe_bank *bank, moe_split split, const int8_t *xq, const float *xs,
                       int T, int k, int H, int I, void *workspace, uint16_t *Y, void *stream);

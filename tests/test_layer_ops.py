@@ -247,3 +247,16 @@ def test_i8_banks_take_bf16_bits_in_any_type(monkeypatch, dtype):
     layer.forward(*args, bufs, stream=Recorder.Stream())
     x = rec.args["moe_quantize_rows_i8"][0]
     assert x.dtype == torch.bfloat16 and x.data_ptr() == args[0].data_ptr()
+
+
+def test_ffn_i8_refuses_overlapping_buffers(L):
+    T, k, H, I = 4, 2, 256, 128
+    n = {"xq": T * H, "xs": 4 * T, "ws": moe.moe_ffn_i8_workspace_bytes(T, k, H, I), "Y": 2 * T * k * H}
+    bank, split = moe.MoeBankC(P, P, P, P, 4, 0), moe.MoeSplitC(P, P, P, P)
+    for a, b in (("Y", "ws"), ("Y", "xq"), ("Y", "xs"), ("ws", "xq"), ("ws", "xs")):
+        at = {"xq": 2 * P, "xs": 4 * P, "ws": 8 * P, "Y": 16 * P}
+        for shift in (0, n[b] - 16, -(n[a] - 16)):  # the same place, the last and first bytes shared
+            at[a] = at[b] + shift // 16 * 16
+            rc = L.moe_expert_ffn_i8(ctypes.byref(bank), split, at["xq"], at["xs"], T, k, H, I, at["ws"],
+                                     at["Y"], None)
+            refused(rc, moe.MOE_EINVAL, "overlap")
