@@ -118,6 +118,28 @@ int moe_layer_few_mxfp4(const moe_bank* hot, const moe_bank* cold, const int32_t
     if (rc != MOE_OK) return rc;
     *dst[i] = {p[0], p[1], p[2], p[3], src[i]->n_rows, src[i]->on_host != MOE_BANK_DEVICE};
   }
+  // every workgroup reads the step's tables while another may write already
+  if (!aligned(row_map, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
+      !aligned(n_invalid, 4) || !aligned(counts_layer, 4))
+    return set_error(MOE_EINVAL, "row_map, topk_ids, topk_w, counts_layer and n_invalid must be "
+                                 "aligned to their elements");
+  const size_t pb = (size_t)T * k * 4, eb = (size_t)E * 4;
+  const struct {
+    const void* p;
+    size_t n;
+  } read[] = {{row_map, eb}, {topk_ids, pb}, {topk_w, pb}, {x, nb}},
+    written[] = {{workspace, wb}, {out, nb}, {n_invalid, 4}, {counts_layer, counts_layer ? eb : 0}};
+  for (const auto& w : written) {
+    if (w.n == 0) continue;
+    for (const auto& r : read)
+      if (overlap(w.p, w.n, r.p, r.n))
+        return set_error(MOE_EINVAL, "workspace, out, n_invalid and counts_layer must not overlap "
+                                     "row_map, topk_ids, topk_w or x");
+    for (const auto& v : written)
+      if (&v < &w && v.n != 0 && overlap(w.p, w.n, v.p, v.n))
+        return set_error(MOE_EINVAL, "workspace, out, n_invalid and counts_layer must not overlap "
+                                     "each other");
+  }
   a.row_map = row_map;
   a.x = x;
   a.ids = topk_ids;

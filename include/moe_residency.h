@@ -396,9 +396,11 @@ size_t moe_layer_few_workspace_bytes(int T, int k, int H, int I);
  * device bf16 [T][H]. topk_ids: device int32 [T][k]. topk_w: device fp32
  * [T][k]. n_invalid: device int32 [1]. workspace: device,
  * moe_layer_few_workspace_bytes(T, k, H, I) bytes; calls that overlap need one
- * each. out: device bf16 [T][H]. x, workspace and out 16-byte aligned, none
- * overlapping another. MOE_ENOTSUP past the limits above. Launches nothing, and
- * leaves *n_invalid as it was, when T == 0. May be captured.
+ * each. out: device bf16 [T][H]. x, workspace and out 16-byte aligned, the
+ * other arrays aligned to their elements; workspace, out, n_invalid and
+ * counts_layer overlap neither each other nor row_map, topk_ids, topk_w or x.
+ * MOE_ENOTSUP past the limits above. Launches nothing, and leaves *n_invalid as
+ * it was, when T == 0. May be captured.
  */
 int moe_layer_few_mxfp4(const moe_bank *hot, const moe_bank *cold, const int32_t *row_map, int E,
                         const uint16_t *x, const int32_t *topk_ids, const float *topk_w, int T,

@@ -260,3 +260,23 @@ def test_ffn_i8_refuses_overlapping_buffers(L):
             rc = L.moe_expert_ffn_i8(ctypes.byref(bank), split, at["xq"], at["xs"], T, k, H, I, at["ws"],
                                      at["Y"], None)
             refused(rc, moe.MOE_EINVAL, "overlap")
+
+
+def test_few_refuses_misaligned_and_overlapping_arrays(L):
+    T, k, E, H, I = 4, 2, 8, 256, 128
+    n = {"rm": 4 * E, "ids": 4 * T * k, "w": 4 * T * k, "x": 2 * T * H, "ninv": 4, "counts": 4 * E,
+         "ws": moe.moe_layer_few_workspace_bytes(T, k, H, I), "out": 2 * T * H}
+    bank = moe.MoeBankC(P, P, P, P, 4, 0)
+
+    def call(**move):
+        at = {**{name: (2 + 2 * i) * P for i, name in enumerate(n)}, **move}
+        return L.moe_layer_few_mxfp4(ctypes.byref(bank), ctypes.byref(bank), at["rm"], E, at["x"], at["ids"],
+                                     at["w"], T, k, H, I, at["counts"], 256, at["ninv"], at["ws"], at["out"],
+                                     None)
+    for name in ("rm", "ids", "w", "ninv", "counts"):
+        refused(call(**{name: 64 * P + 2}), moe.MOE_EINVAL, "aligned")
+    for a in ("ninv", "counts", "ws", "out"):
+        for b in n:
+            if a != b:
+                for at in (64 * P, 64 * P + (n[b] - 1) // 16 * 16, 64 * P - (n[a] - 1) // 16 * 16):
+                    refused(call(**{a: at, b: 64 * P}), moe.MOE_EINVAL, "overlap")
