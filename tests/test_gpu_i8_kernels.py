@@ -1,0 +1,136 @@
+"""Every kernel instance behind the 8-bit products, at ragged sizes with enough
+steps to turn its buffers over: the dense product and the expert FFN against
+exact integer sums in 64 bits, and that the sizes here reach every instance the
+library holds (a moved threshold must not leave one untested)."""
+import re
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import expert_weight_residency_amd as moe
+from layer_ref import HALF_STEP, U32
+from test_gpu_i8 import check_ffn, make_bank, run_ffn, bank_on
+
+pytestmark = pytest.mark.gpu
+
+# Tiles. 128-byte steps of K that are no multiple of the buffers, a part-filled
+# last step, part-filled last tiles, a last group of fewer than 8 rows of tiles.
+TILES = {
+    (5043, 6300, 528): "big<256, 256, 2>",
+    (4096, 4095, 1040): "big<256, 256, 2>",
+    (5043, 3300, 656): "big<192, 256, 2>",
+    (4000, 5700, 912): "big<192, 256, 2>",
+    (5043, 3137, 1168): "big<128, 256, 3>",
+    (500, 4096, 4096): "big<128, 128, 3>",
+    (385, 4100, 2064): "big<128, 128, 3>",
+    (1200, 1700, 2192): "big<128, 128, 3>",
+    (1001, 2047, 1040): "tile<128, 64, 4, 2, 3, false>",
+    (700, 1600, 1168): "tile<64, 64, 2, 2, 3, false>",
+    (641, 1665, 400): "tile<64, 64, 2, 2, 3, false>",
+    (112, 1000, 2896): "tile<32, 64, 2, 2, 4, false>",
+    (17, 63, 9232): "tile<32, 64, 2, 2, 4, false>",
+}
+# Few rows: chunks of 128 bytes per wavefront, K of whole lines and not.
+CHUNKS = {1: (1024, 1008), 2: (2048, 1936), 3: (2944, 2896), 4: (4096, 4080), 6: (5120, 5136),
+          8: (8192, 7056)}
+STREAM = {(M, 45, K): f"stream<{cpw}, {1 if M <= 8 else 2}, false, {'false' if i else 'true'}>"
+          for cpw, Ks in CHUNKS.items() for i, K in enumerate(Ks) for M in (1, 7, 12)}
+# Expert FFN, gate/up (K = H) and down (K = I): T, k, E, H, I
+FFN = {(4, 2, 3, H, 192): f"stream<{cpw}, 1, true, {'false' if H % 128 else 'true'}>"
+       for cpw, H in ((1, 1024), (1, 960), (2, 2048), (2, 1984), (3, 2944), (3, 2880), (4, 4096),
+                      (4, 4032), (6, 5120), (6, 5184), (8, 8192), (8, 7104))}
+FFN.update({(3, 2, 3, 128, 5184): "stream<6, 1, false, false>",
+            (90, 3, 5, 1088, 320): "tile<128, 64, 4, 2, 3, true>",
+            (90, 3, 5, 320, 1088): "tile<128, 64, 4, 2, 3, false>"})
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    moe.lib()
+    yield
+
+
+def instances(text):
+    return set(re.findall(r"gemm_i8_(\w+<[^>]*>)", text))
+
+
+def launched(f):
+    """The instances that f launches."""
+    from torch.profiler import ProfilerActivity, profile
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CUDA], acc_events=True) as p:
+        f()
+        torch.cuda.synchronize()
+    return instances("\n".join(e.key for e in p.key_averages()))
+
+
+def linear(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M * 7 + N * 3 + K)
+    xq = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    w = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    xq[0], w[N - 1] = 127, -128
+    xs = torch.rand(M, device="cuda", generator=g) + 0.01
+    ws = torch.rand(N, device="cuda", generator=g) / (73 * K ** 0.5)
+    return xq, xs, w, ws
+
+
+@pytest.mark.parametrize("M,N,K", list(TILES) + list(STREAM))
+def test_dense(M, N, K):
+    xq, xs, w, ws = linear(M, N, K)
+    # sums of integers below 2^53: exact in any order
+    ref = (xq.double() @ w.double().T.contiguous()) * xs.double()[:, None] * ws.double()
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        y = torch.full((M + 1, N), 7.0, dtype=dtype, device="cuda")
+        moe.moe_linear_i8(xq, xs, w, ws, y[:M])
+        torch.cuda.synchronize()
+        assert (y[M] == 7.0).all()
+        # the sum to fp32, two products, the type's rounding (and fp16's subnormals)
+        tol = (3.1 * U32 + HALF_STEP[dtype]) * ref.abs() + (2.0 ** -25 if dtype == torch.float16
+                                                           else 2.0 ** -140)
+        off = (y[:M].double() - ref).abs()
+        assert bool((off <= tol).all()), (dtype, float((off / tol).max()))
+
+
+def ffn_step(T, k, E, H, I):
+    b = make_bank(E, H, I, T + E + H)
+    g = torch.Generator().manual_seed(H + I)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16)
+    return b, ids, x
+
+
+def run(b, ids, x, H, I):
+    none = {n: v[:0] for n, v in b.items()}
+    return run_ffn(bank_on(b, "device"), bank_on(none, "device"), np.arange(len(b["s2"])), ids, x, H, I)
+
+
+@pytest.mark.parametrize("T,k,E,H,I", list(FFN))
+def test_expert_ffn(T, k, E, H, I):
+    b, ids, x = ffn_step(T, k, E, H, I)
+    check_ffn(run(b, ids, x, H, I), b, ids, x, H, I)
+
+
+def test_the_sizes_reach_every_instance():
+    """Which instance a size selects is the dispatch rules' choice on a card of
+    256 CUs."""
+    assert torch.cuda.get_device_properties(0).multi_processor_count == 256
+    nm = shutil.which("nm")
+    assert nm, "nm lists the library's kernels"
+    held = instances(subprocess.run([nm, "-C", moe.LIB_PATH], capture_output=True, text=True,
+                                    check=True).stdout)
+    reached = set()
+    for (M, N, K), want in {**TILES, **STREAM}.items():
+        xq, xs, w, ws = linear(M, N, K)
+        y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        got = launched(lambda: moe.moe_linear_i8(xq, xs, w, ws, y))
+        assert got == {want}, (M, N, K, got)
+        reached |= got
+    for shape, want in FFN.items():
+        got = launched(lambda: run(*ffn_step(*shape), *shape[3:]))
+        assert want in got and len(got) == 2, (shape, got)
+        reached |= got
+    assert reached == held, held ^ reached
