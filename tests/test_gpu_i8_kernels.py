@@ -2,49 +2,48 @@
 steps to turn its buffers over: the dense product and the expert FFN against
 exact integer sums in 64 bits, and that the sizes here reach every instance the
 library holds (a moved threshold must not leave one untested)."""
-import re
-import shutil
-import subprocess
-
 import numpy as np
 import pytest
 import torch
 
 import expert_weight_residency_amd as moe
+from kernel_instances import held, launched
 from layer_ref import HALF_STEP, U32
 from test_gpu_i8 import check_ffn, make_bank, run_ffn, bank_on
 
 pytestmark = pytest.mark.gpu
 
+KERNELS = "gemm_i8_[a-z]+"
+
 # Tiles. 128-byte steps of K that are no multiple of the buffers, a part-filled
 # last step, part-filled last tiles, a last group of fewer than 8 rows of tiles.
 TILES = {
-    (5043, 6300, 528): "big<256, 256, 2>",
-    (4096, 4095, 1040): "big<256, 256, 2>",
-    (5043, 3300, 656): "big<192, 256, 2>",
-    (4000, 5700, 912): "big<192, 256, 2>",
-    (5043, 3137, 1168): "big<128, 256, 3>",
-    (500, 4096, 4096): "big<128, 128, 3>",
-    (385, 4100, 2064): "big<128, 128, 3>",
-    (1200, 1700, 2192): "big<128, 128, 3>",
-    (1001, 2047, 1040): "tile<128, 64, 4, 2, 3, false>",
-    (700, 1600, 1168): "tile<64, 64, 2, 2, 3, false>",
-    (641, 1665, 400): "tile<64, 64, 2, 2, 3, false>",
-    (112, 1000, 2896): "tile<32, 64, 2, 2, 4, false>",
-    (17, 63, 9232): "tile<32, 64, 2, 2, 4, false>",
+    (5043, 6300, 528): "gemm_i8_big<256, 256, 2>",
+    (4096, 4095, 1040): "gemm_i8_big<256, 256, 2>",
+    (5043, 3300, 656): "gemm_i8_big<192, 256, 2>",
+    (4000, 5700, 912): "gemm_i8_big<192, 256, 2>",
+    (5043, 3137, 1168): "gemm_i8_big<128, 256, 3>",
+    (500, 4096, 4096): "gemm_i8_big<128, 128, 3>",
+    (385, 4100, 2064): "gemm_i8_big<128, 128, 3>",
+    (1200, 1700, 2192): "gemm_i8_big<128, 128, 3>",
+    (1001, 2047, 1040): "gemm_i8_tile<128, 64, 4, 2, 3, false>",
+    (700, 1600, 1168): "gemm_i8_tile<64, 64, 2, 2, 3, false>",
+    (641, 1665, 400): "gemm_i8_tile<64, 64, 2, 2, 3, false>",
+    (112, 1000, 2896): "gemm_i8_tile<32, 64, 2, 2, 4, false>",
+    (17, 63, 9232): "gemm_i8_tile<32, 64, 2, 2, 4, false>",
 }
 # Few rows: chunks of 128 bytes per wavefront, K of whole lines and not.
 CHUNKS = {1: (1024, 1008), 2: (2048, 1936), 3: (2944, 2896), 4: (4096, 4080), 6: (5120, 5136),
           8: (8192, 7056)}
-STREAM = {(M, 45, K): f"stream<{cpw}, {1 if M <= 8 else 2}, false, {'false' if i else 'true'}>"
+STREAM = {(M, 45, K): f"gemm_i8_stream<{cpw}, {1 if M <= 8 else 2}, false, {'false' if i else 'true'}>"
           for cpw, Ks in CHUNKS.items() for i, K in enumerate(Ks) for M in (1, 7, 12)}
 # Expert FFN, gate/up (K = H) and down (K = I): T, k, E, H, I
-FFN = {(4, 2, 3, H, 192): f"stream<{cpw}, 1, true, {'false' if H % 128 else 'true'}>"
+FFN = {(4, 2, 3, H, 192): f"gemm_i8_stream<{cpw}, 1, true, {'false' if H % 128 else 'true'}>"
        for cpw, H in ((1, 1024), (1, 960), (2, 2048), (2, 1984), (3, 2944), (3, 2880), (4, 4096),
                       (4, 4032), (6, 5120), (6, 5184), (8, 8192), (8, 7104))}
-FFN.update({(3, 2, 3, 128, 5184): "stream<6, 1, false, false>",
-            (90, 3, 5, 1088, 320): "tile<128, 64, 4, 2, 3, true>",
-            (90, 3, 5, 320, 1088): "tile<128, 64, 4, 2, 3, false>"})
+FFN.update({(3, 2, 3, 128, 5184): "gemm_i8_stream<6, 1, false, false>",
+            (90, 3, 5, 1088, 320): "gemm_i8_tile<128, 64, 4, 2, 3, true>",
+            (90, 3, 5, 320, 1088): "gemm_i8_tile<128, 64, 4, 2, 3, false>"})
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -52,20 +51,6 @@ def gpu():
     assert torch.cuda.is_available(), "GPU tests need a GPU"
     moe.lib()
     yield
-
-
-def instances(text):
-    return set(re.findall(r"gemm_i8_(\w+<[^>]*>)", text))
-
-
-def launched(f):
-    """The instances that f launches."""
-    from torch.profiler import ProfilerActivity, profile
-    torch.cuda.synchronize()
-    with profile(activities=[ProfilerActivity.CUDA], acc_events=True) as p:
-        f()
-        torch.cuda.synchronize()
-    return instances("\n".join(e.key for e in p.key_averages()))
 
 
 def linear(M, N, K):
@@ -118,19 +103,15 @@ def test_the_sizes_reach_every_instance():
     """Which instance a size selects is the dispatch rules' choice on a card of
     256 CUs."""
     assert torch.cuda.get_device_properties(0).multi_processor_count == 256
-    nm = shutil.which("nm")
-    assert nm, "nm lists the library's kernels"
-    held = instances(subprocess.run([nm, "-C", moe.LIB_PATH], capture_output=True, text=True,
-                                    check=True).stdout)
     reached = set()
     for (M, N, K), want in {**TILES, **STREAM}.items():
         xq, xs, w, ws = linear(M, N, K)
         y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
-        got = launched(lambda: moe.moe_linear_i8(xq, xs, w, ws, y))
+        got = launched(lambda: moe.moe_linear_i8(xq, xs, w, ws, y), KERNELS)
         assert got == {want}, (M, N, K, got)
         reached |= got
     for shape, want in FFN.items():
-        got = launched(lambda: run(*ffn_step(*shape), *shape[3:]))
+        got = launched(lambda: run(*ffn_step(*shape), *shape[3:]), KERNELS)
         assert want in got and len(got) == 2, (shape, got)
         reached |= got
-    assert reached == held, held ^ reached
+    assert reached == held(KERNELS), held(KERNELS) ^ reached
