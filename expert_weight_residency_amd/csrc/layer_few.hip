@@ -170,9 +170,9 @@ struct Lane {
 
   // This lane's scales of group g: the E8M0 byte of its piece of chunk j, of row
   // (r & 7) + 8g, turned into the exponent field of the conversion's fp32 scale
-  // operand. The instruction reads that field only (checked for all 256 bytes
-  // and any sign and mantissa: the same results as the exact power of two, its
-  // subnormal and NaN included), so a rotation replaces e8m0_to_f32's selects.
+  // operand. The instruction reads that field only (the tests run bytes 0 .. 254
+  // through both products with other bytes beside them, and NaN's), so a rotation
+  // replaces e8m0_to_f32's selects.
   __device__ __forceinline__ void scales(const Slot<CPW, WIDE>& o, int g, float (&sc)[CPW]) const {
     const int row = 32 * g + 4 * (r & 7);
     auto fetch = [&](int src, uint32_t v) {

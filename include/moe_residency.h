@@ -379,11 +379,12 @@ size_t moe_layer_few_workspace_bytes(int T, int k, int H, int I);
  *
  * out[t] = bf16( sum over j of topk_w[t][j] * y(t, topk_ids[t][j]) ), with y
  * as in moe_expert_ffn_mxfp4. The router weight multiplies the SwiGLU output
- * before that is rounded to bf16, and the down products of a token's experts
- * are summed in fp32 and rounded once, so the result is as accurate as that of
- * moe_route_split, moe_expert_ffn_mxfp4 on both banks and moe_finalize, but
- * not the same bits. Every sum has one order, given by the shapes and the order
- * of the picks, so the bits do not depend on which bank holds an expert (a
+ * before that is rounded to bf16 (the weighted value has to stay in that type's
+ * range), and the down products of a token's experts are summed in fp32 and
+ * rounded once, so the result is as accurate as that of moe_route_split,
+ * moe_expert_ffn_mxfp4 on both banks and moe_finalize, but not the same bits.
+ * Every sum has one order, given by the shapes and the order of the picks, so
+ * the bits do not depend on which bank holds an expert (a
  * swap between steps, or an all-hot run, changes nothing).
  *
  * A pick whose id is outside [0, E) or whose row is outside its bank adds
