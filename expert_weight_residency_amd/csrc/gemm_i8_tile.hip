@@ -50,8 +50,6 @@ constexpr int vm_lds(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
     __builtin_amdgcn_sched_barrier(0);                     \
   } while (0)
 
-
-// TN x TM tile (weight rows x activation rows), WN x WM wavefronts.
 // Workgroups go round the 8 XCDs in turn, each with its own L2: XCD x takes the
 // x-th eighth of the items, so that neighbours, which share rows, meet in one
 // L2. The item of this workgroup, -1: none.
@@ -62,16 +60,17 @@ __device__ __forceinline__ int xcd_item(int items) {
   return at < per && item < items ? item : -1;
 }
 
+// TN x TM tile (weight rows x activation rows), WN x WM wavefronts, S buffers.
 template <int TN, int TM, int WN, int WM, int S, bool GU>
-__global__ __launch_bounds__(64 * WN * WM, TN + TM >= 512 ? 2 : WN * WM / 2) void gemm_i8_tile(I8Args a,
-                                                                               int tiles_n) {
+__global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_i8_tile(I8Args a, int tiles_n) {
   constexpr int kW = WN * WM, kRows = TN + TM, kCopies = kRows / 8 / kW;
-  static_assert(kRows % (8 * kW) == 0 && TN % (8 * kW) == 0, "whole copies per wavefront");
+  static_assert(kRows % (8 * kW) == 0 && TN % (8 * kW) == 0 && (S == 3 || S == 4),
+                "whole copies per wavefront");
   constexpr int NF = TN / WN / 16, MF = TM / WM / 16;  // MFMA tiles per wavefront
   static_assert(!GU || NF % 2 == 0, "gate and up tiles in pairs");
   __shared__ __align__(128) uint8_t buf0[kRows * 128];
   __shared__ __align__(128) uint8_t buf1[kRows * 128];
-  __shared__ __align__(128) uint8_t buf2[S > 2 ? kRows * 128 : 16];
+  __shared__ __align__(128) uint8_t buf2[kRows * 128];
   __shared__ __align__(128) uint8_t buf3[S > 3 ? kRows * 128 : 16];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -172,22 +171,20 @@ __global__ __launch_bounds__(64 * WN * WM, TN + TM >= 512 ? 2 : WN * WM / 2) voi
   const int steps = (K + 127) / 128;
   // past the end of K a copy brings zeros, which the products ignore
   copy(buf0, 0);
-  if constexpr (S > 2) copy(buf1, 128);
+  copy(buf1, 128);
   if constexpr (S > 3) copy(buf2, 256);
   for (int s = 0; s < steps; s += S) {
     // each step: its copies (the oldest) have arrived for every wavefront, and
     // the buffer the last step read is free for the copies S - 1 steps ahead
     tile_barrier(vm_lds((S - 2) * kCopies));
-    copy(S == 2 ? buf1 : (S == 3 ? buf2 : buf3), (s + S - 1) * 128);
+    copy(S == 3 ? buf2 : buf3, (s + S - 1) * 128);
     compute(buf0);
     tile_barrier(vm_lds((S - 2) * kCopies));
     copy(buf0, (s + S) * 128);
     compute(buf1);
-    if constexpr (S > 2) {
-      tile_barrier(vm_lds((S - 2) * kCopies));
-      copy(buf1, (s + S + 1) * 128);
-      compute(buf2);
-    }
+    tile_barrier(vm_lds((S - 2) * kCopies));
+    copy(buf1, (s + S + 1) * 128);
+    compute(buf2);
     if constexpr (S > 3) {
       tile_barrier(vm_lds((S - 2) * kCopies));
       copy(buf2, (s + S + 2) * 128);
