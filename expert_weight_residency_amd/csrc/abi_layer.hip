@@ -274,7 +274,6 @@ int moe_expert_ffn_i8(const moe_bank* bank, moe_split split, const int8_t* xq, c
   a.k = k;
   a.by_token = 1;
   a.gate_up = 1;
-  a.host = bank->on_host != MOE_BANK_DEVICE;
   a.y = h;
   a.dtype = MOE_DTYPE_F32;
   a.ldy = I;

@@ -1,5 +1,6 @@
 // Products of 8-bit rows with a scale per activation row and per weight row, in
-// tiles: steps with many activation rows per weight matrix.
+// tiles: the grouped products of the expert FFN, and dense ones but for those of
+// gemm_i8_use_stream.
 //
 //   y[r][n] = sa[r] * sw[n] * sum_k a[r][k] w[n][k]
 //
@@ -421,7 +422,11 @@ hipError_t launch_gemm_i8_tile(const I8Args& a, hipStream_t s) {
   // 256 wide 60 us, 128 wide 63, 192 wide 81; 8192 x 8192 x 4096: 261, 312, 308).
   const int cus = device_cus();
   const int64_t tiles_m = (a.M + 255) / 256;
-  if (tiles_m * ((a.N + 255) / 256) >= cus) {
+  // Products of at most 64 rows take one row of tiles of 64 (a 128- or 256-row
+  // tile of the same width multiplies as many rows of padding: 17 x 65536 x 2880
+  // 57.1 us at 256 x 256, 38.5 at 128 x 64; 64 x 16384 x 4096 25.0 us at 128 x 128,
+  // 19.9).
+  if (a.M > 64 && tiles_m * ((a.N + 255) / 256) >= cus) {
     auto cost = [&](int tn) {
       return (tiles_m * ((a.N + tn - 1) / tn) + cus - 1) / cus * tn;
     };
@@ -436,7 +441,7 @@ hipError_t launch_gemm_i8_tile(const I8Args& a, hipStream_t s) {
   auto tiles = [&](int tn, int tm) {
     return (int64_t)((a.N + tn - 1) / tn) * ((a.M + tm - 1) / tm);
   };
-  if (a.K >= 2048 && tiles(128, 128) >= cus / 2) return go_big<128, 128, 3>(a, s);
+  if (a.M > 64 && a.K >= 2048 && tiles(128, 128) >= cus / 2) return go_big<128, 128, 3>(a, s);
   if (tiles(128, 64) >= cus) return go<128, 64, 4, 2, 3, false>(a, s);
   if (tiles(64, 64) >= cus) return go<64, 64, 2, 2, 3, false>(a, s);
   return go<32, 64, 2, 2, 4, false>(a, s);

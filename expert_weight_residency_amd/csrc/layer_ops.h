@@ -65,7 +65,6 @@ struct I8Args {
   const int32_t *n_active, *active_rows, *row_off, *slots;  // null: dense
   int n_rows;   // grouped: rows of the bank
   int k, by_token, gate_up;
-  int host;     // the weights are in pinned host memory
   void* y;
   int dtype;
   int64_t ldy;

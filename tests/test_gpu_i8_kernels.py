@@ -32,18 +32,21 @@ TILES = {
     (112, 1000, 2896): "gemm_i8_tile<32, 64, 2, 2, 4, false>",
     (17, 63, 9232): "gemm_i8_tile<32, 64, 2, 2, 4, false>",
 }
-# Few rows: chunks of 128 bytes per wavefront, K of whole lines and not.
-CHUNKS = {1: (1024, 1008), 2: (2048, 1936), 3: (2944, 2896), 4: (4096, 4080), 6: (5120, 5136),
-          8: (8192, 7056)}
-STREAM = {(M, 45, K): f"gemm_i8_stream<{cpw}, {1 if M <= 8 else 2}, false, {'false' if i else 'true'}>"
-          for cpw, Ks in CHUNKS.items() for i, K in enumerate(Ks) for M in (1, 7, 12)}
+# Few rows times few long ones, or many of 4096 or 8192: chunks of 128 bytes per
+# wavefront; rows of whole lines and not.
+STREAM = {(M, N, K): f"gemm_i8_stream<{4 if K == 4096 else 8}, {1 if M <= 8 else 2}, {'false' if K % 128 else 'true'}>"
+          for N, K in ((16391, 4096), (16391, 8192), (45, 8192), (1030, 7056), (2047, 6160)) for M in (1, 7, 12)}
+# Few rows elsewhere
+FEW = {(M, 45, K): "gemm_i8_tile<32, 64, 2, 2, 4, false>" for K in (1008, 1024, 2048, 2896, 4096, 5136)
+       for M in (1, 12)}
+FEW[(5, 16421, 1936)] = "gemm_i8_tile<64, 64, 2, 2, 3, false>"
+FEW[(16, 33001, 1936)] = "gemm_i8_tile<128, 64, 4, 2, 3, false>"
+FEW.update({(M, N, K): "gemm_i8_tile<128, 64, 4, 2, 3, false>"
+            for M, N, K in ((16, 33001, 4112), (64, 33001, 2064), (17, 66000, 272), (3, 40001, 7184))})
+FEW[(65, 16390, 2064)] = "gemm_i8_big<128, 128, 3>"
 # Expert FFN, gate/up (K = H) and down (K = I): T, k, E, H, I
-FFN = {(4, 2, 3, H, 192): f"gemm_i8_stream<{cpw}, 1, true, {'false' if H % 128 else 'true'}>"
-       for cpw, H in ((1, 1024), (1, 960), (2, 2048), (2, 1984), (3, 2944), (3, 2880), (4, 4096),
-                      (4, 4032), (6, 5120), (6, 5184), (8, 8192), (8, 7104))}
-FFN.update({(3, 2, 3, 128, 5184): "gemm_i8_stream<6, 1, false, false>",
-            (90, 3, 5, 1088, 320): "gemm_i8_tile<128, 64, 4, 2, 3, true>",
-            (90, 3, 5, 320, 1088): "gemm_i8_tile<128, 64, 4, 2, 3, false>"})
+FFN = [(4, 2, 3, H, 192) for H in (960, 1024, 1984, 2048, 2880, 2944, 4032, 4096, 5120, 5184, 7104, 8192)]
+FFN += [(3, 2, 3, 128, 5184), (90, 3, 5, 1088, 320), (90, 3, 5, 320, 1088)]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -63,7 +66,7 @@ def linear(M, N, K):
     return xq, xs, w, ws
 
 
-@pytest.mark.parametrize("M,N,K", list(TILES) + list(STREAM))
+@pytest.mark.parametrize("M,N,K", list(TILES) + list(STREAM) + list(FEW))
 def test_dense(M, N, K):
     xq, xs, w, ws = linear(M, N, K)
     # sums of integers below 2^53: exact in any order
@@ -93,7 +96,7 @@ def run(b, ids, x, H, I):
     return run_ffn(bank_on(b, "device"), bank_on(none, "device"), np.arange(len(b["s2"])), ids, x, H, I)
 
 
-@pytest.mark.parametrize("T,k,E,H,I", list(FFN))
+@pytest.mark.parametrize("T,k,E,H,I", FFN)
 def test_expert_ffn(T, k, E, H, I):
     b, ids, x = ffn_step(T, k, E, H, I)
     check_ffn(run(b, ids, x, H, I), b, ids, x, H, I)
@@ -104,14 +107,23 @@ def test_the_sizes_reach_every_instance():
     256 CUs."""
     assert torch.cuda.get_device_properties(0).multi_processor_count == 256
     reached = set()
-    for (M, N, K), want in {**TILES, **STREAM}.items():
+    for (M, N, K), want in {**TILES, **STREAM, **FEW}.items():
         xq, xs, w, ws = linear(M, N, K)
         y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
         got = launched(lambda: moe.moe_linear_i8(xq, xs, w, ws, y), KERNELS)
         assert got == {want}, (M, N, K, got)
         reached |= got
-    for shape, want in FFN.items():
+    for M in (1, 16):  # weights off a line
+        xq, xs, w, ws = linear(M, 16391, 4096)
+        off = torch.empty(w.numel() + 16, dtype=torch.int8, device="cuda")[16:].view(w.shape)
+        y, z = (torch.empty(M, 16391, device="cuda") for _ in range(2))
+        got = launched(lambda: moe.moe_linear_i8(xq, xs, off.copy_(w), ws, y), KERNELS)
+        assert got == {f"gemm_i8_stream<4, {1 if M <= 8 else 2}, false>"}, got
+        moe.moe_linear_i8(xq, xs, w, ws, z)
+        assert torch.equal(y, z)
+        reached |= got
+    for shape in FFN:
         got = launched(lambda: run(*ffn_step(*shape), *shape[3:]), KERNELS)
-        assert want in got and len(got) == 2, (shape, got)
+        assert got == {f"gemm_i8_tile<128, 64, 4, 2, 3, {gu}>" for gu in ("true", "false")}, (shape, got)
         reached |= got
     assert reached == held(KERNELS), held(KERNELS) ^ reached
