@@ -17,15 +17,18 @@
 //  - Each wavefront holds its slice of the activations in registers (gate/up)
 //    or in LDS (down) and streams weights through a register ring
 //    some items ahead, with one barrier per two gate/up items for the sum of
-//    the wavefronts' partial results (one barrier per item: 170 us instead of
-//    158 at 16 tokens) and none but the staging's in the down kernel.
+//    the wavefronts' partial results (the step at 16 tokens: 247 us, 260 with
+//    one barrier per item; at 1 and 7 tokens no difference) and none but the
+//    staging's in the down kernel.
 //  - A weight load takes 8 rows x one whole 128-byte line (256 elements). Lanes
 //    r < 8 of the MFMA operand hold the first half of row r's line, lanes r >= 8
 //    the second half of row r - 8's; the B operand holds the tokens' first
 //    halves in columns 0-7 and their second halves in columns 8-15. The result
 //    tile's two diagonal 8 x 8 blocks are then the two halves' partial sums
 //    (the other two are discarded), and no lane exchange is needed. More than 8
-//    tokens take a second set of columns.
+//    tokens take a second set of columns (which 8 and fewer could do without
+//    harm to the result, but not for nothing: the step at 1, 7 and 8 tokens 34.3,
+//    129.5 and 144.4 us with two sets, 32.7, 127.5 and 140.6 with one).
 // The order of every sum is fixed by the shapes and the picks' order alone, not
 // by the banks: a step gives the same bits wherever its experts are.
 #include <algorithm>
@@ -64,7 +67,12 @@ struct Cut {
   int nchunk, cpw, ks, sub;
 };
 // Gate/up: as many wavefronts per row as there are (its partial sums go through
-// LDS for every item anyway, and short slices keep the x operands few).
+// LDS for every item anyway, and short slices keep the x operands few): the step
+// at 1, 7 and 16 tokens and H = 4096 32.7, 127.5 and 247 us with 8 wavefronts of
+// 2 chunks, 37.2, 132.4 and 248 with 2 x 4 of 4. Above 4096 a wavefront takes 4
+// chunks, so H just past it leaves some idle (16 tokens: 2.9 TB/s at H = 4160, 4.6
+// at 8128, 4.95 at 8192, 4.5 at 4096; the ragged form for two sets also spills 16
+// registers).
 __host__ __device__ inline Cut gate_up_cut(int H) {
   Cut c;
   c.nchunk = (H + kChunkElems - 1) / kChunkElems;
@@ -356,7 +364,8 @@ __device__ __forceinline__ void write_h(const FewArgs& a, const Shared& L, int i
 // reads (see ffn_host.hip): an item's 8 gate and 8 up rows are two contiguous
 // blocks, copied in linear order through registers into LDS while the last item
 // is multiplied out of it, instead of 8 rows x 128 bytes per load (one expert
-// of 12.5 MB beside 35 in HBM: 315 us in place, 230 us so).
+// of 12.5 MB beside 35 in HBM: 315 us in place, 230 us so; the step with 4, 8, 16
+// and 32 workgroups for it 423, 396, 403 and 396 us).
 constexpr int kHostBlocks = 8;
 constexpr int kHostVecs = kMaxH / 2 / 512;  // 16-byte pieces per thread and item
 
@@ -875,7 +884,8 @@ hipError_t go_down(const FewArgs& a, hipStream_t stream) {
 }
 
 // R ring slots, 32 CPW KB of weights each and CU. At H = 4096 (CPW = 2), 2 slots
-// take 21.3, 78.4 and 158 us for 1, 7 and 16 tokens, 4 slots 24.2, 83.1 and 154.
+// take 21.3, 78.4 and 158 us for 1, 7 and 16 tokens, 4 slots 24.2, 83.1 and 154
+// (traces of one build range over 154-174 us at 16 tokens).
 template <int CPW, int R, bool WIDE>
 hipError_t gate_up_sets(const FewArgs& a, hipStream_t s) {
   return a.T <= 8 ? go_gate_up<CPW, 1, R, WIDE>(a, s) : go_gate_up<CPW, 2, R, WIDE>(a, s);

@@ -373,3 +373,40 @@ def test_graph_replays_match_eager(T):
         for got, ref in zip((out, shared), want[n]):
             assert torch.equal(got.view(torch.int16), ref.view(torch.int16))
         assert torch.randn(64, 64, device="cuda").sum().isfinite()
+
+
+@pytest.mark.parametrize("side", ["hot_stream", "cold_stream"])
+def test_captured_layer_on_two_streams(side):
+    """The whole int8 layer with a side stream, captured: the fork and the join
+    are in the graph, and every replay gives the eager bits."""
+    from expert_weight_residency_amd.layer import LayerBuffers, ResidencyLayer
+    T, k, E, H, I = 9, 3, 12, 256, 320
+    b = make_bank(E, H, I, 17)
+    rm, ho, co = synth.random_map(E, 4, 6)
+    layer = ResidencyLayer(bank_on(rows_of(b, ho), "device"), bank_on(rows_of(b, co), "host"),
+                           torch.from_numpy(rm.astype(np.int32)).cuda(), H, I)
+    bufs = LayerBuffers.allocate(T, k, H, I, E - 4, 4, i8=True)
+    other = torch.cuda.Stream()
+    steps = []
+    for s in range(3):
+        ids, w = synth.gaussian_routing(T, k, E, 50 + s)
+        x = torch.randn(T, H, generator=torch.Generator().manual_seed(s)).to(torch.bfloat16)
+        steps.append([torch.from_numpy(ids.astype(np.int32)).cuda(), torch.from_numpy(w).cuda(), x.cuda()])
+    want = []
+    for ids, w, x in steps:
+        layer.forward(x.view(torch.uint16), ids, w, bufs)
+        torch.cuda.synchronize()
+        want.append(bufs.out.clone())
+    st = [t.clone() for t in steps[0]]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        layer.forward(st[2], st[0], st[1], bufs, **{side: other})
+    for rep in range(6):
+        for d, v in zip(st, steps[rep % 3]):
+            d.copy_(v)
+        bufs.out.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bufs.out, want[rep % 3])
+        assert torch.randn(64, 64, device="cuda").sum().isfinite()
