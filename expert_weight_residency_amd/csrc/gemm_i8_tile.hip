@@ -26,7 +26,8 @@
 // 1.13. Two or three buffers and two or three workgroups per CU are equal; one
 // workgroup with four buffers takes 2.5 ms; tiles of 32 slots 2.5, of 128 slots
 // 2.18, of 256 weight rows 2.6; weights straight into registers, six steps
-// ahead, 2.6.
+// ahead, 2.6. At 16 tokens (65-73 experts, bound by HBM reads) 276 and 148 us, 6.0
+// and 5.6 TB/s.
 #include "gemm_i8.h"
 #include "mxfp4_common.h"
 #include "tile_items.h"
