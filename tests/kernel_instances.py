@@ -21,9 +21,15 @@ def held(names):
 
 
 def launched(f, names):
+    """The instances that f launches (once more if the profiler delivered no
+    event at all)."""
     from torch.profiler import ProfilerActivity, profile
     torch.cuda.synchronize()
-    with profile(activities=[ProfilerActivity.CUDA], acc_events=True) as p:
-        f()
-        torch.cuda.synchronize()
-    return instances("\n".join(e.key for e in p.key_averages()), names)
+    for _ in range(3):
+        with profile(activities=[ProfilerActivity.CUDA], acc_events=True) as p:
+            f()
+            torch.cuda.synchronize()
+        got = instances("\n".join(e.key for e in p.key_averages()), names)
+        if got:
+            break
+    return got

@@ -410,3 +410,49 @@ def test_captured_layer_on_two_streams(side):
         torch.cuda.synchronize()
         assert torch.equal(bufs.out, want[rep % 3])
         assert torch.randn(64, 64, device="cuda").sum().isfinite()
+
+
+def check_rows(y, rows, xq, xs, w, ws):
+    for m in rows:
+        for n in (0, 1, y.shape[1] // 2, y.shape[1] - 1):
+            ref = float((xq[m].double() * w[n].double()).sum()) * float(xs[m]) * float(ws[n])
+            assert abs(float(y[m, n]) - ref) <= (3.1 * U32 + HALF_STEP[y.dtype]) * abs(ref) + 2.0 ** -140, (m, n)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 1100003, 4096), (20, 1100003, 4096), (70, 540001, 8192),
+                                   (600001, 4090, 64), (2200003, 1000, 2048)])
+def test_linear_offsets_past_32_bits(M, N, K):
+    """Weights, outputs or activations of more than 4 GB."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    xq = torch.randint(-127, 128, (M, K), dtype=torch.int8, device="cuda", generator=g)
+    w = torch.randint(-127, 128, (N, K), dtype=torch.int8, device="cuda", generator=g)
+    xs = torch.rand(M, device="cuda", generator=g) + 0.5
+    ws = (torch.rand(N, device="cuda", generator=g) + 0.5) / 1000
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    assert max(w.numel(), 2 * y.numel(), xq.numel()) > 2 ** 32
+    moe.moe_linear_i8(xq, xs, w, ws, y)
+    torch.cuda.synchronize()
+    check_rows(y, (0, 1, M // 2, M - 2, M - 1), xq, xs, w, ws)
+
+
+def test_layers_of_no_tokens():
+    """Steps of no tokens, in each form of the layer, launch nothing that fails."""
+    from expert_weight_residency_amd.layer import LayerBuffers, ResidencyLayer
+    k, E, H, I = 2, 4, 128, 64
+    b = make_bank(E, H, I, 3)
+    rm = torch.tensor([0, 1, -1, -2], dtype=torch.int32, device="cuda")
+    mx = [torch.zeros(s, dtype=torch.uint8, device="cuda")
+          for s in ((2, 2 * I, H // 2), (2, 2 * I, H // 32), (2, H, I // 2), (2, H, I // 32))]
+    ids, w = torch.empty(0, k, dtype=torch.int32, device="cuda"), torch.empty(0, k, device="cuda")
+    x = torch.empty(0, H, dtype=torch.bfloat16, device="cuda")
+    i8 = [bank_on({n: v[i:i + 2] for n, v in b.items()}, where) for i, where in ((0, "device"), (2, "host"))]
+    for layer, kind in ((ResidencyLayer(*i8, rm, H, I), True),
+                        (ResidencyLayer(moe.Bank(*mx), moe.Bank(*mx), rm, H, I), False)):
+        bufs = LayerBuffers.allocate(0, k, H, I, 2, 2, i8=kind)
+        bufs.out.fill_(7)
+        layer.route(torch.empty(0, E, device="cuda"), ids, w)
+        layer.forward(x, ids, w, bufs)
+        if not kind:
+            layer.forward_few(x, ids, w, bufs)
+        torch.cuda.synchronize()
+        assert (bufs.out == 7).all()
