@@ -26,11 +26,13 @@ ENTRY_POINTS = ("moe_expert_bytes", "moe_ffn_workspace_bytes", "moe_route_split"
                 "moe_last_error", "moe_expert_ffn_mxfp4_noalloc", "moe_stage_rows_dma",
                 "moe_topk_gate", "moe_layer_few_workspace_bytes", "moe_layer_few_mxfp4",
                 "moe_quantize_rows_i8", "moe_linear_i8", "moe_ffn_i8_workspace_bytes",
-                "moe_expert_ffn_i8")
+                "moe_expert_ffn_i8", "moe_quantize_rows_f8", "moe_linear_f8",
+                "moe_ffn_f8_workspace_bytes", "moe_expert_ffn_f8")
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_H, MOE_FEW_MAX_I = 16, 8192, 4096
 # moe_topk_gate weights: softmax over the picks, or over all unmasked experts
 GATE_NORM_PICKS, GATE_NORM_ALL = 0, 1
+MOE_F8_BLOCK = 128
 
 
 class MoeError(RuntimeError):
@@ -115,6 +117,14 @@ def lib():
         L.moe_ffn_i8_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.moe_expert_ffn_i8.restype = i32
         L.moe_expert_ffn_i8.argtypes = [bankp, MoeSplitC, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        L.moe_quantize_rows_f8.restype = i32
+        L.moe_quantize_rows_f8.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp]
+        L.moe_linear_f8.restype = i32
+        L.moe_linear_f8.argtypes = [vp, i64, vp, i32, vp, vp, i32, i32, vp, i32, i64, vp]
+        L.moe_ffn_f8_workspace_bytes.restype = sz
+        L.moe_ffn_f8_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.moe_expert_ffn_f8.restype = i32
+        L.moe_expert_ffn_f8.argtypes = [bankp, MoeSplitC, vp, vp, i32, i32, i32, i32, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -216,7 +226,7 @@ BANK_DEVICE, BANK_HOST, BANK_HOST_WEIGHTS = 0, 1, 2
 
 
 def _bank_abi(bank, dtypes) -> MoeBankC:
-    """The C form of a Bank or BankI8 whose weights and scales have the two
+    """The C form of a Bank, BankI8 or BankF8 whose weights and scales have the two
     dtypes (str names); built once per set of tensors (the call path stays
     cheap on the host)."""
     key = (bank.w13.data_ptr(), bank.s13.data_ptr(), bank.w2.data_ptr(), bank.s2.data_ptr(),
@@ -668,5 +678,100 @@ def moe_expert_ffn_i8(bank: BankI8, split: Split, xq, xs, k: int, I: int, worksp
         _need(Y, "Y", 2 * T * k * H)
     b = bank.abi()
     _check(lib().moe_expert_ffn_i8(ctypes.byref(b), split.abi(), _ptr(xq, "xq", torch.int8),
+                                   _ptr(xs, "xs", torch.float32), T, k, H, I,
+                                   _gpu(workspace, "workspace"), _gpu(Y, "Y", _BF16_BITS), s))
+
+
+@dataclass
+class BankF8:
+    """A bank of 8-bit floating point experts: E4M3 tensors w13 [R,2I,H], w2 [R,H,I]
+    (torch.float8_e4m3fn) and their float32 scales per block of 128 x 128, s13
+    [R,2,ceil(I/128),ceil(H/128)] (gate, then up), s2 [R,ceil(H/128),ceil(I/128)];
+    on_host as in Bank."""
+    w13: object
+    s13: object
+    w2: object
+    s2: object
+    on_host: int = BANK_DEVICE
+
+    @property
+    def n_rows(self) -> int:
+        return int(self.w13.shape[0])
+
+    def abi(self) -> MoeBankC:
+        return _bank_abi(self, ("torch.float8_e4m3fn", "torch.float32"))
+
+    def tensors(self) -> dict:
+        return {"w13": self.w13, "s13": self.s13, "w2": self.w2, "s2": self.s2}
+
+
+def _f8_blocks(n: int) -> int:
+    return (n + MOE_F8_BLOCK - 1) // MOE_F8_BLOCK
+
+
+def moe_quantize_rows_f8(x, q, scale, stream=None) -> None:
+    """x [rows,K] (bfloat16, float16 or float32; rows may be strided) -> q E4M3
+    (torch.float8_e4m3fn) [rows,K], scale fp32 [rows,ceil(K/128)]."""
+    import torch
+    p, dtype, rows, K, ld = _rows2d(x, "x", _dtypes())
+    dev, s = _current(stream)
+    _on(dev, x=x, q=q, scale=scale)
+    if q.shape != x.shape or scale.shape != (rows, _f8_blocks(K)):
+        raise MoeError(MOE_EINVAL, f"q {tuple(q.shape)}, scale {tuple(scale.shape)}: need "
+                                   f"{(rows, K)} and {(rows, _f8_blocks(K))}")
+    _check(lib().moe_quantize_rows_f8(p, dtype, ld, rows, K, _ptr(q, "q", torch.float8_e4m3fn),
+                                      _ptr(scale, "scale", torch.float32), s))
+
+
+def moe_linear_f8(xq, xs, w, ws, y, stream=None) -> None:
+    """xq E4M3 [M,K] (rows may be strided) with scales xs fp32 [M,ceil(K/128)], times
+    w E4M3 [N,K] with scales ws fp32 [ceil(N/128),ceil(K/128)] -> y [M,N] (bfloat16,
+    float16 or float32; rows may be strided)."""
+    import torch
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    xp, _, M, K, ldx = _rows2d(xq, "xq", {f8: 0})
+    yp, dtype, my, N, ldy = _rows2d(y, "y", _dtypes())
+    dev, s = _current(stream)
+    _on(dev, xq=xq, xs=xs, w=w, ws=ws, y=y)
+    blocks = _f8_blocks(K)
+    if my != M or w.shape != (N, K) or xs.shape != (M, blocks) or \
+            ws.shape != (_f8_blocks(N), blocks):
+        raise MoeError(MOE_EINVAL, f"xq {(M, K)}, xs {tuple(xs.shape)}, w {tuple(w.shape)}, ws "
+                                   f"{tuple(ws.shape)}, y {(my, N)}: need [M,K], [M,K/128], [N,K], "
+                                   "[N/128,K/128] (blocks rounded up), [M,N]")
+    _check(lib().moe_linear_f8(xp, ldx, _ptr(xs, "xs", f32), M, _ptr(w, "w", f8),
+                               _ptr(ws, "ws", f32), N, K, yp, dtype, ldy, s))
+
+
+def moe_ffn_f8_workspace_bytes(T: int, k: int, H: int, I: int) -> int:
+    return int(lib().moe_ffn_f8_workspace_bytes(T, k, H, I))
+
+
+def moe_expert_ffn_f8(bank: BankF8, split: Split, xq, xs, k: int, I: int, workspace, Y,
+                      stream=None) -> None:
+    """The expert FFN over one bank's picks with 8-bit floating point experts; xq
+    E4M3 [T,H] and xs fp32 [T,ceil(H/128)] from moe_quantize_rows_f8."""
+    import torch
+    T, H = xq.shape
+    dev, s = _current(stream)
+    _on(dev, xq=xq, xs=xs, slots=split.slots, workspace=workspace, Y=Y)
+    _on(dev, **bank.tensors())
+    if T > 0 and bank.n_rows > 0:
+        R, bh, bi = bank.n_rows, _f8_blocks(H), _f8_blocks(I)
+        for name, n in (("w13", R * 2 * I * H), ("s13", R * 2 * bi * bh), ("w2", R * H * I),
+                        ("s2", R * bh * bi)):
+            got = int(getattr(bank, name).numel())
+            if got != n:
+                raise MoeError(MOE_EINVAL, f"bank {name}: {got} elements, {R} rows at H={H}, "
+                                           f"I={I} need {n}")
+        if int(split.slots.numel()) < T * k:
+            raise MoeError(MOE_EINVAL, f"split slots: {int(split.slots.numel())} entries, "
+                                       f"need T*k = {T * k}")
+        _need(xs, "xs", 4 * T * bh)
+        _need(workspace, "workspace", moe_ffn_f8_workspace_bytes(T, k, H, I))
+        _need(Y, "Y", 2 * T * k * H)
+    b = bank.abi()
+    _check(lib().moe_expert_ffn_f8(ctypes.byref(b), split.abi(),
+                                   _ptr(xq, "xq", torch.float8_e4m3fn),
                                    _ptr(xs, "xs", torch.float32), T, k, H, I,
                                    _gpu(workspace, "workspace"), _gpu(Y, "Y", _BF16_BITS), s))

@@ -31,18 +31,9 @@ int bank_ptrs(const moe_bank* b, const size_t align[4], const uint8_t* out[4]) {
 
 }  // namespace moe
 
-namespace {
-
+using moe::aligned;
+using moe::overlap;
 using moe::set_error;
-
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-bool overlap(const void* p, size_t np, const void* q, size_t nq) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + nq && b < a + np;
-}
-
-}  // namespace
 
 extern "C" {
 

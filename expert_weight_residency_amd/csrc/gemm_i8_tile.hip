@@ -37,31 +37,6 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __align__(16) const uint8_t kZeros[16] = {};
-
-// s_waitcnt immediate: at most n vector-memory operations and no LDS operation
-// outstanding.
-constexpr int vm_lds(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
-
-#define tile_barrier(W)                                    \
-  do {                                                     \
-    __builtin_amdgcn_sched_barrier(0);                     \
-    __builtin_amdgcn_s_waitcnt(W);                         \
-    __builtin_amdgcn_s_barrier();                          \
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup"); \
-    __builtin_amdgcn_sched_barrier(0);                     \
-  } while (0)
-
-// Workgroups go round the 8 XCDs in turn, each with its own L2: XCD x takes the
-// x-th eighth of the items, so that neighbours, which share rows, meet in one
-// L2. The item of this workgroup, -1: none.
-constexpr int kXcds = 8;
-__device__ __forceinline__ int xcd_item(int items) {
-  const int per = (items + kXcds - 1) / kXcds, at = blockIdx.x / kXcds;
-  const int item = (blockIdx.x % kXcds) * per + at;
-  return at < per && item < items ? item : -1;
-}
-
 // TN x TM tile (weight rows x activation rows), WN x WM wavefronts, S buffers.
 template <int TN, int TM, int WN, int WM, int S, bool GU>
 __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_i8_tile(I8Args a, int tiles_n) {

@@ -1,0 +1,85 @@
+// Shared by the tiled products (8-bit integers, 8-bit floating point, products
+// grouped by expert): waits for global-to-LDS copies, the order of tiles over the
+// XCDs, and the epilogue's stores.
+#pragma once
+
+#include <type_traits>
+
+#include "layer_ops.h"
+
+namespace moe {
+
+// Source of the granules past the end of a row.
+static __device__ __align__(16) const uint8_t kZeros[16] = {};
+
+// s_waitcnt immediate: at most n vector-memory operations and no LDS operation
+// outstanding.
+constexpr int vm_lds(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
+
+#define tile_barrier(W)                                    \
+  do {                                                     \
+    __builtin_amdgcn_sched_barrier(0);                     \
+    __builtin_amdgcn_s_waitcnt(W);                         \
+    __builtin_amdgcn_s_barrier();                          \
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup"); \
+    __builtin_amdgcn_sched_barrier(0);                     \
+  } while (0)
+
+// Workgroups go round the 8 XCDs in turn, each with its own L2: XCD x takes the
+// x-th eighth of the items, so that neighbours, which share rows, meet in one
+// L2. The item of this workgroup, -1: none.
+constexpr int kXcds = 8;
+__device__ __forceinline__ int xcd_item(int items) {
+  const int per = (items + kXcds - 1) / kXcds, at = blockIdx.x / kXcds;
+  const int item = (blockIdx.x % kXcds) * per + at;
+  return at < per && item < items ? item : -1;
+}
+
+// Outputs n .. n+3 (n a multiple of 4) of a row in type DT. VEC: N is a multiple
+// of 4 and every such group is aligned for one store; else the outputs past N
+// are left out one by one.
+template <int DT, bool VEC, typename A>
+__device__ __forceinline__ void store4(const A& a, int64_t row, int n, const float (&y)[4]) {
+  if constexpr (DT == MOE_DTYPE_F32) {
+    float* p = static_cast<float*>(a.y) + row * a.ldy + n;
+    if constexpr (VEC) {
+      *reinterpret_cast<float4*>(p) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (n + v < a.N) p[v] = y[v];
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(a.y) + row * a.ldy + n;
+    uint32_t b[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      b[v] = DT == MOE_DTYPE_BF16 ? f32_to_bf16_bits(y[v])
+                                  : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)y[v]);
+    if constexpr (VEC) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (n + v < a.N) p[v] = (uint16_t)b[v];
+    }
+  }
+}
+
+// f(type, vec) for the launch's output type and alignment, both compile-time in
+// f: the branches sit around one copy of the epilogue each. (Inside it, at every
+// store, they made the 256 x 256 tile's epilogue thousands of instructions.)
+template <typename A, typename F>
+__device__ __forceinline__ void with_output(const A& a, F f) {
+  const bool vec = ((a.ldy | a.N) & 3) == 0 &&
+                   (reinterpret_cast<uintptr_t>(a.y) & (4 * dtype_bytes(a.dtype) - 1)) == 0;
+  auto by_type = [&](auto v) {
+    if (a.dtype == MOE_DTYPE_BF16) f(std::integral_constant<int, MOE_DTYPE_BF16>(), v);
+    else if (a.dtype == MOE_DTYPE_F16) f(std::integral_constant<int, MOE_DTYPE_F16>(), v);
+    else f(std::integral_constant<int, MOE_DTYPE_F32>(), v);
+  };
+  if (vec) by_type(std::true_type());
+  else by_type(std::false_type());
+}
+
+}  // namespace moe

@@ -16,6 +16,13 @@ inline bool dtype_known(int dtype) {
 // tensor's required alignment. MOE_OK, or an error with its message set.
 int bank_ptrs(const moe_bank* b, const size_t align[4], const uint8_t* out[4]);
 
+inline bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+inline bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + nq && b < a + np;
+}
+
 inline int succeed() { return set_error(MOE_OK, "%s", ""); }
 
 // Router logits -> top-k ids and weights (gate_topk.hip).
@@ -73,5 +80,33 @@ struct I8Args {
 // call is enqueued).
 bool gemm_i8_fits(const I8Args& a);
 hipError_t launch_gemm_i8(const I8Args& a, hipStream_t stream);
+
+// Rows to E4M3 with a scale per 128 elements (quantize_f8.hip); rows and split as
+// in launch_quantize_rows.
+hipError_t launch_quantize_f8(const void* x, int dtype, int64_t ld, int rows, int K,
+                              const moe_split* split, uint8_t* q, float* scale,
+                              hipStream_t stream);
+
+// Products of E4M3 rows (gemm_f8.hip): y[r][n] = sum over 128-blocks b of
+// sa[r][b] * sw[n / 128][b] * sum over k in b of a[r][k] w[n][k]. Dense, grouped
+// and gate_up as in I8Args; with gate_up the scales of up's blocks follow gate's.
+struct F8Args {
+  const uint8_t* a;
+  int64_t lda;
+  const float* sa;
+  const uint8_t* w;
+  const float* sw;
+  int M, N, K;  // grouped: M = T * k, a bound on the slots
+  const int32_t *n_active, *active_rows, *row_off, *slots;  // null: dense
+  int n_rows;   // grouped: rows of the bank
+  int k, by_token, gate_up;
+  void* y;
+  int dtype;
+  int64_t ldy;
+};
+bool gemm_f8_fits(const F8Args& a);
+hipError_t launch_gemm_f8(const F8Args& a, hipStream_t stream);
+
+inline int f8_blocks(int n) { return (n + MOE_F8_BLOCK - 1) / MOE_F8_BLOCK; }
 
 }  // namespace moe

@@ -14,7 +14,7 @@
 // at prefill sizes (4096 rows of 4096 bf16: 15.5 us, 50 MB at 3.2 TB/s; 24576
 // rows of 2880 fp32: 69 us, 354 MB at 5.1 TB/s), by one round trip to memory for a
 // few rows (3.1 us for one).
-#include "layer_ops.h"
+#include "quantize.h"
 
 namespace moe {
 namespace {
@@ -29,45 +29,6 @@ struct QuantArgs {
   int8_t* q;
   float* scale;
 };
-
-template <int DT>
-struct Elem {
-  using type = uint16_t;
-};
-template <>
-struct Elem<MOE_DTYPE_F32> {
-  using type = float;
-};
-template <int DT>
-__device__ __forceinline__ float widen(typename Elem<DT>::type v) {
-  if constexpr (DT == MOE_DTYPE_F32)
-    return v;
-  else if constexpr (DT == MOE_DTYPE_BF16)
-    return bf16_bits_to_f32(v);
-  else
-    return (float)__builtin_bit_cast(_Float16, v);
-}
-
-// 8 consecutive elements
-template <int DT>
-__device__ __forceinline__ void load8(const typename Elem<DT>::type* p, float (&v)[8]) {
-  if constexpr (DT == MOE_DTYPE_F32) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0];
-    const float4 b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = widen<DT>((uint16_t)(w[i] & 0xffffu));
-      v[2 * i + 1] = widen<DT>((uint16_t)(w[i] >> 16));
-    }
-  }
-}
-
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // round-half-even of 127 |x| / most, with x's sign; most > 0 finite, inv = 127 / most
 __device__ __forceinline__ int quant1(float x, float inv, float most) {

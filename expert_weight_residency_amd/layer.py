@@ -14,7 +14,7 @@ library's kernels.
 
 Two further forms of the same step: forward_few, the whole layer in two
 launches for at most MOE_FEW_MAX_TOKENS tokens, and forward on a pair of 8-bit
-integer banks (BankI8). route turns router logits into the ids and weights that
+banks, integers (BankI8) or floating point (BankF8). route turns router logits into the ids and weights that
 all of them take; where a token has fewer unmasked experts than k, its picks left
 over (id -1, weight 0) are counted as invalid and add nothing in any of the forms.
 """
@@ -24,12 +24,13 @@ from dataclasses import dataclass
 
 import torch
 
-from . import (GATE_NORM_PICKS, MOE_EINVAL, MOE_FEW_MAX_TOKENS, STAGE_ALL, STAGE_DOWN, STAGE_GATE_UP, Bank, BankI8,
-               MoeError, Split, moe_expert_down_mxfp4, moe_expert_ffn_i8, moe_expert_ffn_mxfp4,
-               moe_expert_gate_up_mxfp4, moe_ffn_i8_workspace_bytes, moe_ffn_workspace_bytes,
+from . import (GATE_NORM_PICKS, MOE_EINVAL, MOE_F8_BLOCK, MOE_FEW_MAX_TOKENS, STAGE_ALL, STAGE_DOWN,
+               STAGE_GATE_UP, Bank, BankF8, BankI8, MoeError, Split, moe_expert_down_mxfp4,
+               moe_expert_ffn_f8, moe_expert_ffn_i8, moe_expert_ffn_mxfp4, moe_expert_gate_up_mxfp4,
+               moe_ffn_f8_workspace_bytes, moe_ffn_i8_workspace_bytes, moe_ffn_workspace_bytes,
                moe_finalize, moe_layer_few_mxfp4, moe_layer_few_workspace_bytes,
-               moe_quantize_rows_i8, moe_route_split, moe_stage_rows, moe_stage_rows_dma,
-               moe_topk_gate)
+               moe_quantize_rows_f8, moe_quantize_rows_i8, moe_route_split, moe_stage_rows,
+               moe_stage_rows_dma, moe_topk_gate)
 
 
 @dataclass
@@ -45,19 +46,28 @@ class LayerBuffers:
 
     @classmethod
     def allocate(cls, T: int, k: int, H: int, I: int, n_hot: int, n_cold: int, device="cuda",
-                 i8: bool = False):
+                 i8: bool = False, f8: bool = False):
         """Buffers for steps of up to T tokens (forward, and forward_few of as many
-        as it takes); i8: for a pair of BankI8."""
-        ws = moe_ffn_i8_workspace_bytes(T, k, H, I) if i8 else max(
-            moe_ffn_workspace_bytes(T, k, H, I),
-            moe_layer_few_workspace_bytes(min(T, MOE_FEW_MAX_TOKENS), k, H, I))
+        as it takes); i8, f8: for a pair of BankI8 or BankF8."""
+        if i8 and f8:
+            raise MoeError(MOE_EINVAL, "buffers are for one kind of banks (i8 or f8)")
+        if i8:
+            ws = moe_ffn_i8_workspace_bytes(T, k, H, I)
+            q, scales = torch.int8, (max(T, 1),)
+        elif f8:
+            ws = moe_ffn_f8_workspace_bytes(T, k, H, I)
+            q, scales = torch.float8_e4m3fn, (max(T, 1), (H + MOE_F8_BLOCK - 1) // MOE_F8_BLOCK)
+        else:
+            ws = max(moe_ffn_workspace_bytes(T, k, H, I),
+                     moe_layer_few_workspace_bytes(min(T, MOE_FEW_MAX_TOKENS), k, H, I))
+            q = None
         return cls(Split.empty(n_hot, T, k, device), Split.empty(n_cold, T, k, device),
                    torch.zeros(1, dtype=torch.int32, device=device),
                    torch.empty(max(ws, 16), dtype=torch.uint8, device=device),
                    torch.empty((max(T * k, 1), H), dtype=torch.int16, device=device),
                    torch.empty((max(T, 1), H), dtype=torch.int16, device=device),
-                   torch.empty((max(T, 1), H), dtype=torch.int8, device=device) if i8 else None,
-                   torch.empty(max(T, 1), dtype=torch.float32, device=device) if i8 else None)
+                   None if q is None else torch.empty((max(T, 1), H), dtype=q, device=device),
+                   None if q is None else torch.empty(scales, dtype=torch.float32, device=device))
 
 
 class ColdStage:
@@ -143,10 +153,10 @@ class ResidencyLayer:
                  stage: ColdStage | None = None):
         """With `stage`, the cold bank's active rows are copied to it in one
         contiguous stream per row and the cold FFN reads them from HBM."""
-        self.i8 = isinstance(hot, BankI8)
-        if self.i8 != isinstance(cold, BankI8):
-            raise MoeError(MOE_EINVAL, "hot and cold must be of one kind (Bank or BankI8)")
-        if self.i8 and stage is not None:
+        self.i8, self.f8 = isinstance(hot, BankI8), isinstance(hot, BankF8)
+        if self.i8 != isinstance(cold, BankI8) or self.f8 != isinstance(cold, BankF8):
+            raise MoeError(MOE_EINVAL, "hot and cold must be of one kind (Bank, BankI8 or BankF8)")
+        if (self.i8 or self.f8) and stage is not None:
             raise MoeError(MOE_EINVAL, "the cold stage holds MXFP4 rows: none for 8-bit banks")
         self.hot, self.cold, self.row_map, self.H, self.I = hot, cold, row_map, H, I
         self.stage = stage
@@ -173,14 +183,17 @@ class ResidencyLayer:
                             count_tmax, stream=stream)
         return bufs.out
 
-    def _forward_i8(self, x, topk_w, k, bufs, s, cold_stream, hot_stream):
+    def _forward_8bit(self, x, topk_w, k, bufs, s, cold_stream, hot_stream):
         T = int(x.shape[0])
-        if bufs.xq is None:
-            raise MoeError(MOE_EINVAL, "8-bit banks need LayerBuffers.allocate(..., i8=True)")
+        kind, q = ("i8", torch.int8) if self.i8 else ("f8", torch.float8_e4m3fn)
+        if bufs.xq is None or bufs.xq.dtype != q:
+            raise MoeError(MOE_EINVAL, f"such banks need LayerBuffers.allocate(..., {kind}=True)")
+        quantize = moe_quantize_rows_i8 if self.i8 else moe_quantize_rows_f8
+        ffn = moe_expert_ffn_i8 if self.i8 else moe_expert_ffn_f8
         xq, xs = bufs.xq[:T], bufs.xs[:T]
         # bf16 bits in any of the types that the MXFP4 step takes them in
         xb = x.view(torch.bfloat16) if x.dtype in (torch.int16, torch.uint16) else x
-        moe_quantize_rows_i8(xb, xq, xs, stream=s)
+        quantize(xb, xq, xs, stream=s)
         cold_on = cold_stream if hot_stream is None and cold_stream is not None else s
         hot_on = hot_stream if hot_stream is not None else s
         # the side stream branches off before either bank's kernels
@@ -189,7 +202,7 @@ class ResidencyLayer:
                 on.wait_stream(s)
         for bank, split, on in ((self.cold, bufs.cold_split, cold_on),
                                 (self.hot, bufs.hot_split, hot_on)):
-            moe_expert_ffn_i8(bank, split, xq, xs, k, self.I, bufs.workspace, bufs.Y, stream=on)
+            ffn(bank, split, xq, xs, k, self.I, bufs.workspace, bufs.Y, stream=on)
         for on in (cold_on, hot_on):
             if on is not s:
                 s.wait_stream(on)
@@ -212,8 +225,8 @@ class ResidencyLayer:
         s = stream if stream is not None else torch.cuda.current_stream()
         moe_route_split(topk_ids, self.row_map, self.hot.n_rows, self.cold.n_rows, bufs.hot_split,
                         bufs.cold_split, bufs.n_invalid, counts_layer, count_tmax, stream=s)
-        if self.i8:
-            return self._forward_i8(x, topk_w, k, bufs, s, cold_stream, hot_stream)
+        if self.i8 or self.f8:
+            return self._forward_8bit(x, topk_w, k, bufs, s, cold_stream, hot_stream)
         if hot_stream is not None:
             hot_stream.wait_stream(s)
             moe_expert_ffn_mxfp4(self.hot, bufs.hot_split, x, k, self.I, bufs.workspace, bufs.Y,

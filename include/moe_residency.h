@@ -482,6 +482,85 @@ size_t moe_ffn_i8_workspace_bytes(int T, int k, int H, int I);
 int moe_expert_ffn_i8(const moe_bank *bank, moe_split split, const int8_t *xq, const float *xs,
                       int T, int k, int H, int I, void *workspace, uint16_t *Y, void *stream);
 
+/*
+ * Products in 8-bit floating point (E4M3, OCP: 448 the largest value, codes 0x7f
+ * and 0xff NaN, no infinities), with one fp32 scale per MOE_F8_BLOCK elements of
+ * an activation row and per MOE_F8_BLOCK x MOE_F8_BLOCK block of the weights:
+ *   y[m][n] = sum over blocks b of K of
+ *             xs[m][b] * ws[n / 128][b] * sum over k in b of xq[m][k] * w[n][k].
+ * A block's sum is taken in fp32, multiplied by the two scales' product (fp32,
+ * one rounding; it should be a normal number) and added in fp32, blocks in
+ * ascending order; one rounding to y's type. Where y has 16 bits the block's sum is
+ * the FP8 matrix instruction's, which cuts a product at 2^-13 of the largest of the
+ * 8 that it adds first (about 3e-5 of a sum of Gaussian terms). The last block of
+ * an axis may be a part. Results do not depend on the tile, bank or step size.
+ *
+ * moe_quantize_rows_f8 -- rows to E4M3 with one scale per 128 elements.
+ *
+ * For the elements k of a row's block b: scale[r][b] = max |x[r][k]| / 448 (fp32)
+ * and q[r][k] = the E4M3 value nearest to 448 * x[r][k] / max |x|, ties to the
+ * even code, decided exactly. A block whose scale would be below the smallest
+ * normal fp32 number (an all-zero block among them) becomes zeros with scale 0;
+ * one with an infinity or a NaN becomes zeros with scale NaN, so that whatever is
+ * computed from it is NaN.
+ *
+ * x: device, element type dtype, row r at x + r * ld elements, ld >= K, aligned
+ * to its element size (rows of whole 16-byte granules are faster). q: device
+ * bytes [rows][K]. scale: device fp32 [rows][ceil(K / 128)]. x, q and scale must
+ * not overlap. rows <= MOE_F8_MAX_ROWS, 1 <= K <= MOE_F8_MAX_K. Launches one
+ * kernel; nothing when rows == 0. May be captured.
+ */
+#define MOE_F8_BLOCK 128
+#define MOE_F8_MAX_K 131072
+#define MOE_F8_MAX_ROWS (1 << 23)
+int moe_quantize_rows_f8(const void *x, int dtype, int64_t ld, int rows, int K, uint8_t *q,
+                         float *scale, void *stream);
+
+/*
+ * moe_linear_f8 -- the dense product.
+ *
+ * xq: device E4M3, M rows of K at xq + m * ldx (ldx >= K). xs: device fp32
+ * [M][ceil(K / 128)]. w: device E4M3 [N][K]. ws: device fp32 [ceil(N / 128)]
+ * [ceil(K / 128)]. y: device, element type dtype, row m at y + m * ldy elements
+ * (ldy >= N), aligned to its element size; must not overlap the inputs. K and ldx
+ * multiples of 16, K <= MOE_F8_MAX_K; M, N <= MOE_F8_MAX_ROWS; xq and w 16-byte
+ * aligned. MOE_ENOTSUP for a product of more tiles than one launch takes (M * N
+ * past about 2^35). Launches one kernel; nothing when M or N is 0. May be
+ * captured.
+ */
+int moe_linear_f8(const uint8_t *xq, int64_t ldx, const float *xs, int M, const uint8_t *w,
+                  const float *ws, int N, int K, void *y, int dtype, int64_t ldy, void *stream);
+
+/* Bytes of the device workspace moe_expert_ffn_f8 needs. 0 when an argument is
+ * <= 0. */
+size_t moe_ffn_f8_workspace_bytes(int T, int k, int H, int I);
+
+/*
+ * moe_expert_ffn_f8 -- moe_expert_ffn_mxfp4 for a bank of E4M3 experts.
+ *
+ * For each active row r of `split` and each slot s of that row, with token t =
+ * s / k: g and u = the products of x[t] with the gate and the up rows of w13[r],
+ * h = silu(g) * u in fp32, h quantized per 128 elements (moe_quantize_rows_f8), y
+ * = its product with w2[r], Y[s] = bf16(y). Rows are unweighted, as there; only
+ * this bank's slots of Y are written.
+ *
+ * bank: w13 E4M3 [R][2I][H] (rows [0, I) gate, [I, 2I) up), s13 fp32
+ * [R][2][ceil(I / 128)][ceil(H / 128)] (gate and up have blocks of their own), w2
+ * E4M3 [R][H][I], s2 fp32 [R][ceil(H / 128)][ceil(I / 128)], 16-byte aligned;
+ * on_host as in moe_bank (pinned host tensors are read in place). moe_stage_rows,
+ * moe_stage_rows_dma and moe_swap_rows move MXFP4 banks only. xq, xs: the step's
+ * activations from moe_quantize_rows_f8, E4M3 [T][H] and fp32 [T][ceil(H / 128)].
+ * H and I positive multiples of 64, at most 32768; T * k <= MOE_F8_MAX_ROWS
+ * (MOE_ENOTSUP past what one launch takes). workspace: device,
+ * moe_ffn_f8_workspace_bytes(T, k, H, I) bytes; both bank calls of one step may
+ * share one (each writes only its own slots). Y: device bf16 [T*k][H]. xq,
+ * workspace and Y 16-byte aligned; workspace and Y overlap neither each other nor
+ * xq or xs. Launches kernels only; nothing when T == 0 or the bank has no rows.
+ * May be captured.
+ */
+int moe_expert_ffn_f8(const moe_bank *bank, moe_split split, const uint8_t *xq, const float *xs,
+                      int T, int k, int H, int I, void *workspace, uint16_t *Y, void *stream);
+
 /* Message for the last error returned on this thread ("" if none). */
 const char *moe_last_error(void);
 
