@@ -27,7 +27,8 @@ ENTRY_POINTS = ("moe_expert_bytes", "moe_ffn_workspace_bytes", "moe_route_split"
                 "moe_topk_gate", "moe_layer_few_workspace_bytes", "moe_layer_few_mxfp4",
                 "moe_quantize_rows_i8", "moe_linear_i8", "moe_ffn_i8_workspace_bytes",
                 "moe_expert_ffn_i8", "moe_quantize_rows_f8", "moe_linear_f8",
-                "moe_ffn_f8_workspace_bytes", "moe_expert_ffn_f8")
+                "moe_ffn_f8_workspace_bytes", "moe_expert_ffn_f8", "moe_grouped_linear",
+                "moe_grouped_linear_dx", "moe_grouped_linear_dw")
 MOE_NOALLOC_SCRATCH_BYTES = 32 << 20
 MOE_FEW_MAX_TOKENS, MOE_FEW_MAX_H, MOE_FEW_MAX_I = 16, 8192, 4096
 # moe_topk_gate weights: softmax over the picks, or over all unmasked experts
@@ -125,6 +126,15 @@ def lib():
         L.moe_ffn_f8_workspace_bytes.argtypes = [i32, i32, i32, i32]
         L.moe_expert_ffn_f8.restype = i32
         L.moe_expert_ffn_f8.argtypes = [bankp, MoeSplitC, vp, vp, i32, i32, i32, i32, vp, vp, vp]
+        L.moe_grouped_linear.restype = i32
+        L.moe_grouped_linear.argtypes = [vp, i32, i32, vp, i32, i32, MoeSplitC, i32, i32, i32, i32,
+                                         vp, i32, vp]
+        L.moe_grouped_linear_dx.restype = i32
+        L.moe_grouped_linear_dx.argtypes = [vp, i32, vp, i32, i32, MoeSplitC, i32, i32, i32, i32, vp,
+                                            i32, vp]
+        L.moe_grouped_linear_dw.restype = i32
+        L.moe_grouped_linear_dw.argtypes = [vp, vp, i32, i32, i32, MoeSplitC, i32, i32, i32, i32, vp,
+                                            i32, vp]
         _lib = L
     return _lib
 
@@ -775,3 +785,101 @@ def moe_expert_ffn_f8(bank: BankF8, split: Split, xq, xs, k: int, I: int, worksp
                                    _ptr(xq, "xq", torch.float8_e4m3fn),
                                    _ptr(xs, "xs", torch.float32), T, k, H, I,
                                    _gpu(workspace, "workspace"), _gpu(Y, "Y", _BF16_BITS), s))
+
+
+def _grouped_rows(t, name: str, dtypes, dtype=None, shape=None):
+    """(pointer, dtype code) of a contiguous GPU tensor of one of the types (of
+    `dtype` if given) and of the shape."""
+    code = dtypes.get(t.dtype)
+    if code is None or not t.is_cuda or not t.is_contiguous() or (dtype is not None and
+                                                                  t.dtype != dtype):
+        want = str(dtype) if dtype is not None else ", ".join(str(d) for d in dtypes)
+        raise _bad(name, f"a contiguous GPU tensor ({want})", t)
+    if shape is not None and tuple(t.shape) != shape:
+        raise MoeError(MOE_EINVAL, f"{name} {tuple(t.shape)}: need {shape}")
+    return t.data_ptr(), code
+
+
+def _grouped_weights(w, dtype):
+    """(pointer, rows, N, K, on_host) of weights [rows,N,K] on the GPU or pinned."""
+    if w.dim() != 3 or w.dtype != dtype or not w.is_contiguous() or \
+            not (w.is_cuda or (w.device.type == "cpu" and w.is_pinned())):
+        raise _bad("w", f"contiguous [rows,N,K] weights ({dtype}) on the GPU or in pinned memory", w)
+    return (w.data_ptr(), *w.shape, BANK_DEVICE if w.is_cuda else BANK_HOST)
+
+
+def _grouped_split(split: Split, slots: int, k: int) -> int:
+    """Tokens of `slots` rows of k each."""
+    if k < 1 or slots % k:
+        raise MoeError(MOE_EINVAL, f"{slots} slots are no multiple of k={k}")
+    if slots and int(split.slots.numel()) < slots:
+        raise MoeError(MOE_EINVAL, f"split slots: {int(split.slots.numel())} entries, "
+                                   f"need T*k = {slots}")
+    return slots // k
+
+
+_g16 = None
+
+
+def _grouped_types():
+    global _g16
+    if _g16 is None:
+        import torch
+        _g16 = {torch.bfloat16: 0, torch.float16: 1}
+    return _g16
+
+
+def _grouped_by_token(x, T: int, k: int) -> int:
+    if x.dim() != 2 or x.shape[0] not in (T, T * k):
+        raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)}: need {T} rows (a token's) or {T * k} (a slot's)")
+    return int(x.shape[0] == T)
+
+
+def moe_grouped_linear(x, w, split: Split, k: int, y, stream=None) -> None:
+    """y[s] = w[row of s] x[s or its token] over the split's slots: x [T,K] (a row per
+    token) or [T*k,K] (per slot), w [R,N,K], both bfloat16 or float16 (w also in pinned
+    host memory) -> y [T*k,N] (bfloat16, float16 or float32)."""
+    dev, s = _current(stream)
+    _on(dev, x=x, w=w, y=y, slots=split.slots)
+    xp, code = _grouped_rows(x, "x", _grouped_types())
+    wp, rows, N, K, on_host = _grouped_weights(w, x.dtype)
+    yp, ycode = _grouped_rows(y, "y", _dtypes(), shape=(int(y.shape[0]), N))
+    T = _grouped_split(split, int(y.shape[0]), k)
+    by_token = _grouped_by_token(x, T, k)
+    if x.shape[1] != K:
+        raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)}: rows of w have {K} elements")
+    _check(lib().moe_grouped_linear(xp, code, by_token, wp, rows, on_host, split.abi(), T, k, N, K,
+                                    yp, ycode, s))
+
+
+def moe_grouped_linear_dx(dy, w, split: Split, k: int, dx, stream=None) -> None:
+    """The gradient of moe_grouped_linear's input rows: dy [T*k,N] and w [R,N,K] in one
+    type -> dx [T*k,K] (bfloat16, float16 or float32)."""
+    dev, s = _current(stream)
+    _on(dev, dy=dy, w=w, dx=dx, slots=split.slots)
+    yp, code = _grouped_rows(dy, "dy", _grouped_types())
+    wp, rows, N, K, on_host = _grouped_weights(w, dy.dtype)
+    T = _grouped_split(split, int(dy.shape[0]), k)
+    if tuple(dy.shape) != (T * k, N):
+        raise MoeError(MOE_EINVAL, f"dy {tuple(dy.shape)}: need {(T * k, N)}")
+    xp, xcode = _grouped_rows(dx, "dx", _dtypes(), shape=(T * k, K))
+    _check(lib().moe_grouped_linear_dx(yp, code, wp, rows, on_host, split.abi(), T, k, N, K, xp,
+                                       xcode, s))
+
+
+def moe_grouped_linear_dw(dy, x, split: Split, k: int, dw, stream=None) -> None:
+    """The gradient of moe_grouped_linear's weights: dy [T*k,N] and x as there, in one
+    type -> dw [R,N,K] (bfloat16, float16 or float32), zeros for a row without slots."""
+    dev, s = _current(stream)
+    _on(dev, dy=dy, x=x, dw=dw, slots=split.slots)
+    yp, code = _grouped_rows(dy, "dy", _grouped_types())
+    xp, _ = _grouped_rows(x, "x", _grouped_types(), dtype=dy.dtype)
+    T = _grouped_split(split, int(dy.shape[0]), k)
+    by_token = _grouped_by_token(x, T, k)
+    wp, wcode = _grouped_rows(dw, "dw", _dtypes())
+    if dw.dim() != 3 or tuple(dy.shape) != (T * k, dw.shape[1]) or x.shape[1] != dw.shape[2]:
+        raise MoeError(MOE_EINVAL, f"dy {tuple(dy.shape)}, x {tuple(x.shape)}, dw {tuple(dw.shape)}: "
+                                   "need [T*k,N], [T or T*k,K], [R,N,K]")
+    rows, N, K = dw.shape
+    _check(lib().moe_grouped_linear_dw(yp, xp, code, by_token, rows, split.abi(), T, k, N, K, wp,
+                                       wcode, s))

@@ -109,4 +109,21 @@ hipError_t launch_gemm_f8(const F8Args& a, hipStream_t stream);
 
 inline int f8_blocks(int n) { return (n + MOE_F8_BLOCK - 1) / MOE_F8_BLOCK; }
 
+// Products grouped by expert (grouped_linear.hip): op 0 forward, 1 the input's
+// gradient, 2 the weights' gradient. Rows of one expert are the slots that the split
+// lists for it; x holds a row per token (by_token) or per slot, dy, y and dx a row
+// per slot.
+struct GroupedArgs {
+  int op, elem;  // elem: type of w, x and dy (bf16 or fp16)
+  const uint8_t *w, *x, *dy;
+  int M, N, K;  // M = T * k, a bound on the slots
+  const int32_t *n_active, *active_rows, *row_off, *slots;  // n_active null: no slots
+  int n_rows, k, by_token;
+  void* y;  // y, dx or dw
+  int dtype;
+  int64_t ldy;
+};
+bool grouped_fits(const GroupedArgs& a);
+hipError_t launch_grouped(const GroupedArgs& a, hipStream_t stream);
+
 }  // namespace moe

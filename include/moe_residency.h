@@ -561,6 +561,46 @@ size_t moe_ffn_f8_workspace_bytes(int T, int k, int H, int I);
 int moe_expert_ffn_f8(const moe_bank *bank, moe_split split, const uint8_t *xq, const float *xs,
                       int T, int k, int H, int I, void *workspace, uint16_t *Y, void *stream);
 
+/*
+ * Products grouped by expert: unquantised weights (whole experts' or low-rank
+ * adapters beside them), in bf16 or fp16 with fp32 sums, over the ragged rows that
+ * a split gives each expert, and their gradients. For each active row r of `split`
+ * and each slot s of that row:
+ *   moe_grouped_linear:    y[s][n]  = sum over k of w[r][n][k] * x[s][k]
+ *   moe_grouped_linear_dx: dx[s][k] = sum over n of w[r][n][k] * dy[s][n]
+ * and for every row r of the weights
+ *   moe_grouped_linear_dw: dw[r][n][k] = sum over the slots s of row r of
+ *                                        dy[s][n] * x[s][k],
+ * zero for a row without a slot (and for every row when T == 0). One rounding, to
+ * the output's type. Only the split's slots of y and dx are written. by_token:
+ * slot s reads row s / k of x, [T][K] (a token's row is shared by its k picks; the
+ * gradient of such a row is the sum of dx over the token's slots, for bf16
+ * moe_finalize with weights 1); else row s of x, [T*k][K]. The sums have one order,
+ * given by the slots' order and the shapes, so the bits depend on no step or grid.
+ *
+ * dtype: type of x, w and dy, MOE_DTYPE_BF16 or MOE_DTYPE_F16; ydtype, xdtype,
+ * wdtype: that of the output, any. w: [n_rows][N][K], device, or with on_host =
+ * MOE_BANK_HOST pinned host memory, read in place (MOE_BANK_DEVICE else). dy: device
+ * [T*k][N]. split: as moe_route_split leaves it for a bank of n_rows rows at T tokens
+ * of k picks; active rows differ from each other. Everything contiguous and 16-byte
+ * aligned; an output overlaps no input. n_rows <= MOE_MAX_ROWS, T * k <=
+ * MOE_GROUPED_MAX_SLOTS, N and K multiples of 8, at most MOE_GROUPED_MAX_DIM;
+ * MOE_ENOTSUP for more tiles than one launch takes. Each launches one kernel;
+ * moe_grouped_linear and _dx nothing when T == 0, all nothing when n_rows == 0.
+ * They may be captured.
+ */
+#define MOE_GROUPED_MAX_SLOTS (1 << 23)
+#define MOE_GROUPED_MAX_DIM 131072
+int moe_grouped_linear(const void *x, int dtype, int by_token, const void *w, int n_rows,
+                       int on_host, moe_split split, int T, int k, int N, int K, void *y,
+                       int ydtype, void *stream);
+int moe_grouped_linear_dx(const void *dy, int dtype, const void *w, int n_rows, int on_host,
+                          moe_split split, int T, int k, int N, int K, void *dx, int xdtype,
+                          void *stream);
+int moe_grouped_linear_dw(const void *dy, const void *x, int dtype, int by_token, int n_rows,
+                          moe_split split, int T, int k, int N, int K, void *dw, int wdtype,
+                          void *stream);
+
 /* Message for the last error returned on this thread ("" if none). */
 const char *moe_last_error(void);
 
