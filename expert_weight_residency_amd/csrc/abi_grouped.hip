@@ -16,16 +16,16 @@ struct Part {
 
 // The checks that the three calls share, and the launch. in: two inputs; out: the
 // output with its dtype.
-int grouped(moe::GroupedArgs& a, int T, int on_host, const moe_split& split, const Part (&in)[2],
+int grouped(moe::GroupedArgs& a, int T, int k, int by_token, int on_host, const moe_split& split, const Part (&in)[2],
             const Part& out, void* stream) {
   if (a.elem != MOE_DTYPE_BF16 && a.elem != MOE_DTYPE_F16)
     return set_error(MOE_EINVAL, "dtype=%d is not MOE_DTYPE_BF16 or MOE_DTYPE_F16", a.elem);
   if (!moe::dtype_known(a.dtype))
     return set_error(MOE_EINVAL, "dtype=%d of %s unknown", a.dtype, out.name);
   if (T < 0) return set_error(MOE_EINVAL, "T=%d must be >= 0", T);
-  if (a.k < 1 || a.k > MOE_MAX_TOPK)
-    return set_error(MOE_EINVAL, "k=%d outside [1, %d]", a.k, MOE_MAX_TOPK);
-  if ((int64_t)T * a.k > MOE_GROUPED_MAX_SLOTS)
+  if (k < 1 || k > MOE_MAX_TOPK)
+    return set_error(MOE_EINVAL, "k=%d outside [1, %d]", k, MOE_MAX_TOPK);
+  if ((int64_t)T * k > MOE_GROUPED_MAX_SLOTS)
     return set_error(MOE_EINVAL, "T*k above %d", MOE_GROUPED_MAX_SLOTS);
   if (a.n_rows < 0 || a.n_rows > MOE_MAX_ROWS)
     return set_error(MOE_EINVAL, "rows %d outside [0, %d]", a.n_rows, MOE_MAX_ROWS);
@@ -60,7 +60,8 @@ int grouped(moe::GroupedArgs& a, int T, int on_host, const moe_split& split, con
       a.w = static_cast<const uint8_t*>(d);
     }
   }
-  a.M = T * a.k;
+  a.M = T * k;
+  a.by_token = by_token && k > 1 ? (uint32_t)((((uint64_t)1 << 32) + k - 1) / k) : 0;
   a.y = const_cast<void*>(out.p);
   if (!moe::grouped_fits(a))
     return set_error(MOE_ENOTSUP, "T*k=%d, %d rows at N=%d, K=%d: more tiles than one launch takes",
@@ -89,12 +90,10 @@ int moe_grouped_linear(const void* x, int dtype, int by_token, const void* w, in
   a.N = N;
   a.K = K;
   a.n_rows = n_rows;
-  a.k = k;
-  a.by_token = by_token != 0;
   a.dtype = ydtype;
   a.ldy = N;
   const int64_t slots = (int64_t)T * k;
-  return grouped(a, T, on_host, split,
+  return grouped(a, T, k, by_token, on_host, split,
                  {{x, bytes(by_token ? T : slots, K, dtype), "x"},
                   {w, bytes((int64_t)n_rows * N, K, dtype), "w"}},
                  {y, bytes(slots, N, ydtype), "y"}, stream);
@@ -111,11 +110,10 @@ int moe_grouped_linear_dx(const void* dy, int dtype, const void* w, int n_rows, 
   a.N = N;
   a.K = K;
   a.n_rows = n_rows;
-  a.k = k;
   a.dtype = xdtype;
   a.ldy = K;
   const int64_t slots = (int64_t)T * k;
-  return grouped(a, T, on_host, split,
+  return grouped(a, T, k, 0, on_host, split,
                  {{dy, bytes(slots, N, dtype), "dy"},
                   {w, bytes((int64_t)n_rows * N, K, dtype), "w"}},
                  {dx, bytes(slots, K, xdtype), "dx"}, stream);
@@ -132,12 +130,10 @@ int moe_grouped_linear_dw(const void* dy, const void* x, int dtype, int by_token
   a.N = N;
   a.K = K;
   a.n_rows = n_rows;
-  a.k = k;
-  a.by_token = by_token != 0;
   a.dtype = wdtype;
   a.ldy = K;
   const int64_t slots = (int64_t)T * k;
-  return grouped(a, T, MOE_BANK_DEVICE, split,
+  return grouped(a, T, k, by_token, MOE_BANK_DEVICE, split,
                  {{dy, bytes(slots, N, dtype), "dy"},
                   {x, bytes(by_token ? T : slots, K, dtype), "x"}},
                  {dw, bytes((int64_t)n_rows * N, K, wdtype), "dw"}, stream);

@@ -35,6 +35,19 @@ __device__ __forceinline__ int xcd_item(int items) {
   return at < per && item < items ? item : -1;
 }
 
+// Two values rounded to a 16-bit type, the first one low.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (DT == MOE_DTYPE_BF16) {
+    const bf16x2 v = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  } else {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    const f16x2 v = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+}
+
 // Outputs n .. n+3 (n a multiple of 4) of a row in type DT. VEC: N is a multiple
 // of 4 and every such group is aligned for one store; else the outputs past N
 // are left out one by one.

@@ -46,9 +46,29 @@ __device__ __forceinline__ uint64_t read_turned(const uint8_t* p) {
                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
 }
 
+// Row of x for a slot (at most 2^23): its token, by the multiple of 2^32 / k rounded up,
+// off by less than 32 / 2^32 of the slot, or itself.
+__device__ __forceinline__ int token(const GroupedArgs& a, int slot) {
+  return a.by_token ? (int)__umulhi((uint32_t)slot, a.by_token) : slot;
+}
+
+// 16 bytes per lane from p to LDS, lane after lane.
+__device__ __forceinline__ void copy16(uint8_t* buf, const uint8_t* p) {
+  asm volatile("" : "+v"(p));  // a select, not a branch around two copies
+  __builtin_amdgcn_global_load_lds(p, buf, 16, 0, 0);
+}
+
+// The value of another lane of the same 16: lane r ^ 8, or 7 - r of the same 8.
+constexpr int kRor8 = 0x128, kHalfMirror = 0x141;
+template <int CTRL>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+
 // An operand of ROWS result rows (or columns) that is contiguous along the sum.
 template <int ROWS>
 struct Along {
+  static constexpr int kBytes = ROWS * 128;
   // copy c of a step (of ROWS / 8): rows 8 c .. + 7, lane l granule l % 8 of row l /
   // 8 from where the swizzle has it
   static __device__ __forceinline__ int row(int c, int lane) { return 8 * c + (lane >> 3); }
@@ -89,154 +109,310 @@ struct Across {
 
 enum { kForward, kInput, kWeights };
 
-// TA x TB result tile, WA x WB wavefronts, S buffers.
-template <int OP, int DT, int TA, int TB, int WA, int WB, int S>
-__global__ __launch_bounds__(64 * WA * WB,
-                                  (TA + TB) * 128 * S > 80 << 10 ? WA * WB / 4
-                                                                 : WA * WB / 2) void grouped(GroupedArgs a, int tiles_a,
-                                                                    int tiles_b) {
-  constexpr int kW = WA * WB, kRows = TA + TB, kCopies = kRows / 8 / kW, kCopiesA = TA / 8 / kW;
-  static_assert(TA % (8 * kW) == 0 && TB % (8 * kW) == 0 && (S == 3 || S == 4),
-                "whole copies per wavefront");
-  constexpr int NF = TA / WA / 16, MF = TB / WB / 16;  // MFMA tiles per wavefront
-  constexpr bool kTurnA = OP != kForward, kTurnB = OP == kWeights;
+// The slots of a long group, for the weights' gradient: a ring of two halves of
+// kHalf slots (x row and dy row of each), one read while the other is filled.
+constexpr int kHalf = 256;
+struct SlotRing {
+  int x[2 * kHalf], dy[2 * kHalf];
+};
+struct NoRing {};
+
+// The result tile of a workgroup and where its operands come from.
+template <int OP, int TA, int TB, int kW>
+struct Tile {
+  static constexpr bool kTurnA = OP != kForward, kTurnB = OP == kWeights;
   using A = std::conditional_t<kTurnA, Across<TA>, Along<TA>>;
   using B = std::conditional_t<kTurnB, Across<TB>, Along<TB>>;
-  __shared__ __align__(128) uint8_t buf0[kRows * 128];
-  __shared__ __align__(128) uint8_t buf1[kRows * 128];
-  __shared__ __align__(128) uint8_t buf2[kRows * 128];
-  __shared__ __align__(128) uint8_t buf3[S > 3 ? kRows * 128 : 16];
+  using Ring = std::conditional_t<OP == kWeights, SlotRing, NoRing>;
+  static constexpr int kCopiesA = TA / 8 / kW, kCopiesB = TB / 8 / kW;
+  static constexpr int kCopies = kCopiesA + kCopiesB;
+  static_assert(TA % (8 * kW) == 0 && TB % (8 * kW) == 0, "whole copies per wavefront");
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int N = a.N, K = a.K;
-  const int wn = wv % WA, wm = wv / WA, r = lane & 15, q = lane >> 4;
+  int a0, b0, m0, m1;  // first result row and column; slots of the tile, or of the group
+  int sum, steps;      // length of the sum, 64-element steps of it
+  int64_t row;         // of the bank
+  // Along: where each copy's granule lies at element 0 of the sum. Across: where it
+  // lies in row 0 (the same in all copies of a wavefront: rows that they are apart
+  // swizzle alike), and whether inside the row
+  const uint8_t *sa[kTurnA ? 1 : kCopiesA], *sb[kTurnB ? 1 : kCopiesB];
+  bool ina, inb;
 
-  // the tile: result rows of A from a0 (of na_), of B from b0, of expert `row`; its
-  // slots [m0, m1), all of the expert's (kWeights) or those of the tile
-  int a0, b0 = 0, m0, m1;
-  int64_t row;
-  if constexpr (OP == kWeights) {
-    const int per = tiles_a * tiles_b;
-    const int item = xcd_item(a.n_rows * per);
-    if (item < 0) return;
-    const int e = item / per, local = item - e * per;
-    const int active = a.n_active ? *a.n_active : 0;
-    a0 = local % tiles_a * TA;
-    b0 = local / tiles_a * TB;
-    if (e < active) {
-      m0 = a.row_off[e];
-      m1 = a.row_off[e + 1];
-      row = a.active_rows[e];
-    } else {
-      // the (e - active)-th row of the bank that has no slot: its gradient is zero
-      __shared__ uint32_t seen[MOE_MAX_ROWS / 32];
-      for (int i = tid; i < MOE_MAX_ROWS / 32; i += 64 * kW) seen[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < active; i += 64 * kW)
-        atomicOr(&seen[a.active_rows[i] >> 5], 1u << (a.active_rows[i] & 31));
-      __syncthreads();
-      int left = e - active, word = 0;
-      uint32_t free = ~seen[0];
-      while (left >= __popc(free)) {
-        left -= __popc(free);
-        free = ~seen[++word];
-      }
-      for (; left > 0; --left) free &= free - 1;
-      row = 32 * word + __ffs(free) - 1;
-      m0 = m1 = 0;
-    }
-  } else {
-    extern __shared__ int tpre[];  // [n_active + 1]
-    __shared__ int wsum[kW];
-    const int active = *a.n_active;
-    tiles::build_tile_prefix<TB, kW>(a.row_off, active, tpre, wsum);
-    const int item = xcd_item(tpre[active] * tiles_a);
-    if (item < 0) return;  // the whole workgroup
-    // items of one expert: weight rows outermost, so that its tiles meet a block of
-    // weights together
-    const int e = tiles::row_of_tile(tpre, active, item / tiles_a);
-    const int local = item - tpre[e] * tiles_a, nt = tpre[e + 1] - tpre[e];
-    a0 = local / nt * TA;
-    m0 = a.row_off[e] + (local - local / nt * nt) * TB;
-    m1 = min(m0 + TB, a.row_off[e + 1]);
-    row = a.active_rows[e];
-  }
-  const int width = OP == kForward ? N : K;                              // of A's rows
-  const int sum = OP == kForward ? K : OP == kInput ? N : m1 - m0;      // length of the sum
-  const uint8_t* w = OP == kWeights ? nullptr : a.w + row * N * (int64_t)K * 2;
-
-  // copies: wavefront wv takes copies wv + kW i of each operand. Per copy, where its
-  // granule lies at element 0 of the sum (Along) or in row 0 (Across), and which byte
-  // of the sum's axis (Along) or row (Across) it is in a step
-  constexpr int kCopiesB = kCopies - kCopiesA;
-  const uint8_t *sa[kCopiesA], *sb[kCopiesB];
-  int fa[kCopiesA], fb[kCopiesB];
-  bool ina[kCopiesA], inb[kCopiesB];  // Across: the granule lies inside the row
-#pragma unroll
-  for (int i = 0; i < kCopiesA; ++i) {
-    const int c = wv + kW * i;
-    if constexpr (OP == kForward) {
-      sa[i] = w + (int64_t)min(a0 + A::row(c, lane), N - 1) * K * 2 + 16 * A::gran(c, lane);
-      fa[i] = 16 * A::gran(c, lane);
-    } else {
-      const int col = a0 + 8 * A::gran(c, lane);
-      sa[i] = (OP == kInput ? w : a.x) + col * 2;
-      fa[i] = A::row(c, lane);
-      ina[i] = col < K;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kCopiesB; ++i) {
-    const int c = wv + kW * i;
+  // false: no tile is left for this workgroup
+  __device__ __forceinline__ bool init(const GroupedArgs& a, int tiles_a, int tiles_b, int* tpre,
+                                       int* wsum, uint32_t* seen) {
+    const int tid = threadIdx.x;
     if constexpr (OP == kWeights) {
-      const int col = b0 + 8 * B::gran(c, lane);
-      sb[i] = a.dy + col * 2;
-      fb[i] = B::row(c, lane);
-      inb[i] = col < N;
+      const int per = tiles_a * tiles_b;
+      const int item = xcd_item(a.n_rows * per);
+      if (item < 0) return false;
+      const int e = item / per, local = item - e * per;
+      a0 = local % tiles_a * TA;
+      b0 = local / tiles_a * TB;
+      // asked for at once with their count: entries past it are not used
+      const int at = min(e, min(a.n_rows, a.M) - 1);
+      const int active = a.n_active ? *a.n_active : 0;
+      m0 = a.n_active ? a.row_off[at] : 0;
+      m1 = a.n_active ? a.row_off[at + 1] : 0;
+      row = a.n_active ? a.active_rows[at] : 0;
+      if (e >= active) {
+        // the (e - active)-th row of the bank that has no slot: its gradient is zero
+        for (int i = tid; i < MOE_MAX_ROWS / 32; i += 64 * kW) seen[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < active; i += 64 * kW)
+          atomicOr(&seen[a.active_rows[i] >> 5], 1u << (a.active_rows[i] & 31));
+        __syncthreads();
+        int left = e - active, word = 0;
+        uint32_t free = ~seen[0];
+        while (left >= __popc(free)) {
+          left -= __popc(free);
+          free = ~seen[++word];
+        }
+        for (; left > 0; --left) free &= free - 1;
+        row = 32 * word + __ffs(free) - 1;
+        m0 = m1 = 0;
+      }
     } else {
-      const int s = a.slots[min(m0 + B::row(c, lane), m1 - 1)];
-      const int64_t at = OP == kForward && a.by_token ? s / a.k : s;
-      sb[i] = (OP == kForward ? a.x + at * K * 2 : a.dy + at * N * 2) + 16 * B::gran(c, lane);
-      fb[i] = 16 * B::gran(c, lane);
+      const int active = *a.n_active;
+      tiles::build_tile_prefix<TB, kW>(a.row_off, active, tpre, wsum);
+      const int item = xcd_item(tpre[active] * tiles_a);
+      if (item < 0) return false;
+      // items of one expert: weight rows outermost, so that its tiles meet a block of
+      // weights together
+      const int e = tiles::row_of_tile(tpre, active, item / tiles_a);
+      const int local = item - tpre[e] * tiles_a, nt = tpre[e + 1] - tpre[e];
+      a0 = local / nt * TA;
+      b0 = 0;
+      m0 = a.row_off[e] + (local - local / nt * nt) * TB;
+      m1 = min(m0 + TB, a.row_off[e + 1]);
+      row = a.active_rows[e];
+    }
+    sum = OP == kForward ? a.K : OP == kInput ? a.N : m1 - m0;
+    steps = (sum + 63) / 64;
+    return true;
+  }
+
+  __device__ __forceinline__ void sources(const GroupedArgs& a) {
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int N = a.N, K = a.K;
+    const uint8_t* w = OP == kWeights ? nullptr : a.w + row * N * (int64_t)K * 2;
+    if constexpr (kTurnA) {
+      const int col = a0 + 8 * A::gran(wv, lane);
+      sa[0] = (OP == kInput ? w : a.x) + col * 2;
+      ina = col < K;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCopiesA; ++i)
+        sa[i] = w + (int64_t)min(a0 + A::row(wv + kW * i, lane), N - 1) * K * 2 +
+                16 * A::gran(0, lane);
+    }
+    if constexpr (kTurnB) {
+      const int col = b0 + 8 * B::gran(wv, lane);
+      sb[0] = a.dy + col * 2;
+      inb = col < N;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCopiesB; ++i) {
+        const int s = a.slots[min(m0 + B::row(wv + kW * i, lane), m1 - 1)];
+        const int64_t at = OP == kForward ? token(a, s) : s;
+        sb[i] = (OP == kForward ? a.x + at * K * 2 : a.dy + at * N * 2) + 16 * B::gran(0, lane);
+      }
     }
   }
-  auto copy1 = [&](uint8_t* buf, const uint8_t* p) {
-    asm volatile("" : "+v"(p));  // a select, not a branch around two copies
-    __builtin_amdgcn_global_load_lds(p, buf, 16, 0, 0);
+
+  // Half h of the ring: each thread's share of its slots, asked for and then kept.
+  struct Slots {
+    int v[(kHalf + 64 * kW - 1) / (64 * kW)];
   };
-  auto copy = [&](uint8_t* buf, int step) {
+  __device__ __forceinline__ Slots ask(const GroupedArgs& a, int h) const {
+    Slots s;
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(s.v) / 4); ++i)
+      s.v[i] = a.slots[m0 + min(h * kHalf + (int)threadIdx.x + 64 * kW * i, sum - 1)];
+    return s;
+  }
+  __device__ __forceinline__ void keep(const GroupedArgs& a, Ring& ring, int h,
+                                       const Slots& s) const {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(s.v) / 4); ++i) {
+      const int at = threadIdx.x + 64 * kW * i;
+      if (at < kHalf) {
+        ring.dy[(h & 1) * kHalf + at] = s.v[i];
+        ring.x[(h & 1) * kHalf + at] = token(a, s.v[i]);
+      }
+    }
+  }
+
+  // The copies of a step into buf, A's rows first; past the end of the sum zeros,
+  // which the products ignore.
+  __device__ __forceinline__ void copy(const GroupedArgs& a, const Ring& ring, uint8_t* buf,
+                                       int step) const {
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint8_t* p[kCopies];
 #pragma unroll
     for (int i = 0; i < kCopiesA; ++i) {
-      const int at = step * (kTurnA ? 64 : 128) + fa[i];
-      const uint8_t* p;
-      if constexpr (OP == kForward) {
-        p = at < 2 * sum ? sa[i] + step * 128 : kZeros;
+      if constexpr (kTurnA) {
+        const int at = step * 64 + A::row(wv + kW * i, lane);
+        int from = at;
+        if constexpr (OP == kWeights) from = ring.x[at & (2 * kHalf - 1)];
+        p[i] = at < sum && ina ? sa[0] + (int64_t)from * a.K * 2 : kZeros;
       } else {
-        int from = at;  // row of w, or of x
-        if constexpr (OP == kWeights) {
-          from = a.slots[m0 + (at < sum ? at : 0)];
-          if (a.by_token) from /= a.k;
-        }
-        p = at < sum && ina[i] ? sa[i] + (int64_t)from * K * 2 : kZeros;
+        p[i] = step * 128 + 16 * A::gran(0, lane) < 2 * sum ? sa[i] + (int64_t)step * 128 : kZeros;
       }
-      copy1(buf + 1024 * (wv + kW * i), p);
     }
 #pragma unroll
     for (int i = 0; i < kCopiesB; ++i) {
-      const int at = step * (kTurnB ? 64 : 128) + fb[i];
-      const uint8_t* p;
-      if constexpr (OP == kWeights) {
-        const int64_t from = a.slots[m0 + (at < sum ? at : 0)];
-        p = at < sum && inb[i] ? sb[i] + from * N * 2 : kZeros;
+      if constexpr (kTurnB) {
+        const int at = step * 64 + B::row(wv + kW * i, lane);
+        const int from = ring.dy[at & (2 * kHalf - 1)];
+        p[kCopiesA + i] = at < sum && inb ? sb[0] + (int64_t)from * a.N * 2 : kZeros;
       } else {
-        p = at < 2 * sum ? sb[i] + step * 128 : kZeros;
+        p[kCopiesA + i] =
+            step * 128 + 16 * B::gran(0, lane) < 2 * sum ? sb[i] + (int64_t)step * 128 : kZeros;
       }
-      copy1(buf + TA * 128 + 1024 * (wv + kW * i), p);
     }
-    __builtin_amdgcn_sched_barrier(0);
-  };
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      copy16(buf + (i < kCopiesA ? 0 : TA * 128) +
+                 1024 * (wv + kW * (i < kCopiesA ? i : i - kCopiesA)),
+             p[i]);
+    }
+  }
 
+  // Lane (r, q) of wavefront tile (wn, wm) holds result rows 16 i + 4 q + v of column
+  // 16 j + r.
+  template <int NF, int MF>
+  __device__ __forceinline__ void store(const GroupedArgs& a, const f32x4 (&acc)[NF][MF], int wn,
+                                        int wm) const {
+    const int r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+    const int width = OP == kForward ? a.N : a.K;
+    auto as = [&](auto type) {
+#pragma unroll
+      for (int j = 0; j < MF; ++j) {
+        const int at = (wm * MF + j) * 16 + r;
+        int64_t out;
+        if constexpr (OP == kWeights) {
+          if (b0 + at >= a.N) continue;
+          out = row * a.N + b0 + at;
+        } else {
+          if (m0 + at >= m1) continue;
+          out = a.slots[m0 + at];
+        }
+#pragma unroll
+        for (int i = 0; i < NF; ++i) {
+          const int n = a0 + (wn * NF + i) * 16 + 4 * q;
+          if (n >= width) continue;  // a multiple of 8
+          const f32x4 y = acc[i][j];
+          if constexpr (type() == MOE_DTYPE_F32)
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + out * a.ldy + n) = y;
+          else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + out * a.ldy + n) =
+                make_uint2(pack2<type()>(y[0], y[1]), pack2<type()>(y[2], y[3]));
+        }
+      }
+    };
+    if (a.dtype == MOE_DTYPE_BF16) as(std::integral_constant<int, MOE_DTYPE_BF16>());
+    else if (a.dtype == MOE_DTYPE_F16) as(std::integral_constant<int, MOE_DTYPE_F16>());
+    else as(std::integral_constant<int, MOE_DTYPE_F32>());
+  }
+
+  // The weights' gradients, which are many: whole lines with the streaming policy, so
+  // that they do not push the operands out of the L2 (64 rows of 2880 x 4096 in 32 bits,
+  // all of it: 1.63 ms with ordinary stores, 1.15 so). Lanes trade tiles until a store
+  // takes 128 bytes of a row: 64, as the tiles lie, are written at 3.8 TB/s with that
+  // policy instead of 6.6. Lanes r and r + 8 swap a tile of each pair; for 16-bit types,
+  // whose rows are half as long, lanes r and 7 - r then swap a pair of each two.
+  template <int DT, int NF, int MF>
+  __device__ __forceinline__ void store_lines(const GroupedArgs& a, const f32x4 (&acc)[NF][MF],
+                                              int wn, int wm) const {
+    constexpr bool kWide = DT == MOE_DTYPE_F32;
+    constexpr int kWords = kWide ? 4 : 2;  // of 4 outputs
+    typedef uint32_t words __attribute__((ext_vector_type(kWords)));
+    const int r = threadIdx.x & 15, q = (threadIdx.x & 63) >> 4;
+    const bool low = r < 8, left = !(r & 4);
+    auto pack = [](const f32x4& v) {
+      words w;
+      if constexpr (kWide) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
+      } else {
+        w[0] = pack2<DT>(v[0], v[1]);
+        w[1] = pack2<DT>(v[2], v[3]);
+      }
+      return w;
+    };
+    // x where mine, else the other lane's y; every lane takes part in the exchange
+    auto swap = [](auto ctrl, bool mine, const words& x, const words& y) {
+      words w;
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const uint32_t other = from_lane<ctrl()>(y[i]);
+        w[i] = mine ? x[i] : other;
+      }
+      return w;
+    };
+    auto put = [&](int at, int n, const words& w) {
+      if (at < a.N && n < a.K)  // K is a multiple of 8
+        __builtin_nontemporal_store(
+            w, reinterpret_cast<words*>(static_cast<uint8_t*>(a.y) +
+                                        ((row * a.N + at) * a.ldy + n) * (kWide ? 4 : 2)));
+    };
+    constexpr std::integral_constant<int, kRor8> ror8;
+    constexpr std::integral_constant<int, kHalfMirror> mirror;
+#pragma unroll
+    for (int j = 0; j < MF; ++j) {
+      const int at = b0 + (wm * MF + j) * 16;
+#pragma unroll
+      for (int i = 0; i < NF; i += kWide ? 2 : 4) {
+        words two[2][2];  // [pair][rows r & 7, and 8 on] of tile 2 pair + r / 8
+#pragma unroll
+        for (int p = 0; p < (kWide ? 1 : 2); ++p) {
+          const words x = pack(acc[i + 2 * p][j]), y = pack(acc[i + 2 * p + 1][j]);
+          two[p][0] = swap(ror8, low, x, y);
+          two[p][1] = swap(ror8, !low, y, x);
+        }
+        if constexpr (kWide) {
+          const int n = a0 + (wn * NF + i + r / 8) * 16 + 4 * q;
+          put(at + (r & 7), n, two[0][0]);
+          put(at + (r & 7) + 8, n, two[0][1]);
+        } else {
+          const int n = a0 + (wn * NF + i + (left ? 0 : 2) + r / 8) * 16 + 4 * q;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // rows 0 .. 3, then 4 .. 7 of the 8
+            put(at + 8 * h + (left ? r & 3 : 7 - (r & 7)), n,
+                swap(mirror, left, two[0][h], two[1][h]));
+            put(at + 8 * h + (left ? 7 - (r & 7) : r & 7), n,
+                swap(mirror, !left, two[1][h], two[0][h]));
+          }
+        }
+      }
+    }
+  }
+};
+
+// Tiles of the kernels for groups of many rows.
+constexpr int kWideA = 256, kWideB = 128;
+
+// TA x TB result tile, WA x WB wavefronts, 3 buffers.
+template <int OP, int DT, int TA, int TB, int WA, int WB>
+__global__ __launch_bounds__(64 * WA * WB, (TA + TB) * 384 > 80 << 10 ? WA * WB / 4 : WA * WB / 2)
+void grouped(GroupedArgs a, int tiles_a, int tiles_b) {
+  constexpr int kW = WA * WB, kRows = TA + TB;
+  constexpr int NF = TA / WA / 16, MF = TB / WB / 16;  // MFMA tiles per wavefront
+  using T = Tile<OP, TA, TB, kW>;
+  __shared__ __align__(128) uint8_t buf0[kRows * 128];
+  __shared__ __align__(128) uint8_t buf1[kRows * 128];
+  __shared__ __align__(128) uint8_t buf2[kRows * 128];
+  __shared__ typename T::Ring ring;
+  __shared__ uint32_t seen[OP == kWeights ? MOE_MAX_ROWS / 32 : 1];
+  __shared__ int wsum[kW];
+  extern __shared__ int tpre[];  // [n_active + 1]
+
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wv % WA, wm = wv / WA, r = lane & 15, q = lane >> 4;
+  T t;
+  if (!t.init(a, tiles_a, tiles_b, tpre, wsum, seen)) return;  // the whole workgroup
   f32x4 acc[NF][MF];
 #pragma unroll
   for (int i = 0; i < NF; ++i)
@@ -247,9 +423,10 @@ __global__ __launch_bounds__(64 * WA * WB,
     for (int half = 0; half < 2; ++half) {
       i32x4 bf[MF], af[NF];
 #pragma unroll
-      for (int j = 0; j < MF; ++j) bf[j] = B::frag(buf + TA * 128, (wm * MF + j) * 16, half, r, q);
+      for (int j = 0; j < MF; ++j)
+        bf[j] = T::B::frag(buf + TA * 128, (wm * MF + j) * 16, half, r, q);
 #pragma unroll
-      for (int i = 0; i < NF; ++i) af[i] = A::frag(buf, (wn * NF + i) * 16, half, r, q);
+      for (int i = 0; i < NF; ++i) af[i] = T::A::frag(buf, (wn * NF + i) * 16, half, r, q);
 #pragma unroll
       for (int i = 0; i < NF; ++i)
 #pragma unroll
@@ -257,84 +434,400 @@ __global__ __launch_bounds__(64 * WA * WB,
     }
   };
 
-  const int steps = (sum + 63) / 64;
-  if (steps > 0) {  // the whole workgroup
-    // past the end of the sum a copy brings zeros, which the products ignore
+  if (t.steps > 0) {  // the whole workgroup
+    t.sources(a);
+    typename T::Slots slots;
+    if constexpr (OP == kWeights) {
+      const typename T::Slots first = t.ask(a, 0), second = t.ask(a, 1);
+      t.keep(a, ring, 0, first);
+      t.keep(a, ring, 1, second);
+      __syncthreads();
+    }
+    // the copies of step s; where they are the first of a half of the ring, the other
+    // half is free for the slots after it, which arrive a step later
+    auto copy = [&](uint8_t* buf, int s) {
+      t.copy(a, ring, buf, s);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (OP == kWeights) {
+        if (s >= kHalf / 64 && s < t.steps) {
+          if ((s & (kHalf / 64 - 1)) == 0) slots = t.ask(a, s / (kHalf / 64) + 1);
+          if ((s & (kHalf / 64 - 1)) == 1) t.keep(a, ring, s / (kHalf / 64) + 1, slots);
+        }
+      }
+    };
     copy(buf0, 0);
     copy(buf1, 1);
-    if constexpr (S > 3) copy(buf2, 2);
-    for (int s = 0; s < steps; s += S) {
-      // each step: its copies (the oldest) have arrived for every wavefront, and
-      // the buffer the last step read is free for the copies S - 1 steps ahead
-      tile_barrier(vm_lds((S - 2) * kCopies));
-      copy(S == 3 ? buf2 : buf3, s + S - 1);
+    for (int s = 0; s < t.steps; s += 3) {
+      // each step: its copies (the oldest) have arrived for every wavefront, and the
+      // buffer the last step read is free for the copies 2 steps ahead
+      tile_barrier(vm_lds(T::kCopies));
+      copy(buf2, s + 2);
       compute(buf0);
-      tile_barrier(vm_lds((S - 2) * kCopies));
-      copy(buf0, s + S);
+      tile_barrier(vm_lds(T::kCopies));
+      copy(buf0, s + 3);
       compute(buf1);
-      tile_barrier(vm_lds((S - 2) * kCopies));
-      copy(buf1, s + S + 1);
+      tile_barrier(vm_lds(T::kCopies));
+      copy(buf1, s + 4);
       compute(buf2);
-      if constexpr (S > 3) {
-        tile_barrier(vm_lds((S - 2) * kCopies));
-        copy(buf2, s + S + 2);
-        compute(buf3);
-      }
     }
     __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
   }
-
-  // lane (r, q): result rows 16 i + 4 q + v of column 16 j + r
-  auto store = [&](auto type) {
-#pragma unroll
-    for (int j = 0; j < MF; ++j) {
-      const int at = (wm * MF + j) * 16 + r;
-      int64_t out;
-      if constexpr (OP == kWeights) {
-        if (b0 + at >= N) continue;
-        out = row * N + b0 + at;
-      } else {
-        if (m0 + at >= m1) continue;
-        out = a.slots[m0 + at];
-      }
-#pragma unroll
-      for (int i = 0; i < NF; ++i) {
-        const int n = a0 + (wn * NF + i) * 16 + 4 * q;
-        if (n >= width) continue;  // a multiple of 8
-        const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
-        store4<type(), true>(a, out, n, y);
-      }
-    }
-  };
-  if (a.dtype == MOE_DTYPE_BF16) store(std::integral_constant<int, MOE_DTYPE_BF16>());
-  else if (a.dtype == MOE_DTYPE_F16) store(std::integral_constant<int, MOE_DTYPE_F16>());
-  else store(std::integral_constant<int, MOE_DTYPE_F32>());
+  t.store(a, acc, wn, wm);
 }
 
-template <int OP, int DT, int TA, int TB, int WA, int WB, int S>
-hipError_t go(const GroupedArgs& a, hipStream_t stream) {
-  const int64_t tiles_a = ((OP == kForward ? a.N : a.K) + TA - 1) / TA;
-  int64_t tiles, tiles_b = 0, lds = 0;
-  if (OP == kWeights) {
-    tiles_b = (a.N + TB - 1) / TB;
-    tiles = a.n_rows * tiles_a * tiles_b;
-  } else {
-    // at most one part-filled tile per active row
-    const int64_t cap = a.n_rows < a.M ? a.n_rows : a.M;
-    tiles = (cap + a.M / TB) * tiles_a;
-    lds = (cap + 1) * sizeof(int);
+// Operands in steps of 32 elements, for the wide tiles. Along: rows of 64 bytes, 16 to a
+// copy, swizzled as above.
+template <int ROWS>
+struct Along32 {
+  static constexpr int kBytes = ROWS * 64;
+  static __device__ __forceinline__ int row(int c, int lane) { return 16 * c + (lane >> 2); }
+  static __device__ __forceinline__ int gran(int, int lane) { return (lane & 3) ^ (lane >> 3 & 3); }
+  static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int at, int r, int q) {
+    const int row = at + r;
+    return *reinterpret_cast<const i32x4*>(buf + row * 64 + 16 * (q ^ (row >> 1 & 3)));
   }
-  hipLaunchKernelGGL((grouped<OP, DT, TA, TB, WA, WB, S>),
-                     dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds)), dim3(64 * WA * WB), lds,
-                     stream, a, (int)tiles_a, (int)tiles_b);
+};
+// Across: // 32 rows of the sum's axis. A copy is followed by 32 bytes that nothing uses,
+// and brings rows that no read joins, so that the 8 rows that 32 lanes read at once lie
+// in different banks and a lane's addresses are one and constants (swizzled chunks
+// would take a register or an operation each). Place p of a row: copy p % kCopies,
+// part p / kCopies of it. Lane (r, q) reads rows 8 q + r / 4 + 4 i, i = 0, 1, as the
+// operand beside it holds them (PAIRED), or 4 q + r / 4 + 16 i where both are across.
+template <int COLS, bool PAIRED>
+struct Across32 {
+  static constexpr int kGran = COLS / 8, kCopies = COLS / 16, kCopy = 1024 + 32;
+  static constexpr int kBytes = kCopies * kCopy;
+  static_assert(COLS == 256 || (COLS == 128 && !PAIRED), "places of the rows");
+  static __device__ __forceinline__ int row(int c, int lane) {
+    const int p = c + kCopies * (lane / kGran);
+    return PAIRED ? (p & 19) | (p & 4) << 1 | (p & 8) >> 1 : p;
+  }
+  static __device__ __forceinline__ int gran(int lane) { return lane % kGran; }
+  static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int at, int r, int q) {
+    uint64_t v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // PAIRED: row 8 q + r / 4 + 4 i is in place r / 4 + 4 (q & 1) + 8 i + 16 (q / 2)
+      const int p = (r >> 2) + (PAIRED ? 4 * (q & 1) + 8 * i + 16 * (q >> 1) : 4 * q + 16 * i);
+      v[i] = read_turned(buf + p % kCopies * kCopy + p / kCopies * (2 * COLS) + 2 * at +
+                         8 * (r & 3));
+    }
+    return i32x4{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
+  }
+};
+
+// 16 bytes per lane from base + off to LDS, zeros where off is not below bytes. base and
+// bytes are the same in all lanes.
+__device__ __forceinline__ void copy16(uint8_t* buf, const uint8_t* base, uint32_t bytes,
+                                       uint32_t off) {
+  auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes, 0x27000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      rsrc, (__attribute__((address_space(3))) void*)buf, 16, off, 0, 0, 0);
+}
+
+// The same for groups of many rows, in 256 x 128 tiles. Forward: 8 wavefronts (2 x 4) of
+// 128 x 32 outputs, 3 buffers. The operands of the next half step are read from LDS,
+// spread between the products of this one; the one barrier per step sits between its
+// halves, after the last read of the step's buffer, which then takes the copies for the
+// step 3 steps on (as in gemm_i8_big).
+template <int DT>
+__global__ __launch_bounds__(512, 2) void grouped_forward(GroupedArgs a, int tiles_a) {
+  constexpr int TA = kWideA, TB = kWideB, WA = 2, NF = TA / WA / 16, MF = TB / 4 / 16;
+  using T = Tile<kForward, TA, TB, 8>;
+  __shared__ __align__(128) uint8_t buf0[(TA + TB) * 128];
+  __shared__ __align__(128) uint8_t buf1[(TA + TB) * 128];
+  __shared__ __align__(128) uint8_t buf2[(TA + TB) * 128];
+  __shared__ int wsum[8];
+  extern __shared__ int tpre[];  // [n_active + 1]
+
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wv % WA, wm = wv / WA, r = lane & 15, q = lane >> 4;
+  T t;
+  if (!t.init(a, tiles_a, 1, tpre, wsum, nullptr)) return;  // the whole workgroup
+  t.sources(a);
+  f32x4 acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  struct Frags {
+    i32x4 b[MF], a[NF];
+  };
+  auto read = [&](const uint8_t* buf, int half, Frags& f) {
+#pragma unroll
+    for (int j = 0; j < MF; ++j)
+      f.b[j] = T::B::frag(buf + TA * 128, (wm * MF + j) * 16, half, r, q);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) f.a[i] = T::A::frag(buf, (wn * NF + i) * 16, half, r, q);
+  };
+  auto mul = [&](const Frags& f) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < MF; ++j) acc[i][j] = mfma<DT>(f.a[i], f.b[j], acc[i][j]);
+  };
+  auto spread = [&](bool copies) {
+    constexpr int kOps = NF + MF, kMul = NF * MF;
+#pragma unroll
+    for (int i = 0; i < kOps; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (copies && i < T::kCopies) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kMul / kOps, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, kMul % kOps, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  Frags f0, f1;
+  int s = 0;
+  // the step out of `here`, f0 its first half's operands. False after the last
+  auto step = [&](uint8_t* here, const uint8_t* next) {
+    read(here, 1, f1);
+    mul(f0);
+    spread(false);
+    tile_barrier(vm_lds(T::kCopies));  // the next step's copies have arrived
+    t.copy(a, NoRing(), here, s + 3);
+    read(next, 0, f0);
+    mul(f1);
+    spread(true);
+    return ++s < t.steps;
+  };
+  t.copy(a, NoRing(), buf0, 0);
+  t.copy(a, NoRing(), buf1, 1);
+  t.copy(a, NoRing(), buf2, 2);
+  tile_barrier(vm_lds(2 * T::kCopies));
+  read(buf0, 0, f0);
+  while (step(buf0, buf1) && step(buf1, buf2) && step(buf2, buf0)) {
+  }
+  __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
+  t.store(a, acc, wn, wm);
+}
+
+// The gradients: 4 wavefronts (2 x 2) of 128 x 64 outputs and steps of 32 elements, two
+// workgroups per CU, so that one's start and end run beside the other's products. The
+// operands of the next step are read from LDS, spread between the products of this one,
+// whose buffer then takes the copies for the step 3 steps on; one barrier per step.
+template <int OP, int DT>
+__global__ __launch_bounds__(256, 2) void grouped_gradient(GroupedArgs a, int tiles_a,
+                                                             int tiles_b) {
+  constexpr int TA = kWideA, TB = kWideB, NF = 8, MF = 4;
+  constexpr int kW = 4;
+  using T = Tile<OP, TA, TB, kW>;
+  using A = Across32<TA, OP == kInput>;
+  using B = std::conditional_t<T::kTurnB, Across32<TB, false>, Along32<TB>>;
+  constexpr int kBytesA = A::kBytes, kBytesB = B::kBytes;
+  constexpr int kCopiesA = TA / 64, kCopiesB = TB / 64, kCopies = kCopiesA + kCopiesB;
+  __shared__ __align__(128) uint8_t buf0[kBytesA + kBytesB];
+  __shared__ __align__(128) uint8_t buf1[kBytesA + kBytesB];
+  __shared__ __align__(128) uint8_t buf2[kBytesA + kBytesB];
+  __shared__ typename T::Ring ring;
+  __shared__ uint32_t seen[OP == kWeights ? MOE_MAX_ROWS / 32 : 1];
+  __shared__ int wsum[kW];
+  extern __shared__ int tpre[];  // [n_active + 1]
+
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wv & 1, wm = wv >> 1, r = lane & 15, q = lane >> 4;
+  const int N = a.N, K = a.K;
+  T t;
+  if (!t.init(a, tiles_a, tiles_b, tpre, wsum, seen)) return;  // the whole workgroup
+  f32x4 acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  if (t.sum > 0) {  // the whole workgroup
+    const int steps = (t.sum + 31) / 32;
+    constexpr uint32_t kOutside = 1u << 31;  // above the bytes of any copy
+    uint32_t offa[kCopiesA];
+    const uint8_t *base = nullptr, *sa = nullptr, *sb[kCopiesB];
+    bool inb = true;
+    const int col = t.a0 + 8 * A::gran(lane);
+    const bool ina = col < K;
+    if constexpr (OP == kInput) {
+      base = a.w + t.row * N * (int64_t)K * 2;
+#pragma unroll
+      for (int i = 0; i < kCopiesA; ++i)
+        offa[i] = ina ? A::row(wv + kW * i, lane) * K * 2 + col * 2 : kOutside;
+    } else {
+      sa = a.x + col * 2;
+    }
+    if constexpr (OP == kWeights) {
+      const int col = t.b0 + 8 * B::gran(lane);
+      sb[0] = a.dy + col * 2;
+      inb = col < N;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCopiesB; ++i) {
+        const int s = a.slots[min(t.m0 + B::row(wv + kW * i, lane), t.m1 - 1)];
+        sb[i] = a.dy + (int64_t)s * N * 2 + 16 * B::gran(0, lane);
+      }
+    }
+    typename T::Slots slots;
+    if constexpr (OP == kWeights) {
+      const typename T::Slots first = t.ask(a, 0), second = t.ask(a, 1);
+      t.keep(a, ring, 0, first);
+      t.keep(a, ring, 1, second);
+      __syncthreads();
+    }
+    auto copy = [&](uint8_t* buf, int s) {
+      if constexpr (OP == kInput) {
+        const int left = min(max(N - 32 * s, 0), 32);
+#pragma unroll
+        for (int i = 0; i < kCopiesA; ++i)
+          copy16(buf + A::kCopy * (wv + kW * i), base + (int64_t)s * 32 * K * 2,
+                 (uint32_t)left * K * 2, offa[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kCopiesA; ++i) {
+          const int at = s * 32 + A::row(wv + kW * i, lane);
+          const int64_t from = ring.x[at & (2 * kHalf - 1)];
+          copy16(buf + A::kCopy * (wv + kW * i), at < t.sum && ina ? sa + from * K * 2 : kZeros);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kCopiesB; ++i) {
+        if constexpr (OP == kWeights) {
+          const int at = s * 32 + B::row(wv + kW * i, lane);
+          const int64_t from = ring.dy[at & (2 * kHalf - 1)];
+          copy16(buf + kBytesA + B::kCopy * (wv + kW * i),
+                 at < t.sum && inb ? sb[0] + from * N * 2 : kZeros);
+        } else {
+          const bool in = s * 64 + 16 * B::gran(0, lane) < 2 * t.sum;
+          copy16(buf + kBytesA + 1024 * (wv + kW * i), in ? sb[i] + (int64_t)s * 64 : kZeros);
+        }
+      }
+    };
+    // where the copies of step s are the first of a half of the ring, the other half is
+    // free for the slots after it, which arrive a step later
+    auto refill = [&](int s) {
+      if constexpr (OP == kWeights) {
+        if (s >= kHalf / 32 && s < steps) {
+          if ((s & (kHalf / 32 - 1)) == 0) slots = t.ask(a, s / (kHalf / 32) + 1);
+          if ((s & (kHalf / 32 - 1)) == 1) t.keep(a, ring, s / (kHalf / 32) + 1, slots);
+        }
+      }
+    };
+    struct Frags {
+      i32x4 b[MF], a[NF];
+    };
+    auto read = [&](const uint8_t* buf, Frags& f) {
+#pragma unroll
+      for (int j = 0; j < MF; ++j) f.b[j] = B::frag(buf + kBytesA, (wm * MF + j) * 16, r, q);
+#pragma unroll
+      for (int i = 0; i < NF; ++i) f.a[i] = A::frag(buf, (wn * NF + i) * 16, r, q);
+    };
+    auto mul = [&](const Frags& f) {
+#pragma unroll
+      for (int i = 0; i < NF; ++i)
+#pragma unroll
+        for (int j = 0; j < MF; ++j) acc[i][j] = mfma<DT>(f.a[i], f.b[j], acc[i][j]);
+    };
+    auto spread = [&]() {
+      constexpr int kOps = NF * 2 + MF * (T::kTurnB ? 2 : 1), kMul = NF * MF;
+#pragma unroll
+      for (int i = 0; i < kOps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (i < kCopies) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, kMul / kOps, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, kMul % kOps, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    Frags f0, f1;
+    int s = 0;
+    // the step whose operands are in f, out of `here`; the next one's go into g. False
+    // after the last
+    auto step = [&](uint8_t* here, const uint8_t* next, const Frags& f, Frags& g) {
+      tile_barrier(vm_lds(kCopies));  // the next step's copies have arrived
+      copy(here, s + 3);
+      read(next, g);
+      mul(f);
+      spread();
+      refill(s + 3);
+      return ++s < steps;
+    };
+    copy(buf0, 0);
+    copy(buf1, 1);
+    copy(buf2, 2);
+    tile_barrier(vm_lds(2 * kCopies));
+    read(buf0, f0);
+    while (step(buf0, buf1, f0, f1) && step(buf1, buf2, f1, f0) && step(buf2, buf0, f0, f1) &&
+           step(buf0, buf1, f1, f0) && step(buf1, buf2, f0, f1) && step(buf2, buf0, f1, f0)) {
+    }
+    __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
+  }
+  if constexpr (OP == kInput) t.store(a, acc, wn, wm);
+  else if (a.dtype == MOE_DTYPE_F32) t.template store_lines<MOE_DTYPE_F32>(a, acc, wn, wm);
+  else if (a.dtype == MOE_DTYPE_BF16) t.template store_lines<MOE_DTYPE_BF16>(a, acc, wn, wm);
+  else t.template store_lines<MOE_DTYPE_F16>(a, acc, wn, wm);
+}
+
+struct Grid {
+  int64_t tiles_a, tiles_b, tiles, lds;
+};
+// Grouped rows: at most one part-filled tile per active row.
+Grid grid_of(const GroupedArgs& a, int ta, int tb) {
+  const int64_t tiles_a = ((a.op == kForward ? a.N : a.K) + ta - 1) / ta;
+  if (a.op == kWeights) {
+    const int64_t tiles_b = (a.N + tb - 1) / tb;
+    return {tiles_a, tiles_b, a.n_rows * tiles_a * tiles_b, 0};
+  }
+  const int64_t cap = a.n_rows < a.M ? a.n_rows : a.M;
+  return {tiles_a, 1, (cap + a.M / tb) * tiles_a, (cap + 1) * (int64_t)sizeof(int)};
+}
+
+template <int OP, int DT, int TA, int TB, int WA, int WB>
+hipError_t go(const GroupedArgs& a, hipStream_t stream) {
+  const Grid g = grid_of(a, TA, TB);
+  hipLaunchKernelGGL((grouped<OP, DT, TA, TB, WA, WB>),
+                     dim3((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds)), dim3(64 * WA * WB),
+                     g.lds, stream, a, (int)g.tiles_a, (int)g.tiles_b);
   return hipGetLastError();
+}
+
+template <int OP, int DT>
+hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
+  const Grid g = grid_of(a, kWideA, kWideB);
+  const dim3 blocks((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds));
+  if constexpr (OP == kForward)
+    hipLaunchKernelGGL((grouped_forward<DT>), blocks, dim3(512), g.lds, stream, a, (int)g.tiles_a);
+  else
+    hipLaunchKernelGGL((grouped_gradient<OP, DT>), blocks, dim3(256), g.lds, stream, a,
+                       (int)g.tiles_a, (int)g.tiles_b);
+  return hipGetLastError();
+}
+
+// Wide tiles where they fill the card (forward one workgroup per CU, the gradients two)
+// and, but for the weights' gradient, an expert has rows for them. us, small tiles / wide
+// ones: forward 2880 x 4096, 64 experts, 48 rows each 298 / 337, 96 400 / 373, 384 1000 /
+// 780; 4096 x 2880, 8 experts, 96 rows (128 wide tiles) 36 / 47, 192 60 / 52; 512 x 512, 16
+// experts, 3072 rows 66 / 74. Input 2880 x 4096, 64 experts, 12 rows 263 / 276, 24 287 / 275,
+// 384 970 / 710; 8 experts, 192 rows (192 wide tiles) 73 / 85. Weights 2880 x 4096, 64
+// experts, 12 rows 975 / 470, 384 2250 / 1140; 1024 x 1024, 4 experts (128 wide tiles), 256
+// rows 11 / 15, 4096 75 / 143.
+bool use_wide(const GroupedArgs& a) {
+  const Grid g = grid_of(a, kWideA, kWideB);
+  const int64_t cus = device_cus(), cap = a.n_rows < a.M ? a.n_rows : a.M;
+  const size_t fixed = a.op == kForward ? 3 * (kWideA + kWideB) * 128 + 256 : 78 << 10;
+  if (g.lds + fixed > (a.op == kForward ? device_lds_per_block() : 80 << 10)) return false;
+  switch (a.op) {
+    case kForward: return a.M >= 96 * cap && g.tiles >= cus && a.K >= 1024;
+    case kInput: return a.M >= 24 * cap && g.tiles >= 2 * cus;
+    default: return g.tiles >= 2 * cus;
+  }
 }
 
 template <int DT>
 hipError_t pick(const GroupedArgs& a, hipStream_t s) {
-  if (a.op == kForward) return go<kForward, DT, 128, 64, 4, 2, 3>(a, s);
-  if (a.op == kInput) return go<kInput, DT, 128, 64, 4, 2, 3>(a, s);
-  return go<kWeights, DT, 128, 128, 4, 2, 3>(a, s);
+  const bool wide = use_wide(a);
+  switch (a.op) {
+    case kForward:
+      return wide ? go_wide<kForward, DT>(a, s) : go<kForward, DT, 128, 64, 4, 2>(a, s);
+    case kInput: return wide ? go_wide<kInput, DT>(a, s) : go<kInput, DT, 128, 64, 4, 2>(a, s);
+    default: return wide ? go_wide<kWeights, DT>(a, s) : go<kWeights, DT, 128, 128, 4, 2>(a, s);
+  }
 }
 
 }  // namespace

@@ -111,14 +111,15 @@ inline int f8_blocks(int n) { return (n + MOE_F8_BLOCK - 1) / MOE_F8_BLOCK; }
 
 // Products grouped by expert (grouped_linear.hip): op 0 forward, 1 the input's
 // gradient, 2 the weights' gradient. Rows of one expert are the slots that the split
-// lists for it; x holds a row per token (by_token) or per slot, dy, y and dx a row
-// per slot.
+// lists for it; x holds a row per token (by_token = ceil(2^32 / k)) or per slot
+// (by_token = 0, also for k = 1), dy, y and dx a row per slot.
 struct GroupedArgs {
   int op, elem;  // elem: type of w, x and dy (bf16 or fp16)
   const uint8_t *w, *x, *dy;
   int M, N, K;  // M = T * k, a bound on the slots
   const int32_t *n_active, *active_rows, *row_off, *slots;  // n_active null: no slots
-  int n_rows, k, by_token;
+  int n_rows;
+  uint32_t by_token;
   void* y;  // y, dx or dw
   int dtype;
   int64_t ldy;

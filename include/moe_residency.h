@@ -575,8 +575,9 @@ int moe_expert_ffn_f8(const moe_bank *bank, moe_split split, const uint8_t *xq, 
  * the output's type. Only the split's slots of y and dx are written. by_token:
  * slot s reads row s / k of x, [T][K] (a token's row is shared by its k picks; the
  * gradient of such a row is the sum of dx over the token's slots, for bf16
- * moe_finalize with weights 1); else row s of x, [T*k][K]. The sums have one order,
- * given by the slots' order and the shapes, so the bits depend on no step or grid.
+ * moe_finalize with weights 1); else row s of x, [T*k][K]. The sums of y and dx have
+ * one order, so their bits depend on no bank, step size or place in a step; those of
+ * dw one order for the slots' order and the call's sizes.
  *
  * dtype: type of x, w and dy, MOE_DTYPE_BF16 or MOE_DTYPE_F16; ydtype, xdtype,
  * wdtype: that of the output, any. w: [n_rows][N][K], device, or with on_host =
