@@ -22,6 +22,8 @@
 //
 // Copies, buffers, swizzle and the order of tiles are those of gemm_i8_tile: a
 // step takes 128 bytes, so one block, of each row of the tile.
+#include <algorithm>
+
 #include "gemm_tile.h"
 #include "mxfp4_common.h"
 #include "tile_items.h"
@@ -165,19 +167,19 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_f8_tile(F8Args
     for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
   const int wn = wv % WN, wm = wv / WN, r = lane & 15, q = lane >> 4;
 
-  // scales of S steps at a time: lane (r, q) holds those of step s + q for the
-  // rows 16 j + r of its tiles, 0 past the end of K (the copies bring zeros there)
+  // scales of S steps at a time: lane (r, q) holds those of step s + q for the rows 16 j
+  // + r of its tiles, taken as 0 past the end of K (the copies bring zeros there) only
+  // once they are used: a select at the loads would wait for them, and for every copy
   const float* xs[MF];
 #pragma unroll
   for (int j = 0; j < MF; ++j)
     xs[j] = a.sa + arow(min(m0 + (wm * MF + j) * 16 + r, m1 - 1)) * blocks;
   auto scales = [&](int s, float (&x)[MF], float (&v)[kSides]) {
     const int b = min(s + q, blocks - 1);
-    const bool in = s + q < blocks;
 #pragma unroll
-    for (int j = 0; j < MF; ++j) x[j] = in ? xs[j][b] : 0.0f;
+    for (int j = 0; j < MF; ++j) x[j] = xs[j][b];
 #pragma unroll
-    for (int h = 0; h < kSides; ++h) v[h] = in ? sw[h * nblocks * (int64_t)blocks + b] : 0.0f;
+    for (int h = 0; h < kSides; ++h) v[h] = sw[h * nblocks * (int64_t)blocks + b];
   };
   float nx[MF], nw[kSides], cur[kSides][MF];
 
@@ -220,7 +222,7 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_f8_tile(F8Args
 #pragma unroll
     for (int h = 0; h < kSides; ++h)
 #pragma unroll
-      for (int j = 0; j < MF; ++j) cur[h][j] = nx[j] * nw[h];
+      for (int j = 0; j < MF; ++j) cur[h][j] = s + q < blocks ? nx[j] * nw[h] : 0.0f;
     scales(s + S, nx, nw);
     // each step: its copies (the oldest) have arrived for every wavefront, and
     // the buffer the last step read is free for the copies S - 1 steps ahead
@@ -279,6 +281,203 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_f8_tile(F8Args
   }
 }
 
+// Dense products with 16-bit outputs, large enough to fill the card with wide tiles: 8
+// wavefronts (2 x 4) of TN/2 x TM/4 outputs, S buffers of 128 bytes, one block, per row.
+// The weights' operand of two tiles on is read from LDS while a row of tiles is
+// multiplied, and the row before it is scaled and added; the one barrier per step sits
+// after the last read of the step's buffer. Copies go out one row of tiles at a time: a
+// step's, asked for at once by all wavefronts, hold the products up.
+template <int TN, int TM, int S>
+__global__ __launch_bounds__(512, 2) void gemm_f8_big(F8Args a, int tiles_n) {
+  constexpr int WN = 2, WM = 4, kW = 8;
+  constexpr int kCopiesA = TN / 8 / kW, kCopiesB = TM / 8 / kW, kCopies = kCopiesA + kCopiesB;
+  static_assert(TN % (8 * kW) == 0 && TM % (8 * kW) == 0 && (S == 2 || S == 3), "whole copies");
+  constexpr int NF = TN / WN / 16, MF = TM / WM / 16;
+  static_assert(128 % (TN / WN) == 0, "a wavefront's weight rows lie in one block");
+  __shared__ __align__(128) uint8_t buf0[(TN + TM) * 128];
+  __shared__ __align__(128) uint8_t buf1[(TN + TM) * 128];
+  __shared__ __align__(128) uint8_t buf2[S > 2 ? (TN + TM) * 128 : 16];
+  const int lane = threadIdx.x & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wv % WN, wm = wv / WN, r = lane & 15, q = lane >> 4;
+  const int N = a.N, K = a.K, M = a.M, blocks = (K + 127) / 128;
+  // items in groups of 8 rows of tiles, column by column, so that an XCD's share is
+  // about square and its L2 meets few rows of either operand
+  const int tiles_m = (M + TM - 1) / TM;
+  const int item = xcd_item(tiles_m * tiles_n);
+  if (item < 0) return;
+  const int group = item / (8 * tiles_n), local = item - group * 8 * tiles_n;
+  const int gm = min(8, tiles_m - 8 * group);
+  const int m0 = (8 * group + local % gm) * TM, n0 = local / gm * TN;
+
+  constexpr uint32_t kOutside = 1u << 31;  // above the bytes of any copy
+  const int gran = (lane & 7) ^ (lane >> 3);
+  const uint8_t *wbase = a.w + (int64_t)n0 * K, *abase = a.a + m0 * a.lda;
+  uint32_t offa[kCopiesA], offb[kCopiesB];
+#pragma unroll
+  for (int i = 0; i < kCopiesA; ++i)
+    offa[i] = min(8 * (wv + kW * i) + (lane >> 3), N - 1 - n0) * K + 16 * gran;
+#pragma unroll
+  for (int i = 0; i < kCopiesB; ++i)
+    offb[i] = min(8 * (wv + kW * i) + (lane >> 3), M - 1 - m0) * (int)a.lda + 16 * gran;
+  // copies [from, to) of step s's: weights first
+  auto copy = [&](uint8_t* buf, int s, int from, int to) __attribute__((always_inline)) {
+    const bool in = s * 128 + 16 * gran < K;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      if (i < from || i >= to) continue;
+      if (i < kCopiesA)
+        copy16(buf + 1024 * (wv + kW * i), wbase + (int64_t)s * 128, kOutside,
+               in ? offa[i < kCopiesA ? i : 0] : kOutside);
+      else
+        copy16(buf + TN * 128 + 1024 * (wv + kW * (i - kCopiesA)), abase + (int64_t)s * 128,
+               kOutside, in ? offb[i < kCopiesA ? 0 : i - kCopiesA] : kOutside);
+    }
+  };
+
+  // scales of 4 steps at a time, as in gemm_f8_tile
+  const int block = min((n0 + wn * (TN / WN)) / 128, (N - 1) / 128);
+  const float* sw = a.sw + block * (int64_t)blocks;
+  const float* sbase = a.sa + m0 * (int64_t)blocks;
+  uint32_t offs[MF];
+#pragma unroll
+  for (int j = 0; j < MF; ++j)
+    offs[j] = min((wm * MF + j) * 16 + r, M - 1 - m0) * blocks;
+  float nx[MF], nw, cur[MF];
+  auto scales = [&](int s) {
+    const int b = min(s + q, blocks - 1);
+#pragma unroll
+    for (int j = 0; j < MF; ++j) nx[j] = sbase[offs[j] + b];
+    nw = sw[b];
+  };
+  auto take = [&](int s) {
+    const bool in = s + q < blocks;
+#pragma unroll
+    for (int j = 0; j < MF; ++j) cur[j] = in ? nx[j] * nw : 0.0f;
+  };
+
+  f32x4 acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  using F = Frag<false>;
+  const int off0 = r * 128 + 16 * (q ^ (r & 7)), off1 = r * 128 + 16 * ((4 + q) ^ (r & 7));
+  auto frag = [&](const uint8_t* p) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(p + off0);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(p + off1);
+    return F(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto fa = [&](const uint8_t* buf, int i) { return frag(buf + (wn * NF + i) * 2048); };
+  auto fb = [&](const uint8_t* buf, int j) { return frag(buf + (TN / 16 + wm * MF + j) * 2048); };
+
+  // w: operands i .. i + kAhead
+  constexpr int kAhead = NF * MF >= 24 ? 1 : 2, kRing = kAhead == 1 ? 2 : 4;
+  static_assert(NF % kRing == 0 && NF % 2 == 0, "the rings start over with a step");
+  F b[MF], w[kRing];
+  f32x4 p[2][MF];     // block products of rows of tiles i and i - 1 (of the step before's last)
+  float sc[MF], due[MF];  // scales of the step, and of the one before
+#pragma unroll
+  for (int j = 0; j < MF; ++j) {
+    p[1][j] = f32x4{0, 0, 0, 0};
+    due[j] = 0.0f;
+  }
+  auto add = [&](int i, int j, float f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      acc[i][j][v] = __builtin_fmaf(f, p[i & 1][j][v], acc[i][j][v]);
+  };
+  int s = 0;
+  // step s out of `here`; phase: its place among the 4 whose scales are in cur. False
+  // after the last. The order of instructions is fixed: a product of each tile, then the
+  // sums of the tile a row before.
+  auto step = [&](auto phase, uint8_t* before, uint8_t* here, const uint8_t* next)
+                  __attribute__((always_inline)) {
+    if constexpr (phase() == 0) {
+      take(s);
+      scales(s + 4);
+    }
+#pragma unroll
+    for (int j = 0; j < MF; ++j) sc[j] = from_lane(cur[j], 16 * phase() + r);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      if (i == NF - kAhead) {
+        tile_barrier(vm_lds((S - 2) * kCopies));  // the next step's copies have arrived
+      }
+      // a share of the copies for the step S on, into the buffer that this step, and
+      // before the barrier the one before, has read
+      const int at = i + kAhead < NF ? i + kAhead : i + kAhead - NF;
+      if (i < NF - kAhead) copy(before, s - 1 + S, at * kCopies / NF, (at + 1) * kCopies / NF);
+      else copy(here, s + S, at * kCopies / NF, (at + 1) * kCopies / NF);
+      w[at % kRing] = i + kAhead < NF ? fa(here, at) : fa(next, at);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < MF; ++j) {
+        p[i & 1][j] = block_product(w[i % kRing], b[j]);
+        if (i == 0) add(NF - 1, j, due[j]);
+        else add(i - 1, j, sc[j]);
+        if (i == NF - 1) b[j] = fb(next, j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < MF; ++j) due[j] = sc[j];
+    return ++s < blocks;
+  };
+  scales(0);
+  copy(buf0, 0, 0, kCopies);
+  if constexpr (S > 2) copy(buf1, 1, 0, kCopies);
+  copy(S > 2 ? buf2 : buf1, S - 1, 0, kAhead * kCopies / NF);  // the first step brings the others
+  tile_barrier(vm_lds((S - 2) * kCopies + kAhead * kCopies / NF));
+#pragma unroll
+  for (int j = 0; j < MF; ++j) b[j] = fb(buf0, j);
+  w[0] = fa(buf0, 0);
+  if constexpr (kAhead > 1) w[1] = fa(buf0, 1);
+  constexpr std::integral_constant<int, 0> p0;
+  constexpr std::integral_constant<int, 1> p1;
+  constexpr std::integral_constant<int, 2> p2;
+  constexpr std::integral_constant<int, 3> p3;
+  if constexpr (S == 2) {
+    while (step(p0, buf1, buf0, buf1) && step(p1, buf0, buf1, buf0) &&
+           step(p2, buf1, buf0, buf1) && step(p3, buf0, buf1, buf0)) {
+    }
+  } else {
+    while (step(p0, buf2, buf0, buf1) && step(p1, buf0, buf1, buf2) &&
+           step(p2, buf1, buf2, buf0) && step(p3, buf2, buf0, buf1) &&
+           step(p0, buf0, buf1, buf2) && step(p1, buf1, buf2, buf0) &&
+           step(p2, buf2, buf0, buf1) && step(p3, buf0, buf1, buf2) &&
+           step(p0, buf1, buf2, buf0) && step(p1, buf2, buf0, buf1) &&
+           step(p2, buf0, buf1, buf2) && step(p3, buf1, buf2, buf0)) {
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
+#pragma unroll
+  for (int j = 0; j < MF; ++j) add(NF - 1, j, due[j]);
+  with_output(a, [&](auto type, auto vec) {
+#pragma unroll
+    for (int j = 0; j < MF; ++j) {
+      const int m = m0 + (wm * MF + j) * 16 + r;
+      if (m >= M) continue;
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        const int n = n0 + (wn * NF + i) * 16 + 4 * q;
+        if (n >= N) continue;
+        const float y[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        store4<type(), vec()>(a, m, n, y);
+      }
+    }
+  });
+}
+
+template <int TN, int TM, int S>
+hipError_t go_big(const F8Args& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.N + TN - 1) / TN, tiles = (int64_t)((a.M + TM - 1) / TM) * tiles_n;
+  hipLaunchKernelGGL((gemm_f8_big<TN, TM, S>),
+                     dim3((unsigned)((tiles + kXcds - 1) / kXcds * kXcds)), dim3(512), 0, stream, a,
+                     (int)tiles_n);
+  return hipGetLastError();
+}
+
 template <int TN, int TM, int WN, int WM, int S, bool GU, bool EXACT>
 hipError_t go(const F8Args& a, hipStream_t stream) {
   const int per = GU ? TN / 2 : TN;
@@ -311,15 +510,32 @@ bool gemm_f8_fits(const F8Args& a) {
 }
 
 hipError_t launch_gemm_f8(const F8Args& a, hipStream_t s) {
-  if (a.gate_up) return go<128, 64, 4, 2, 3, true, true>(a, s);
-  if (a.slots) return go<128, 64, 4, 2, 3, false, false>(a, s);
-  const int cus = device_cus();
+  if (a.gate_up) return go<128, 64, 2, 2, 3, true, true>(a, s);
+  if (a.slots) return go<128, 64, 2, 2, 3, false, false>(a, s);
+  const int64_t cus = device_cus();
   auto tiles = [&](int tn, int tm) {
     return (int64_t)((a.N + tn - 1) / tn) * ((a.M + tm - 1) / tm);
   };
   const bool wide = a.dtype == MOE_DTYPE_F32;
+  // Wide tiles where they fill the card, or half of it with a long sum, us, wide / small:
+  // 1024 x 4096 x 4096 26 / 41, 512 x 4096 x 4096 (128 tiles) 24 / 26, 1001 x 2047 x 1040
+  // (128 tiles) 12.8 / 11.1. Of them the one whose rounds over the CUs cost least; a
+  // round's cost is its time per step, 2.0, 1.6, 1.12 and 0.72 us (4096 x 5760 x 4096: 143,
+  // 118, 121, 176 us; 4096 x 4096 x 2880: 58, 82, 61, 78; 8192 x 8192 x 8192: 520, 588, 580,
+  // 730; 8192 x 1024 x 4096: 62, 52, 40, 49).
+  const int64_t small = tiles(128, 128);
+  if (!wide && a.lda <= 1 << 22 && (small >= cus || (small >= cus / 2 && a.K >= 2048))) {
+    auto cost = [&](int tn, int tm, int us) { return (tiles(tn, tm) + cus - 1) / cus * us; };
+    const int64_t c[4] = {cost(256, 256, 200), cost(256, 192, 160), cost(256, 128, 112),
+                          cost(128, 128, 72)};
+    const int64_t least = std::min(std::min(c[0], c[1]), std::min(c[2], c[3]));
+    if (least == c[0]) return go_big<256, 256, 2>(a, s);
+    if (least == c[1]) return go_big<256, 192, 2>(a, s);
+    if (least == c[2]) return go_big<256, 128, 3>(a, s);
+    return go_big<128, 128, 3>(a, s);
+  }
   if (tiles(128, 64) >= cus)
-    return wide ? go<128, 64, 4, 2, 3, false, true>(a, s) : go<128, 64, 4, 2, 3, false, false>(a, s);
+    return wide ? go<128, 64, 2, 2, 3, false, true>(a, s) : go<128, 64, 2, 2, 3, false, false>(a, s);
   if (tiles(64, 64) >= cus)
     return wide ? go<64, 64, 2, 2, 3, false, true>(a, s) : go<64, 64, 2, 2, 3, false, false>(a, s);
   return wide ? go<32, 64, 2, 2, 4, false, true>(a, s) : go<32, 64, 2, 2, 4, false, false>(a, s);

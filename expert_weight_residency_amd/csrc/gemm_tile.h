@@ -35,6 +35,21 @@ __device__ __forceinline__ int xcd_item(int items) {
   return at < per && item < items ? item : -1;
 }
 
+// 16 bytes per lane from p to LDS, lane after lane.
+__device__ __forceinline__ void copy16(uint8_t* buf, const uint8_t* p) {
+  asm volatile("" : "+v"(p));  // a select, not a branch around two copies
+  __builtin_amdgcn_global_load_lds(p, buf, 16, 0, 0);
+}
+
+// 16 bytes per lane from base + off to LDS, zeros where off is not below bytes. base and
+// bytes are the same in all lanes.
+__device__ __forceinline__ void copy16(uint8_t* buf, const uint8_t* base, uint32_t bytes,
+                                       uint32_t off) {
+  auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes, 0x27000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      rsrc, (__attribute__((address_space(3))) void*)buf, 16, off, 0, 0, 0);
+}
+
 // Two values rounded to a 16-bit type, the first one low.
 template <int DT>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

@@ -52,12 +52,6 @@ __device__ __forceinline__ int token(const GroupedArgs& a, int slot) {
   return a.by_token ? (int)__umulhi((uint32_t)slot, a.by_token) : slot;
 }
 
-// 16 bytes per lane from p to LDS, lane after lane.
-__device__ __forceinline__ void copy16(uint8_t* buf, const uint8_t* p) {
-  asm volatile("" : "+v"(p));  // a select, not a branch around two copies
-  __builtin_amdgcn_global_load_lds(p, buf, 16, 0, 0);
-}
-
 // The value of another lane of the same 16: lane r ^ 8, or 7 - r of the same 8.
 constexpr int kRor8 = 0x128, kHalfMirror = 0x141;
 template <int CTRL>
@@ -515,15 +509,6 @@ struct Across32 {
     return i32x4{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
   }
 };
-
-// 16 bytes per lane from base + off to LDS, zeros where off is not below bytes. base and
-// bytes are the same in all lanes.
-__device__ __forceinline__ void copy16(uint8_t* buf, const uint8_t* base, uint32_t bytes,
-                                       uint32_t off) {
-  auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, bytes, 0x27000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(
-      rsrc, (__attribute__((address_space(3))) void*)buf, 16, off, 0, 0, 0);
-}
 
 // The same for groups of many rows, in 256 x 128 tiles. Forward: 8 wavefronts (2 x 4) of
 // 128 x 32 outputs, 3 buffers. The operands of the next half step are read from LDS,
