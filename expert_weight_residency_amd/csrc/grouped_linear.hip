@@ -476,9 +476,11 @@ struct Along32 {
   static constexpr int kBytes = ROWS * 64;
   static __device__ __forceinline__ int row(int c, int lane) { return 16 * c + (lane >> 2); }
   static __device__ __forceinline__ int gran(int, int lane) { return (lane & 3) ^ (lane >> 3 & 3); }
-  static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int at, int r, int q) {
+  // the operand lies `from` bytes into buf (one sum of offsets: past a few additions to
+  // a pointer the compiler no longer tells the buffers apart, and waits for every copy)
+  static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int from, int at, int r, int q) {
     const int row = at + r;
-    return *reinterpret_cast<const i32x4*>(buf + row * 64 + 16 * (q ^ (row >> 1 & 3)));
+    return *reinterpret_cast<const i32x4*>(buf + (from + row * 64 + 16 * (q ^ (row >> 1 & 3))));
   }
 };
 // Across: // 32 rows of the sum's axis. A copy is followed by 32 bytes that nothing uses,
@@ -497,92 +499,129 @@ struct Across32 {
     return PAIRED ? (p & 19) | (p & 4) << 1 | (p & 8) >> 1 : p;
   }
   static __device__ __forceinline__ int gran(int lane) { return lane % kGran; }
-  static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int at, int r, int q) {
+  static __device__ __forceinline__ i32x4 frag(const uint8_t* buf, int from, int at, int r, int q) {
     uint64_t v[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // PAIRED: row 8 q + r / 4 + 4 i is in place r / 4 + 4 (q & 1) + 8 i + 16 (q / 2)
       const int p = (r >> 2) + (PAIRED ? 4 * (q & 1) + 8 * i + 16 * (q >> 1) : 4 * q + 16 * i);
-      v[i] = read_turned(buf + p % kCopies * kCopy + p / kCopies * (2 * COLS) + 2 * at +
-                         8 * (r & 3));
+      v[i] = read_turned(buf + (from + p % kCopies * kCopy + p / kCopies * (2 * COLS) + 2 * at +
+                                8 * (r & 3)));
     }
     return i32x4{(int)v[0], (int)(v[0] >> 32), (int)v[1], (int)(v[1] >> 32)};
   }
 };
 
-// The same for groups of many rows, in 256 x 128 tiles. Forward: 8 wavefronts (2 x 4) of
-// 128 x 32 outputs, 3 buffers. The operands of the next half step are read from LDS,
-// spread between the products of this one; the one barrier per step sits between its
-// halves, after the last read of the step's buffer, which then takes the copies for the
-// step 3 steps on (as in gemm_i8_big).
-template <int DT>
+// The same for groups of many rows, in 256 x TB tiles. Forward: 8 wavefronts (2 x 4) of
+// 128 x TB/4 outputs, S buffers of 64 elements. The weights' operand of two tiles on (one,
+// of the larger tile) is read from LDS while a row of tiles is multiplied; the one
+// barrier per step sits after the last read of the step's buffer. The order of
+// instructions is fixed, and copies go out one row of tiles at a time: a step's, asked for
+// at once by all wavefronts, hold the products up (as in gemm_f8_big).
+template <int DT, int TB, int S>
 __global__ __launch_bounds__(512, 2) void grouped_forward(GroupedArgs a, int tiles_a) {
-  constexpr int TA = kWideA, TB = kWideB, WA = 2, NF = TA / WA / 16, MF = TB / 4 / 16;
-  using T = Tile<kForward, TA, TB, 8>;
+  constexpr int TA = kWideA, WN = 2, NF = TA / WN / 16, MF = TB / 4 / 16, kW = 8;
+  using T = Tile<kForward, TA, TB, kW>;
+  constexpr int kCopies = T::kCopies;
   __shared__ __align__(128) uint8_t buf0[(TA + TB) * 128];
   __shared__ __align__(128) uint8_t buf1[(TA + TB) * 128];
-  __shared__ __align__(128) uint8_t buf2[(TA + TB) * 128];
-  __shared__ int wsum[8];
+  __shared__ __align__(128) uint8_t buf2[S > 2 ? (TA + TB) * 128 : 16];
+  __shared__ int wsum[kW];
   extern __shared__ int tpre[];  // [n_active + 1]
 
   const int lane = threadIdx.x & 63;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wn = wv % WA, wm = wv / WA, r = lane & 15, q = lane >> 4;
+  const int wn = wv % WN, wm = wv / WN, r = lane & 15, q = lane >> 4;
+  const int N = a.N, K = a.K;
   T t;
   if (!t.init(a, tiles_a, 1, tpre, wsum, nullptr)) return;  // the whole workgroup
-  t.sources(a);
+
+  constexpr uint32_t kOutside = 1u << 31;  // above the bytes of any copy
+  const int gran = (lane & 7) ^ (lane >> 3);
+  const uint8_t* base = a.w + (t.row * N + t.a0) * K * 2;
+  uint32_t offa[T::kCopiesA];
+  const uint8_t* src[T::kCopiesB];
+#pragma unroll
+  for (int i = 0; i < T::kCopiesA; ++i)
+    offa[i] = min(8 * (wv + kW * i) + (lane >> 3), N - 1 - t.a0) * K * 2 + 16 * gran;
+#pragma unroll
+  for (int i = 0; i < T::kCopiesB; ++i) {
+    const int slot = a.slots[min(t.m0 + 8 * (wv + kW * i) + (lane >> 3), t.m1 - 1)];
+    src[i] = a.x + (int64_t)token(a, slot) * K * 2 + 16 * gran;
+  }
+  // copies [from, to) of step s's: weights first
+  auto copy = [&](uint8_t* buf, int s, int from, int to) __attribute__((always_inline)) {
+    const bool in = s * 128 + 16 * gran < 2 * K;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      if (i < from || i >= to) continue;
+      if (i < T::kCopiesA)
+        copy16(buf + 1024 * (wv + kW * i), base + (int64_t)s * 128, kOutside,
+               in ? offa[i < T::kCopiesA ? i : 0] : kOutside);
+      else
+        copy16(buf + TA * 128 + 1024 * (wv + kW * (i - T::kCopiesA)),
+               in ? src[i < T::kCopiesA ? 0 : i - T::kCopiesA] + (int64_t)s * 128 : kZeros);
+    }
+  };
   f32x4 acc[NF][MF];
 #pragma unroll
   for (int i = 0; i < NF; ++i)
 #pragma unroll
     for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  struct Frags {
-    i32x4 b[MF], a[NF];
+  struct Frag {
+    i32x4 half[2];
   };
-  auto read = [&](const uint8_t* buf, int half, Frags& f) {
-#pragma unroll
-    for (int j = 0; j < MF; ++j)
-      f.b[j] = T::B::frag(buf + TA * 128, (wm * MF + j) * 16, half, r, q);
-#pragma unroll
-    for (int i = 0; i < NF; ++i) f.a[i] = T::A::frag(buf, (wn * NF + i) * 16, half, r, q);
+  const int off0 = r * 128 + 16 * (q ^ (r & 7)), off1 = r * 128 + 16 * ((4 + q) ^ (r & 7));
+  auto frag = [&](const uint8_t* p) {
+    return Frag{{*reinterpret_cast<const i32x4*>(p + off0),
+                 *reinterpret_cast<const i32x4*>(p + off1)}};
   };
-  auto mul = [&](const Frags& f) {
-#pragma unroll
-    for (int i = 0; i < NF; ++i)
-#pragma unroll
-      for (int j = 0; j < MF; ++j) acc[i][j] = mfma<DT>(f.a[i], f.b[j], acc[i][j]);
-  };
-  auto spread = [&](bool copies) {
-    constexpr int kOps = NF + MF, kMul = NF * MF;
-#pragma unroll
-    for (int i = 0; i < kOps; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (copies && i < T::kCopies) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, kMul / kOps, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, kMul % kOps, 0);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  Frags f0, f1;
+  auto fa = [&](const uint8_t* buf, int i) { return frag(buf + (wn * NF + i) * 2048); };
+  auto fb = [&](const uint8_t* buf, int j) { return frag(buf + (TA / 16 + wm * MF + j) * 2048); };
+
+  // w: operands i .. i + kAhead
+  constexpr int kAhead = MF >= 4 ? 1 : 2, kRing = kAhead == 1 ? 2 : 4;
+  static_assert(NF % kRing == 0, "the ring starts over with a step");
+  Frag b[MF], w[kRing];
   int s = 0;
-  // the step out of `here`, f0 its first half's operands. False after the last
-  auto step = [&](uint8_t* here, const uint8_t* next) {
-    read(here, 1, f1);
-    mul(f0);
-    spread(false);
-    tile_barrier(vm_lds(T::kCopies));  // the next step's copies have arrived
-    t.copy(a, NoRing(), here, s + 3);
-    read(next, 0, f0);
-    mul(f1);
-    spread(true);
+  // step s out of `here`. False after the last
+  auto step = [&](uint8_t* before, uint8_t* here, const uint8_t* next)
+                  __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      if (i == NF - kAhead) tile_barrier(vm_lds((S - 2) * kCopies));  // the next step's arrived
+      // a share of the copies for the step S on, into the buffer that this step, and
+      // before the barrier the one before, has read
+      const int at = i + kAhead < NF ? i + kAhead : i + kAhead - NF;
+      if (i < NF - kAhead) copy(before, s - 1 + S, at * kCopies / NF, (at + 1) * kCopies / NF);
+      else copy(here, s + S, at * kCopies / NF, (at + 1) * kCopies / NF);
+      w[at % kRing] = i + kAhead < NF ? fa(here, at) : fa(next, at);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < MF; ++j) {
+          acc[i][j] = mfma<DT>(w[i % kRing].half[h], b[j].half[h], acc[i][j]);
+          if (h == 1 && i == NF - 1) b[j] = fb(next, j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    }
     return ++s < t.steps;
   };
-  t.copy(a, NoRing(), buf0, 0);
-  t.copy(a, NoRing(), buf1, 1);
-  t.copy(a, NoRing(), buf2, 2);
-  tile_barrier(vm_lds(2 * T::kCopies));
-  read(buf0, 0, f0);
-  while (step(buf0, buf1) && step(buf1, buf2) && step(buf2, buf0)) {
+  copy(buf0, 0, 0, kCopies);
+  if constexpr (S > 2) copy(buf1, 1, 0, kCopies);
+  copy(S > 2 ? buf2 : buf1, S - 1, 0, kAhead * kCopies / NF);  // the first step brings the others
+  tile_barrier(vm_lds((S - 2) * kCopies + kAhead * kCopies / NF));
+#pragma unroll
+  for (int j = 0; j < MF; ++j) b[j] = fb(buf0, j);
+  w[0] = fa(buf0, 0);
+  if constexpr (kAhead > 1) w[1] = fa(buf0, 1);
+  if constexpr (S == 2) {
+    while (step(buf1, buf0, buf1) && step(buf0, buf1, buf0)) {
+    }
+  } else {
+    while (step(buf2, buf0, buf1) && step(buf0, buf1, buf2) && step(buf1, buf2, buf0)) {
+    }
   }
   __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
   t.store(a, acc, wn, wm);
@@ -590,8 +629,8 @@ __global__ __launch_bounds__(512, 2) void grouped_forward(GroupedArgs a, int til
 
 // The gradients: 4 wavefronts (2 x 2) of 128 x 64 outputs and steps of 32 elements, two
 // workgroups per CU, so that one's start and end run beside the other's products. The
-// operands of the next step are read from LDS, spread between the products of this one,
-// whose buffer then takes the copies for the step 3 steps on; one barrier per step.
+// operands of the next step are read from LDS between the products of this one, whose
+// buffer then takes the copies for the step 3 steps on; one barrier per step.
 template <int OP, int DT>
 __global__ __launch_bounds__(256, 2) void grouped_gradient(GroupedArgs a, int tiles_a,
                                                              int tiles_b) {
@@ -656,32 +695,44 @@ __global__ __launch_bounds__(256, 2) void grouped_gradient(GroupedArgs a, int ti
       t.keep(a, ring, 1, second);
       __syncthreads();
     }
-    auto copy = [&](uint8_t* buf, int s) {
-      if constexpr (OP == kInput) {
-        const int left = min(max(N - 32 * s, 0), 32);
-#pragma unroll
-        for (int i = 0; i < kCopiesA; ++i)
-          copy16(buf + A::kCopy * (wv + kW * i), base + (int64_t)s * 32 * K * 2,
-                 (uint32_t)left * K * 2, offa[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kCopiesA; ++i) {
-          const int at = s * 32 + A::row(wv + kW * i, lane);
-          const int64_t from = ring.x[at & (2 * kHalf - 1)];
-          copy16(buf + A::kCopy * (wv + kW * i), at < t.sum && ina ? sa + from * K * 2 : kZeros);
-        }
+    // weights: rows of x and dy that a step's copies bring, read a step before
+    uint32_t rows[kCopies];
+    auto look = [&](int s, int i) __attribute__((always_inline)) {
+      if constexpr (OP == kWeights) {
+        if (i < kCopiesA) rows[i] = ring.x[(s * 32 + A::row(wv + kW * i, lane)) & (2 * kHalf - 1)];
+        else rows[i] = ring.dy[(s * 32 + B::row(wv + kW * (i - kCopiesA), lane)) & (2 * kHalf - 1)];
       }
-#pragma unroll
-      for (int i = 0; i < kCopiesB; ++i) {
+    };
+    // copy i of step s's, A's first; then the rows of the next step's
+    auto copy = [&](uint8_t* buf, int s, int i) __attribute__((always_inline)) {
+      if (i < kCopiesA) {
+        uint8_t* const to = buf + A::kCopy * (wv + kW * i);
+        if constexpr (OP == kInput) {
+          const int left = min(max(N - 32 * s, 0), 32);
+          copy16(to, base + (int64_t)s * 32 * K * 2, (uint32_t)left * K * 2,
+                 offa[i < kCopiesA ? i : 0]);
+        } else {
+          const int at = s * 32 + A::row(wv + kW * i, lane);
+          copy16(to, at < t.sum && ina ? sa + (uint64_t)rows[i] * (2u * K) : kZeros);
+        }
+      } else {
+        const int c = wv + kW * (i - kCopiesA);
         if constexpr (OP == kWeights) {
-          const int at = s * 32 + B::row(wv + kW * i, lane);
-          const int64_t from = ring.dy[at & (2 * kHalf - 1)];
-          copy16(buf + kBytesA + B::kCopy * (wv + kW * i),
-                 at < t.sum && inb ? sb[0] + from * N * 2 : kZeros);
+          const int at = s * 32 + B::row(c, lane);
+          copy16(buf + kBytesA + B::kCopy * c,
+                 at < t.sum && inb ? sb[0] + (uint64_t)rows[i] * (2u * N) : kZeros);
         } else {
           const bool in = s * 64 + 16 * B::gran(0, lane) < 2 * t.sum;
-          copy16(buf + kBytesA + 1024 * (wv + kW * i), in ? sb[i] + (int64_t)s * 64 : kZeros);
+          copy16(buf + kBytesA + 1024 * c,
+                 in ? sb[i < kCopiesA ? 0 : i - kCopiesA] + (int64_t)s * 64 : kZeros);
         }
+      }
+    };
+    auto copies = [&](uint8_t* buf, int s) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) {
+        copy(buf, s, i);
+        look(s + 1, i);
       }
     };
     // where the copies of step s are the first of a half of the ring, the other half is
@@ -697,47 +748,46 @@ __global__ __launch_bounds__(256, 2) void grouped_gradient(GroupedArgs a, int ti
     struct Frags {
       i32x4 b[MF], a[NF];
     };
-    auto read = [&](const uint8_t* buf, Frags& f) {
-#pragma unroll
-      for (int j = 0; j < MF; ++j) f.b[j] = B::frag(buf + kBytesA, (wm * MF + j) * 16, r, q);
-#pragma unroll
-      for (int i = 0; i < NF; ++i) f.a[i] = A::frag(buf, (wn * NF + i) * 16, r, q);
-    };
-    auto mul = [&](const Frags& f) {
-#pragma unroll
-      for (int i = 0; i < NF; ++i)
-#pragma unroll
-        for (int j = 0; j < MF; ++j) acc[i][j] = mfma<DT>(f.a[i], f.b[j], acc[i][j]);
-    };
-    auto spread = [&]() {
-      constexpr int kOps = NF * 2 + MF * (T::kTurnB ? 2 : 1), kMul = NF * MF;
-#pragma unroll
-      for (int i = 0; i < kOps; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        if (i < kCopies) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, kMul / kOps, 0);
-      }
-      __builtin_amdgcn_sched_group_barrier(0x008, kMul % kOps, 0);
-      __builtin_amdgcn_sched_barrier(0);
+    auto reada = [&](const uint8_t* buf, int i) { return A::frag(buf, 0, (wn * NF + i) * 16, r, q); };
+    auto readb = [&](const uint8_t* buf, int j) {
+      return B::frag(buf, kBytesA, (wm * MF + j) * 16, r, q);
     };
     Frags f0, f1;
     int s = 0;
     // the step whose operands are in f, out of `here`; the next one's go into g. False
-    // after the last
-    auto step = [&](uint8_t* here, const uint8_t* next, const Frags& f, Frags& g) {
+    // after the last. The order of instructions is fixed: with each row of products one
+    // copy, and reads of the next step's operands
+    auto step = [&](uint8_t* here, const uint8_t* next, const Frags& f, Frags& g)
+                    __attribute__((always_inline)) {
       tile_barrier(vm_lds(kCopies));  // the next step's copies have arrived
-      copy(here, s + 3);
-      read(next, g);
-      mul(f);
-      spread();
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        if (i < kCopies) {
+          copy(here, s + 3, i);
+          look(s + 4, i);
+        }
+        g.a[i] = reada(next, i);
+        if (i % (NF / MF) == 0) g.b[i / (NF / MF)] = readb(next, i / (NF / MF));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < MF; ++j) {
+          acc[i][j] = mfma<DT>(f.a[i], f.b[j], acc[i][j]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
       refill(s + 3);
       return ++s < steps;
     };
-    copy(buf0, 0);
-    copy(buf1, 1);
-    copy(buf2, 2);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) look(0, i);
+    copies(buf0, 0);
+    copies(buf1, 1);
+    copies(buf2, 2);
     tile_barrier(vm_lds(2 * kCopies));
-    read(buf0, f0);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) f0.a[i] = reada(buf0, i);
+#pragma unroll
+    for (int j = 0; j < MF; ++j) f0.b[j] = readb(buf0, j);
     while (step(buf0, buf1, f0, f1) && step(buf1, buf2, f1, f0) && step(buf2, buf0, f0, f1) &&
            step(buf0, buf1, f1, f0) && step(buf1, buf2, f0, f1) && step(buf2, buf0, f1, f0)) {
     }
@@ -777,7 +827,7 @@ hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
   const Grid g = grid_of(a, kWideA, kWideB);
   const dim3 blocks((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds));
   if constexpr (OP == kForward)
-    hipLaunchKernelGGL((grouped_forward<DT>), blocks, dim3(512), g.lds, stream, a, (int)g.tiles_a);
+    hipLaunchKernelGGL((grouped_forward<DT, kWideB, 3>), blocks, dim3(512), g.lds, stream, a, (int)g.tiles_a);
   else
     hipLaunchKernelGGL((grouped_gradient<OP, DT>), blocks, dim3(256), g.lds, stream, a,
                        (int)g.tiles_a, (int)g.tiles_b);
