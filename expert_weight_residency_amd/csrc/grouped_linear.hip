@@ -387,9 +387,10 @@ struct Tile {
 // Tiles of the kernels for groups of many rows.
 constexpr int kWideA = 256, kWideB = 128;
 
-// TA x TB result tile, WA x WB wavefronts, 3 buffers.
-template <int OP, int DT, int TA, int TB, int WA, int WB>
-__global__ __launch_bounds__(64 * WA * WB, (TA + TB) * 384 > 80 << 10 ? WA * WB / 4 : WA * WB / 2)
+// TA x TB result tile, WA x WB wavefronts, S buffers.
+template <int OP, int DT, int TA, int TB, int WA, int WB, int S>
+__global__ __launch_bounds__(64 * WA * WB,
+                             (TA + TB) * 128 * S > 80 << 10 ? WA * WB / 4 : WA * WB / 2)
 void grouped(GroupedArgs a, int tiles_a, int tiles_b) {
   constexpr int kW = WA * WB, kRows = TA + TB;
   constexpr int NF = TA / WA / 16, MF = TB / WB / 16;  // MFMA tiles per wavefront
@@ -397,6 +398,10 @@ void grouped(GroupedArgs a, int tiles_a, int tiles_b) {
   __shared__ __align__(128) uint8_t buf0[kRows * 128];
   __shared__ __align__(128) uint8_t buf1[kRows * 128];
   __shared__ __align__(128) uint8_t buf2[kRows * 128];
+  __shared__ __align__(128) uint8_t buf3[S > 3 ? kRows * 128 : 16];
+  __shared__ __align__(128) uint8_t buf4[S > 3 ? kRows * 128 : 16];
+  __shared__ __align__(128) uint8_t buf5[S > 3 ? kRows * 128 : 16];
+  static_assert(S == 3 || S == 6, "buffers");
   __shared__ typename T::Ring ring;
   __shared__ uint32_t seen[OP == kWeights ? MOE_MAX_ROWS / 32 : 1];
   __shared__ int wsum[kW];
@@ -449,20 +454,28 @@ void grouped(GroupedArgs a, int tiles_a, int tiles_b) {
         }
       }
     };
+    int s = 0;
+    // each step: its copies (the oldest) have arrived for every wavefront, and the
+    // buffer the last step read is free for the copies S - 1 steps ahead. False after
+    // the last
+    auto step = [&](const uint8_t* here, uint8_t* before) __attribute__((always_inline)) {
+      tile_barrier(vm_lds((S - 2) * T::kCopies));
+      copy(before, s + S - 1);
+      compute(here);
+      return ++s < t.steps;
+    };
     copy(buf0, 0);
     copy(buf1, 1);
-    for (int s = 0; s < t.steps; s += 3) {
-      // each step: its copies (the oldest) have arrived for every wavefront, and the
-      // buffer the last step read is free for the copies 2 steps ahead
-      tile_barrier(vm_lds(T::kCopies));
-      copy(buf2, s + 2);
-      compute(buf0);
-      tile_barrier(vm_lds(T::kCopies));
-      copy(buf0, s + 3);
-      compute(buf1);
-      tile_barrier(vm_lds(T::kCopies));
-      copy(buf1, s + 4);
-      compute(buf2);
+    if constexpr (S == 3) {
+      while (step(buf0, buf2) && step(buf1, buf0) && step(buf2, buf1)) {
+      }
+    } else {
+      copy(buf2, 2);
+      copy(buf3, 3);
+      copy(buf4, 4);
+      while (step(buf0, buf5) && step(buf1, buf0) && step(buf2, buf1) && step(buf3, buf2) &&
+             step(buf4, buf3) && step(buf5, buf4)) {
+      }
     }
     __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
   }
@@ -813,10 +826,10 @@ Grid grid_of(const GroupedArgs& a, int ta, int tb) {
   return {tiles_a, 1, (cap + a.M / tb) * tiles_a, (cap + 1) * (int64_t)sizeof(int)};
 }
 
-template <int OP, int DT, int TA, int TB, int WA, int WB>
+template <int OP, int DT, int TA, int TB, int WA, int WB, int S>
 hipError_t go(const GroupedArgs& a, hipStream_t stream) {
   const Grid g = grid_of(a, TA, TB);
-  hipLaunchKernelGGL((grouped<OP, DT, TA, TB, WA, WB>),
+  hipLaunchKernelGGL((grouped<OP, DT, TA, TB, WA, WB, S>),
                      dim3((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds)), dim3(64 * WA * WB),
                      g.lds, stream, a, (int)g.tiles_a, (int)g.tiles_b);
   return hipGetLastError();
@@ -854,20 +867,45 @@ bool use_wide(const GroupedArgs& a) {
   }
 }
 
+// Small tiles, and many buffers, where the next larger ones are few or mostly empty, us,
+// 128 x 64 / 64 x 32: forward 4096 x 2880, one token's 6 experts (192 tiles) 28.7 / 24.9; 2048
+// x 1408, 32 experts, 8 tokens (512) 23.5 / 25.4; 16 x 4096, 64 experts, 8 tokens 27.7 / 18.0,
+// 4096 tokens 54 / 47; 520 x 1032, 8 experts, 1024 tokens (520) 22 / 34. Input 4096 x 2880, one
+// token 36.9 / 29.1; 520 x 1032, 8 experts, 32 tokens (99) 8.6 / 7.4, 256 tokens (288) 9.5 /
+// 16.1. Weights, 128 x 128 / 64 x 64: 4096 x 16, 64 experts, 1000 rows 34.6 / 22.4; 520 x 1032,
+// 8 experts (360) 13.1 / 12.5; 16 x 4096, 64 experts (2048) 12.4 / 15.6.
+bool use_small(const GroupedArgs& a) {
+  const int64_t cus = device_cus();
+  switch (a.op) {
+    case kForward: return a.N <= 64 || grid_of(a, 128, 64).tiles < 2 * cus;
+    case kInput: return a.K <= 64 || grid_of(a, 128, 64).tiles < cus;
+    default: return a.K <= 64 || grid_of(a, 128, 128).tiles < 2 * cus;
+  }
+}
+
 template <int DT>
 hipError_t pick(const GroupedArgs& a, hipStream_t s) {
-  const bool wide = use_wide(a);
+  const bool wide = use_wide(a), small = use_small(a);
   switch (a.op) {
     case kForward:
-      return wide ? go_wide<kForward, DT>(a, s) : go<kForward, DT, 128, 64, 4, 2>(a, s);
-    case kInput: return wide ? go_wide<kInput, DT>(a, s) : go<kInput, DT, 128, 64, 4, 2>(a, s);
-    default: return wide ? go_wide<kWeights, DT>(a, s) : go<kWeights, DT, 128, 128, 4, 2>(a, s);
+      return wide    ? go_wide<kForward, DT>(a, s)
+             : small ? go<kForward, DT, 64, 32, 2, 2, 6>(a, s)
+                     : go<kForward, DT, 128, 64, 4, 2, 3>(a, s);
+    case kInput:
+      return wide    ? go_wide<kInput, DT>(a, s)
+             : small ? go<kInput, DT, 64, 32, 2, 2, 6>(a, s)
+                     : go<kInput, DT, 128, 64, 4, 2, 3>(a, s);
+    default:
+      return wide    ? go_wide<kWeights, DT>(a, s)
+             : small ? go<kWeights, DT, 64, 64, 2, 2, 3>(a, s)
+                     : go<kWeights, DT, 128, 128, 4, 2, 3>(a, s);
   }
 }
 
 }  // namespace
 
-// The finest tiles any of the kernels takes for such a call, times its threads.
+// The finest tiles any of the kernels takes for a large call (small ones are few), times
+// its threads.
 bool grouped_fits(const GroupedArgs& a) {
   const int64_t limit = ((int64_t)1 << 32) - 512 * kXcds;
   if (a.op == kWeights)

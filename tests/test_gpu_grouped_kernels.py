@@ -1,7 +1,5 @@
 """Every kernel of the products grouped by expert: which calls launch which, and that the
 forward product and the input's gradient give the same bits whichever does."""
-import re
-
 import numpy as np
 import pytest
 import torch
@@ -25,10 +23,13 @@ def gpu():
 # sizes on both sides of each rule, each call's kernel by the start of its name
 # T, k, E, N, K, forward, input, weights
 SIZES = [
-    (40, 2, 6, 72, 136, "grouped<0", "grouped<1", "grouped<2"),
-    (1600, 2, 4, 4096, 1032, "grouped_forward<", "grouped<1", "grouped_gradient<2"),
-    (1500, 2, 4, 264, 5000, "grouped<0", "grouped_gradient<1", "grouped<2"),
-    (700, 3, 7, 2600, 2056, "grouped<0", "grouped<1", "grouped_gradient<2"),
+    (40, 2, 6, 72, 136, "grouped<0, {}, 64", "grouped<1, {}, 64", "grouped<2, {}, 64"),
+    (300, 2, 60, 1304, 1400, "grouped<0, {}, 128", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
+    (1600, 2, 4, 4096, 1032, "grouped_forward<{}, ", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
+    (1500, 2, 4, 264, 5000, "grouped<0, {}, 64", "grouped_gradient<1, {}>", "grouped<2, {}, 64"),
+    (100, 2, 4, 1032, 1800, "grouped<0, {}, 64", "grouped<1, {}, 64", "grouped<2, {}, 128"),
+    (700, 3, 7, 2600, 2056, "grouped<0, {}, 128", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
+    (900, 2, 5, 4104, 48, "grouped<0, {}, 128", "grouped<1, {}, 64", "grouped<2, {}, 64"),
 ]
 
 
@@ -48,17 +49,16 @@ def test_kernels(T, k, E, N, K, fwd, inp, wts, dtype):
                        (inp, lambda: moe.moe_grouped_linear_dx(dev[1], dev[2], split, k, dx)),
                        (wts, lambda: moe.moe_grouped_linear_dw(dev[1], dev[0], split, k, dw))):
         got = launched(call, NAMES)
-        assert len(got) == 1 and next(iter(got)).startswith(want), (want, got)
-        assert re.search(rf"[<, ]{code}[,>]", next(iter(got))), (code, got)
+        assert len(got) == 1 and next(iter(got)).startswith(want.format(code)), (want, got)
 
 
 def test_every_kernel_is_launched():
     """The kernels that the library holds are those that test_kernels names, for both types."""
-    start = {s[i] for s in SIZES for i in (5, 6, 7)}
+    start = {s[i].format(code) for s in SIZES for i in (5, 6, 7) for code in (0, 1)}
     have = held(NAMES)
-    assert have and all(any(h.startswith(s) for s in start) for h in have), have
-    for s in start:
-        assert len([h for h in have if h.startswith(s)]) == 2, (s, have)
+    assert len(have) == len(start)
+    for h in have:
+        assert any(h.startswith(s) for s in start), h
 
 
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
