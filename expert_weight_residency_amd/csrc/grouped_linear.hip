@@ -812,6 +812,98 @@ __global__ __launch_bounds__(256, 2) void grouped_gradient(GroupedArgs a, int ti
   else t.template store_lines<MOE_DTYPE_F16>(a, acc, wn, wm);
 }
 
+// Forward with a sum of at most 64 elements (an adapter's second product), which is bound
+// by its output: no buffers. A wavefront holds the 64 x rows of its tile in registers and
+// walks over a quarter of the tile's 1024 weight rows, whose elements go from memory to the
+// products as they lie, 64 rows at a time, the next 64 asked for before. A product's row
+// 4 q + v is weight row 8 q + v of a pair of tiles' 32 for 16-bit outputs, 4 on in the
+// pair's other tile: a lane stores 8 consecutive outputs. N = 4096, us, 256 / 512 / 1024 /
+// 2048 weight rows per tile: K 16, 64 experts, 6000 slots 21.5 / 19.7 / 18.2 / 19.2 (49 MB
+// written); K 32, 24576 slots 60.6 / 48.9 / 46.9 / 52.1.
+constexpr int kShortA = 1024, kShortB = 64, kShortK = 64;
+template <int DT, int OUT>
+__device__ void short_sums(const GroupedArgs& a, const Tile<kForward, kShortA, kShortB, 4>& t) {
+  constexpr bool kPairs = OUT != MOE_DTYPE_F32;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = a.N, K = a.K;
+  const bool in[2] = {8 * q < K, 32 + 8 * q < K};
+  const uint8_t* w = a.w + t.row * N * (int64_t)K * 2 + 16 * q;
+  auto load = [&](const uint8_t* p, int half) {
+    return *reinterpret_cast<const i32x4*>(in[half] ? p + 64 * half : kZeros);
+  };
+  i32x4 x[4][2];
+  int slot[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = t.m0 + 16 * j + r;
+    slot[j] = a.slots[min(at, t.m1 - 1)];
+    const uint8_t* p = a.x + (int64_t)token(a, slot[j]) * K * 2 + 16 * q;
+    for (int h = 0; h < 2; ++h) x[j][h] = load(p, h);
+    if (at >= t.m1) slot[j] = -1;
+  }
+  // weight row of a product's row `m` of tile i
+  auto row = [](int i, int m) {
+    return kPairs ? i / 2 * 32 + m / 4 * 8 + i % 2 * 4 + m % 4 : 16 * i + m;
+  };
+  auto block = [&](int n0, i32x4 (&f)[4][2]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* p = w + (int64_t)min(n0 + row(i, r), N - 1) * K * 2;
+      for (int h = 0; h < 2; ++h) f[i][h] = load(p, h);
+    }
+  };
+  const int end = min(t.a0 + kShortA, N);
+  i32x4 next[4][2];
+  int n0 = t.a0 + 64 * wv;
+  if (n0 < end) block(n0, next);
+  for (; n0 < end; n0 += 256) {
+    i32x4 f[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      for (int h = 0; h < 2; ++h) f[i][h] = next[i][h];
+    if (n0 + 256 < end) block(n0 + 256, next);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f32x4 y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[i] = mfma<DT>(f[i][0], x[j][0], f32x4{0, 0, 0, 0});
+        y[i] = mfma<DT>(f[i][1], x[j][1], y[i]);
+      }
+      if (slot[j] < 0) continue;
+      const int64_t out = slot[j] * a.ldy;
+      if constexpr (kPairs) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const int n = n0 + row(i, 4 * q);
+          if (n < N)  // a multiple of 8
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out + n) =
+                make_uint4(pack2<OUT>(y[i][0], y[i][1]), pack2<OUT>(y[i][2], y[i][3]),
+                           pack2<OUT>(y[i + 1][0], y[i + 1][1]), pack2<OUT>(y[i + 1][2], y[i + 1][3]));
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = n0 + row(i, 4 * q);
+          if (n < N) *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + out + n) = y[i];
+        }
+      }
+    }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void grouped_short(GroupedArgs a, int tiles_a) {
+  __shared__ int wsum[4];
+  extern __shared__ int tpre[];  // [n_active + 1]
+  Tile<kForward, kShortA, kShortB, 4> t;
+  if (!t.init(a, tiles_a, 1, tpre, wsum, nullptr)) return;  // the whole workgroup
+  if (a.dtype == MOE_DTYPE_F32) short_sums<DT, MOE_DTYPE_F32>(a, t);
+  else if (a.dtype == MOE_DTYPE_BF16) short_sums<DT, MOE_DTYPE_BF16>(a, t);
+  else short_sums<DT, MOE_DTYPE_F16>(a, t);
+}
+
 struct Grid {
   int64_t tiles_a, tiles_b, tiles, lds;
 };
@@ -835,6 +927,14 @@ hipError_t go(const GroupedArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int DT>
+hipError_t go_short(const GroupedArgs& a, hipStream_t stream) {
+  const Grid g = grid_of(a, kShortA, kShortB);
+  hipLaunchKernelGGL((grouped_short<DT>), dim3((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds)),
+                     dim3(256), g.lds, stream, a, (int)g.tiles_a);
+  return hipGetLastError();
+}
+
 template <int OP, int DT>
 hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
   const Grid g = grid_of(a, kWideA, kWideB);
@@ -850,18 +950,18 @@ hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
 // Wide tiles where they fill the card (forward one workgroup per CU, the gradients two)
 // and, but for the weights' gradient, an expert has rows for them. us, small tiles / wide
 // ones: forward 2880 x 4096, 64 experts, 48 rows each 298 / 337, 96 400 / 373, 384 1000 /
-// 780; 4096 x 2880, 8 experts, 96 rows (128 wide tiles) 36 / 47, 192 60 / 52; 512 x 512, 16
-// experts, 3072 rows 66 / 74. Input 2880 x 4096, 64 experts, 12 rows 263 / 276, 24 287 / 275,
-// 384 970 / 710; 8 experts, 192 rows (192 wide tiles) 73 / 85. Weights 2880 x 4096, 64
-// experts, 12 rows 975 / 470, 384 2250 / 1140; 1024 x 1024, 4 experts (128 wide tiles), 256
-// rows 11 / 15, 4096 75 / 143.
+// 780; 4096 x 2880, 8 experts, 96 rows (128 wide tiles) 36 / 47, 192 60 / 52; 4096 x 256, 16
+// experts, 2048 rows 257 / 205; 4096 x 512, 125 rows 28 / 30, 512 rows 84 / 72. Input 2880
+// x 4096, 64 experts, 12 rows 263 / 276, 24 287 / 275, 384 970 / 710; 8 experts, 192 rows
+// (192 wide tiles) 73 / 85. Weights 2880 x 4096, 64 experts, 12 rows 975 / 470, 384 2250 /
+// 1010; 1024 x 1024, 4 experts (128 wide tiles), 256 rows 11 / 15, 4096 75 / 143.
 bool use_wide(const GroupedArgs& a) {
   const Grid g = grid_of(a, kWideA, kWideB);
   const int64_t cus = device_cus(), cap = a.n_rows < a.M ? a.n_rows : a.M;
   const size_t fixed = a.op == kForward ? 3 * (kWideA + kWideB) * 128 + 256 : 78 << 10;
   if (g.lds + fixed > (a.op == kForward ? device_lds_per_block() : 80 << 10)) return false;
   switch (a.op) {
-    case kForward: return a.M >= 96 * cap && g.tiles >= cus && a.K >= 1024;
+    case kForward: return a.M >= 96 * cap && g.tiles >= cus;
     case kInput: return a.M >= 24 * cap && g.tiles >= 2 * cus;
     default: return g.tiles >= 2 * cus;
   }
@@ -888,6 +988,9 @@ hipError_t pick(const GroupedArgs& a, hipStream_t s) {
   const bool wide = use_wide(a), small = use_small(a);
   switch (a.op) {
     case kForward:
+      // us, 128 x 64 tiles / this: N = 4096, 64 experts, K 16, 6000 slots 44.2 / 18.2; K 64
+      // 44.5 / 21.9; K 32, 24576 slots 128 / 46.9; 136 x 64, 16000 slots 12.3 / 12.7
+      if (a.K <= kShortK && a.N > 64) return go_short<DT>(a, s);
       return wide    ? go_wide<kForward, DT>(a, s)
              : small ? go<kForward, DT, 64, 32, 2, 2, 6>(a, s)
                      : go<kForward, DT, 128, 64, 4, 2, 3>(a, s);

@@ -29,7 +29,7 @@ SIZES = [
     (1500, 2, 4, 264, 5000, "grouped<0, {}, 64", "grouped_gradient<1, {}>", "grouped<2, {}, 64"),
     (100, 2, 4, 1032, 1800, "grouped<0, {}, 64", "grouped<1, {}, 64", "grouped<2, {}, 128"),
     (700, 3, 7, 2600, 2056, "grouped<0, {}, 128", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
-    (900, 2, 5, 4104, 48, "grouped<0, {}, 128", "grouped<1, {}, 64", "grouped<2, {}, 64"),
+    (900, 2, 5, 4104, 48, "grouped_short<{}>", "grouped<1, {}, 64", "grouped<2, {}, 64"),
 ]
 
 
@@ -97,6 +97,31 @@ def test_bits_do_not_depend_on_banks_or_kernel(out):
             kernels |= launched(call, NAMES)
             assert len(kernels) == 4, kernels
         assert torch.equal(ys, y[at * k:(at + 30) * k]) and torch.equal(dxs, dx[at * k:(at + 30) * k])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("K", [8, 24, 32, 40, 64])
+@pytest.mark.parametrize("T,N", [(1, 72), (5, 1032), (300, 2056)])
+def test_short_sums(T, N, K, dtype):
+    """Sums of at most 64: against the formula, and the bits of the kernel for few outputs."""
+    k, E = 2, 3
+    ids = routing(T, k, E)
+    if T > 1:
+        ids[T // 2, 0] = -1
+    split, _ = make_split(ids, E)
+    for by_token, out in ((True, dtype), (False, torch.float32),
+                          (True, torch.float16 if dtype == torch.bfloat16 else torch.bfloat16)):
+        x, dy, w = inputs(T, k, E, N, K, dtype, by_token, K)
+        dev = [v.cuda() for v in (x, dy, w)]
+        y, dx, dw = run(*dev, split, k, out, torch.float32)
+        check(ids, x, dy, w, y, dx, dw)
+        assert launched(lambda: moe.moe_grouped_linear(dev[0], dev[2], split, k, y), NAMES)
+        for at in (0, N - 64):
+            few = torch.full((T * k, 64), 7.0, dtype=out, device="cuda")
+            part = dev[2][:, at:at + 64].contiguous()
+            moe.moe_grouped_linear(dev[0], part, split, k, few)
+            keep = (ids.reshape(-1) >= 0).cuda()
+            assert torch.equal(few[keep], y[keep, at:at + 64])
 
 
 @pytest.mark.parametrize("T", [500, 521, 2000])
