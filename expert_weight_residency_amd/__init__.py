@@ -774,9 +774,7 @@ def moe_expert_ffn_f8(bank: BankF8, split: Split, xq, xs, k: int, I: int, worksp
             if got != n:
                 raise MoeError(MOE_EINVAL, f"bank {name}: {got} elements, {R} rows at H={H}, "
                                            f"I={I} need {n}")
-        if int(split.slots.numel()) < T * k:
-            raise MoeError(MOE_EINVAL, f"split slots: {int(split.slots.numel())} entries, "
-                                       f"need T*k = {T * k}")
+        _check_split(split, R, T, k)
         _need(xs, "xs", 4 * T * bh)
         _need(workspace, "workspace", moe_ffn_f8_workspace_bytes(T, k, H, I))
         _need(Y, "Y", 2 * T * k * H)
@@ -808,13 +806,13 @@ def _grouped_weights(w, dtype):
     return (w.data_ptr(), *w.shape, BANK_DEVICE if w.is_cuda else BANK_HOST)
 
 
-def _grouped_split(split: Split, slots: int, k: int) -> int:
-    """Tokens of `slots` rows of k each."""
+def _grouped_split(split: Split, slots: int, k: int, n_rows: int = 1) -> int:
+    """Tokens of `slots` rows of k each; the split's buffers hold what a step of that
+    many tokens leaves for weights of n_rows rows."""
     if k < 1 or slots % k:
         raise MoeError(MOE_EINVAL, f"{slots} slots are no multiple of k={k}")
-    if slots and int(split.slots.numel()) < slots:
-        raise MoeError(MOE_EINVAL, f"split slots: {int(split.slots.numel())} entries, "
-                                   f"need T*k = {slots}")
+    if slots and n_rows:
+        _check_split(split, n_rows, slots // k, k)
     return slots // k
 
 
@@ -844,7 +842,7 @@ def moe_grouped_linear(x, w, split: Split, k: int, y, stream=None) -> None:
     xp, code = _grouped_rows(x, "x", _grouped_types())
     wp, rows, N, K, on_host = _grouped_weights(w, x.dtype)
     yp, ycode = _grouped_rows(y, "y", _dtypes(), shape=(int(y.shape[0]), N))
-    T = _grouped_split(split, int(y.shape[0]), k)
+    T = _grouped_split(split, int(y.shape[0]), k, rows)
     by_token = _grouped_by_token(x, T, k)
     if x.shape[1] != K:
         raise MoeError(MOE_EINVAL, f"x {tuple(x.shape)}: rows of w have {K} elements")
@@ -859,7 +857,7 @@ def moe_grouped_linear_dx(dy, w, split: Split, k: int, dx, stream=None) -> None:
     _on(dev, dy=dy, w=w, dx=dx, slots=split.slots)
     yp, code = _grouped_rows(dy, "dy", _grouped_types())
     wp, rows, N, K, on_host = _grouped_weights(w, dy.dtype)
-    T = _grouped_split(split, int(dy.shape[0]), k)
+    T = _grouped_split(split, int(dy.shape[0]), k, rows)
     if tuple(dy.shape) != (T * k, N):
         raise MoeError(MOE_EINVAL, f"dy {tuple(dy.shape)}: need {(T * k, N)}")
     xp, xcode = _grouped_rows(dx, "dx", _dtypes(), shape=(T * k, K))
@@ -874,9 +872,9 @@ def moe_grouped_linear_dw(dy, x, split: Split, k: int, dw, stream=None) -> None:
     _on(dev, dy=dy, x=x, dw=dw, slots=split.slots)
     yp, code = _grouped_rows(dy, "dy", _grouped_types())
     xp, _ = _grouped_rows(x, "x", _grouped_types(), dtype=dy.dtype)
-    T = _grouped_split(split, int(dy.shape[0]), k)
-    by_token = _grouped_by_token(x, T, k)
     wp, wcode = _grouped_rows(dw, "dw", _dtypes())
+    T = _grouped_split(split, int(dy.shape[0]), k, int(dw.shape[0]) if dw.dim() else 0)
+    by_token = _grouped_by_token(x, T, k)
     if dw.dim() != 3 or tuple(dy.shape) != (T * k, dw.shape[1]) or x.shape[1] != dw.shape[2]:
         raise MoeError(MOE_EINVAL, f"dy {tuple(dy.shape)}, x {tuple(x.shape)}, dw {tuple(dw.shape)}: "
                                    "need [T*k,N], [T or T*k,K], [R,N,K]")

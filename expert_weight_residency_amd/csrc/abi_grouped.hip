@@ -16,8 +16,8 @@ struct Part {
 
 // The checks that the three calls share, and the launch. in: two inputs; out: the
 // output with its dtype.
-int grouped(moe::GroupedArgs& a, int T, int k, int by_token, int on_host, const moe_split& split, const Part (&in)[2],
-            const Part& out, void* stream) {
+int grouped(moe::GroupedArgs& a, int T, int k, int by_token, int on_host, const moe_split& split,
+            const Part (&in)[2], const Part& out, void* stream) {
   if (a.elem != MOE_DTYPE_BF16 && a.elem != MOE_DTYPE_F16)
     return set_error(MOE_EINVAL, "dtype=%d is not MOE_DTYPE_BF16 or MOE_DTYPE_F16", a.elem);
   if (!moe::dtype_known(a.dtype))

@@ -60,7 +60,8 @@ struct Frag<true> {
 __device__ __forceinline__ f32x4 block_product(const Frag<true>& a, const Frag<true>& b) {
   f32x4 p = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], p, 0, 0, 0);
+  for (int i = 0; i < 4; ++i)
+    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], p, 0, 0, 0);
   return p;
 }
 
@@ -492,8 +493,8 @@ hipError_t go(const F8Args& a, hipStream_t stream) {
     tiles_m = (a.M + TM - 1) / TM;
   }
   const unsigned grid = (unsigned)((tiles_m * tiles_n + kXcds - 1) / kXcds * kXcds);
-  hipLaunchKernelGGL((gemm_f8_tile<TN, TM, WN, WM, S, GU, EXACT>), dim3(grid), dim3(64 * WN * WM), lds,
-                     stream, a, (int)tiles_n);
+  hipLaunchKernelGGL((gemm_f8_tile<TN, TM, WN, WM, S, GU, EXACT>), dim3(grid),
+                     dim3(64 * WN * WM), lds, stream, a, (int)tiles_n);
   return hipGetLastError();
 }
 

@@ -496,7 +496,7 @@ struct Along32 {
     return *reinterpret_cast<const i32x4*>(buf + (from + row * 64 + 16 * (q ^ (row >> 1 & 3))));
   }
 };
-// Across: // 32 rows of the sum's axis. A copy is followed by 32 bytes that nothing uses,
+// Across: 32 rows of the sum's axis. A copy is followed by 32 bytes that nothing uses,
 // and brings rows that no read joins, so that the 8 rows that 32 lanes read at once lie
 // in different banks and a lane's addresses are one and constants (swizzled chunks
 // would take a register or an operation each). Place p of a row: copy p % kCopies,
@@ -761,7 +761,9 @@ __global__ __launch_bounds__(256, 2) void grouped_gradient(GroupedArgs a, int ti
     struct Frags {
       i32x4 b[MF], a[NF];
     };
-    auto reada = [&](const uint8_t* buf, int i) { return A::frag(buf, 0, (wn * NF + i) * 16, r, q); };
+    auto reada = [&](const uint8_t* buf, int i) {
+      return A::frag(buf, 0, (wn * NF + i) * 16, r, q);
+    };
     auto readb = [&](const uint8_t* buf, int j) {
       return B::frag(buf, kBytesA, (wm * MF + j) * 16, r, q);
     };
@@ -880,7 +882,8 @@ __device__ void short_sums(const GroupedArgs& a, const Tile<kForward, kShortA, k
           if (n < N)  // a multiple of 8
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + out + n) =
                 make_uint4(pack2<OUT>(y[i][0], y[i][1]), pack2<OUT>(y[i][2], y[i][3]),
-                           pack2<OUT>(y[i + 1][0], y[i + 1][1]), pack2<OUT>(y[i + 1][2], y[i + 1][3]));
+                           pack2<OUT>(y[i + 1][0], y[i + 1][1]),
+                           pack2<OUT>(y[i + 1][2], y[i + 1][3]));
         }
       } else {
 #pragma unroll
@@ -940,7 +943,8 @@ hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
   const Grid g = grid_of(a, kWideA, kWideB);
   const dim3 blocks((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds));
   if constexpr (OP == kForward)
-    hipLaunchKernelGGL((grouped_forward<DT, kWideB, 3>), blocks, dim3(512), g.lds, stream, a, (int)g.tiles_a);
+    hipLaunchKernelGGL((grouped_forward<DT, kWideB, 3>), blocks, dim3(512), g.lds, stream, a,
+                       (int)g.tiles_a);
   else
     hipLaunchKernelGGL((grouped_gradient<OP, DT>), blocks, dim3(256), g.lds, stream, a,
                        (int)g.tiles_a, (int)g.tiles_b);

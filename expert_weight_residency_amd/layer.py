@@ -14,9 +14,10 @@ library's kernels.
 
 Two further forms of the same step: forward_few, the whole layer in two
 launches for at most MOE_FEW_MAX_TOKENS tokens, and forward on a pair of 8-bit
-banks, integers (BankI8) or floating point (BankF8). route turns router logits into the ids and weights that
-all of them take; where a token has fewer unmasked experts than k, its picks left
-over (id -1, weight 0) are counted as invalid and add nothing in any of the forms.
+banks, integers (BankI8) or floating point (BankF8). route turns router logits
+into the ids and weights that all of them take; where a token has fewer unmasked
+experts than k, its picks left over (id -1, weight 0) are counted as invalid and
+add nothing in any of the forms.
 """
 from __future__ import annotations
 

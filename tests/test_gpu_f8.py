@@ -336,6 +336,19 @@ def test_ffn_repeated_ids_and_special_tokens():
     check_ffn(Yt[keep].reshape(-1, H), b, ids[keep], x[keep], H, I)
 
 
+def test_ffn_refuses_a_split_of_too_few_entries():
+    T, k, E, H, I = 6, 2, 8, 128, 64
+    b = bank_on(make_bank(E, H, I, 1), "device")
+    xq = torch.zeros(T, H, dtype=F8, device="cuda")
+    xs = torch.zeros(T, 1, dtype=torch.float32, device="cuda")
+    ws = torch.zeros(moe.moe_ffn_f8_workspace_bytes(T, k, H, I), dtype=torch.uint8, device="cuda")
+    Y = torch.zeros(T * k, H, dtype=torch.bfloat16, device="cuda")
+    for made_for in ((E, 2, k), (3, T, k)):
+        with pytest.raises(moe.MoeError, match="split"):
+            moe.moe_expert_ffn_f8(b, moe.Split.empty(*made_for), xq, xs, k, I, ws, Y)
+    moe.moe_expert_ffn_f8(b, moe.Split.empty(E, T, k), xq, xs, k, I, ws, Y)  # of no picks
+
+
 def test_ffn_of_no_valid_picks():
     T, k, E, H, I = 9, 2, 4, 128, 128
     b = make_bank(E, H, I, 9)

@@ -98,6 +98,17 @@ def test_binding_checks_the_slots(rows, k, ok):
             moe._grouped_split(sp, rows, k)
 
 
+@pytest.mark.parametrize("made_for", [(2, 4, 2), (8, 2, 2)])
+def test_binding_checks_the_splits_capacity(made_for):
+    """A split of fewer experts or a shorter step: the kernels would read past its end."""
+    n_rows, T, k = 8, 4, 2
+    with pytest.raises(moe.MoeError, match="split"):
+        moe._grouped_split(moe.Split.empty(*made_for, device="cpu"), T * k, k, n_rows)
+    assert moe._grouped_split(moe.Split.empty(n_rows, T, k, device="cpu"), T * k, k, n_rows) == T
+    # a larger one serves a shorter step and fewer rows
+    assert moe._grouped_split(moe.Split.empty(n_rows, T, k, device="cpu"), 2 * k, k, 2) == 2
+
+
 def test_binding_tells_rows_of_tokens_from_rows_of_slots():
     assert moe._grouped_by_token(torch.zeros(3, 8), 3, 2) == 1
     assert moe._grouped_by_token(torch.zeros(6, 8), 3, 2) == 0
