@@ -525,20 +525,20 @@ struct Across32 {
   }
 };
 
-// The same for groups of many rows, in 256 x TB tiles. Forward: 8 wavefronts (2 x 4) of
-// 128 x TB/4 outputs, S buffers of 64 elements. The weights' operand of two tiles on (one,
-// of the larger tile) is read from LDS while a row of tiles is multiplied; the one
-// barrier per step sits after the last read of the step's buffer. The order of
+// The same for groups of many rows, in 256 x 128 tiles. Forward: 8 wavefronts (2 x 4) of
+// 128 x 32 outputs, 3 buffers of 64 elements. The weights' operand of two tiles on is read
+// from LDS while a row of tiles is multiplied; the one barrier per step sits after the last
+// read of the step's buffer. The order of
 // instructions is fixed, and copies go out one row of tiles at a time: a step's, asked for
 // at once by all wavefronts, hold the products up (as in gemm_f8_big).
-template <int DT, int TB, int S>
+template <int DT>
 __global__ __launch_bounds__(512, 2) void grouped_forward(GroupedArgs a, int tiles_a) {
-  constexpr int TA = kWideA, WN = 2, NF = TA / WN / 16, MF = TB / 4 / 16, kW = 8;
+  constexpr int TA = kWideA, TB = kWideB, S = 3, WN = 2, NF = TA / WN / 16, MF = TB / 4 / 16, kW = 8;
   using T = Tile<kForward, TA, TB, kW>;
   constexpr int kCopies = T::kCopies;
   __shared__ __align__(128) uint8_t buf0[(TA + TB) * 128];
   __shared__ __align__(128) uint8_t buf1[(TA + TB) * 128];
-  __shared__ __align__(128) uint8_t buf2[S > 2 ? (TA + TB) * 128 : 16];
+  __shared__ __align__(128) uint8_t buf2[(TA + TB) * 128];
   __shared__ int wsum[kW];
   extern __shared__ int tpre[];  // [n_active + 1]
 
@@ -593,7 +593,7 @@ __global__ __launch_bounds__(512, 2) void grouped_forward(GroupedArgs a, int til
   auto fb = [&](const uint8_t* buf, int j) { return frag(buf + (TA / 16 + wm * MF + j) * 2048); };
 
   // w: operands i .. i + kAhead
-  constexpr int kAhead = MF >= 4 ? 1 : 2, kRing = kAhead == 1 ? 2 : 4;
+  constexpr int kAhead = 2, kRing = 4;
   static_assert(NF % kRing == 0, "the ring starts over with a step");
   Frag b[MF], w[kRing];
   int s = 0;
@@ -622,19 +622,14 @@ __global__ __launch_bounds__(512, 2) void grouped_forward(GroupedArgs a, int til
     return ++s < t.steps;
   };
   copy(buf0, 0, 0, kCopies);
-  if constexpr (S > 2) copy(buf1, 1, 0, kCopies);
-  copy(S > 2 ? buf2 : buf1, S - 1, 0, kAhead * kCopies / NF);  // the first step brings the others
+  copy(buf1, 1, 0, kCopies);
+  copy(buf2, 2, 0, kAhead * kCopies / NF);  // the first step brings the others
   tile_barrier(vm_lds((S - 2) * kCopies + kAhead * kCopies / NF));
 #pragma unroll
   for (int j = 0; j < MF; ++j) b[j] = fb(buf0, j);
   w[0] = fa(buf0, 0);
-  if constexpr (kAhead > 1) w[1] = fa(buf0, 1);
-  if constexpr (S == 2) {
-    while (step(buf1, buf0, buf1) && step(buf0, buf1, buf0)) {
-    }
-  } else {
-    while (step(buf2, buf0, buf1) && step(buf0, buf1, buf2) && step(buf1, buf2, buf0)) {
-    }
+  w[1] = fa(buf0, 1);
+  while (step(buf2, buf0, buf1) && step(buf0, buf1, buf2) && step(buf1, buf2, buf0)) {
   }
   __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
   t.store(a, acc, wn, wm);
@@ -943,7 +938,7 @@ hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
   const Grid g = grid_of(a, kWideA, kWideB);
   const dim3 blocks((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds));
   if constexpr (OP == kForward)
-    hipLaunchKernelGGL((grouped_forward<DT, kWideB, 3>), blocks, dim3(512), g.lds, stream, a,
+    hipLaunchKernelGGL((grouped_forward<DT>), blocks, dim3(512), g.lds, stream, a,
                        (int)g.tiles_a);
   else
     hipLaunchKernelGGL((grouped_gradient<OP, DT>), blocks, dim3(256), g.lds, stream, a,
@@ -953,19 +948,21 @@ hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
 
 // Wide tiles where they fill the card (forward one workgroup per CU, the gradients two)
 // and, but for the weights' gradient, an expert has rows for them. us, small tiles / wide
-// ones: forward 2880 x 4096, 64 experts, 48 rows each 298 / 337, 96 400 / 373, 384 1000 /
-// 780; 4096 x 2880, 8 experts, 96 rows (128 wide tiles) 36 / 47, 192 60 / 52; 4096 x 256, 16
-// experts, 2048 rows 257 / 205; 4096 x 512, 125 rows 28 / 30, 512 rows 84 / 72. Input 2880
-// x 4096, 64 experts, 12 rows 263 / 276, 24 287 / 275, 384 970 / 710; 8 experts, 192 rows
-// (192 wide tiles) 73 / 85. Weights 2880 x 4096, 64 experts, 12 rows 975 / 470, 384 2250 /
-// 1010; 1024 x 1024, 4 experts (128 wide tiles), 256 rows 11 / 15, 4096 75 / 143.
+// ones: forward 2880 x 4096, 64 experts, 48 rows each 305 / 334, 56 309 / 332, 64 347 / 327,
+// 80 372 / 330, 384 1000 / 790; 5760 x 4096, 384 experts, 64 rows 3980 / 3790; 2048 x 1408,
+// 128 experts, 64 rows 182 / 186, 80 207 / 188; 4096 x 2880, 8 experts, 96 rows (128 wide
+// tiles) 36 / 47, 192 60 / 52; 4096 x 256, 16 experts, 2048 rows 257 / 205; 4096 x 512, 125
+// rows 28 / 30, 512 rows 84 / 72. Input 2880 x 4096, 64 experts, 12 rows 263 / 276, 24 287 /
+// 275, 384 970 / 700; 8 experts, 192 rows (192 wide tiles) 73 / 85. Weights 2880 x 4096, 64
+// experts, 12 rows 975 / 470, 384 2250 / 1010; 1024 x 1024, 4 experts (128 wide tiles), 256
+// rows 11 / 15, 4096 75 / 143.
 bool use_wide(const GroupedArgs& a) {
   const Grid g = grid_of(a, kWideA, kWideB);
   const int64_t cus = device_cus(), cap = a.n_rows < a.M ? a.n_rows : a.M;
   const size_t fixed = a.op == kForward ? 3 * (kWideA + kWideB) * 128 + 256 : 78 << 10;
   if (g.lds + fixed > (a.op == kForward ? device_lds_per_block() : 80 << 10)) return false;
   switch (a.op) {
-    case kForward: return a.M >= 96 * cap && g.tiles >= cus;
+    case kForward: return a.M >= 64 * cap && g.tiles >= cus;
     case kInput: return a.M >= 24 * cap && g.tiles >= 2 * cus;
     default: return g.tiles >= 2 * cus;
   }

@@ -25,7 +25,7 @@ def gpu():
 SIZES = [
     (40, 2, 6, 72, 136, "grouped<0, {}, 64", "grouped<1, {}, 64", "grouped<2, {}, 64"),
     (300, 2, 60, 1304, 1400, "grouped<0, {}, 128", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
-    (1600, 2, 4, 4096, 1032, "grouped_forward<{}, ", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
+    (1600, 2, 4, 4096, 1032, "grouped_forward<{}>", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
     (1500, 2, 4, 264, 5000, "grouped<0, {}, 64", "grouped_gradient<1, {}>", "grouped<2, {}, 64"),
     (100, 2, 4, 1032, 1800, "grouped<0, {}, 64", "grouped<1, {}, 64", "grouped<2, {}, 128"),
     (700, 3, 7, 2600, 2056, "grouped<0, {}, 128", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
