@@ -140,8 +140,14 @@ struct Tile {
       const int item = xcd_item(a.n_rows * per);
       if (item < 0) return false;
       const int e = item / per, local = item - e * per;
-      a0 = local % tiles_a * TA;
-      b0 = local / tiles_a * TB;
+      // in groups of 6 columns of tiles, row by row: the tiles that an XCD runs at one time
+      // are about a square, whose rows its L2 holds (64 experts, 2880 x 4096, 384 rows,
+      // operands not in the caches: 1195 us, by all 16 columns 1265; by 8 1210)
+      constexpr int kGroup = 6;
+      const int group = local / (kGroup * tiles_b), rest = local - group * kGroup * tiles_b;
+      const int wide = min(kGroup, tiles_a - kGroup * group);
+      a0 = (kGroup * group + rest % wide) * TA;
+      b0 = rest / wide * TB;
       // asked for at once with their count: entries past it are not used
       const int at = min(e, min(a.n_rows, a.M) - 1);
       const int active = a.n_active ? *a.n_active : 0;
@@ -955,7 +961,8 @@ hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
 // rows 28 / 30, 512 rows 84 / 72. Input 2880 x 4096, 64 experts, 12 rows 263 / 276, 24 287 /
 // 275, 384 970 / 700; 8 experts, 192 rows (192 wide tiles) 73 / 85. Weights 2880 x 4096, 64
 // experts, 12 rows 975 / 470, 384 2250 / 1010; 1024 x 1024, 4 experts (128 wide tiles), 256
-// rows 11 / 15, 4096 75 / 143.
+// rows 11 / 15, 4096 75 / 143; 4096 x 16, 64 experts, 94 rows 22.7 / 31.9, 4096 x 64 27.2 /
+// 34.2, 4096 x 96 38.5 / 36.7, 16 x 4096 30.5 / 20.6.
 bool use_wide(const GroupedArgs& a) {
   const Grid g = grid_of(a, kWideA, kWideB);
   const int64_t cus = device_cus(), cap = a.n_rows < a.M ? a.n_rows : a.M;
@@ -964,7 +971,7 @@ bool use_wide(const GroupedArgs& a) {
   switch (a.op) {
     case kForward: return a.M >= 64 * cap && g.tiles >= cus;
     case kInput: return a.M >= 24 * cap && g.tiles >= 2 * cus;
-    default: return g.tiles >= 2 * cus;
+    default: return a.K > 64 && g.tiles >= 2 * cus;
   }
 }
 
@@ -973,8 +980,8 @@ bool use_wide(const GroupedArgs& a) {
 // x 1408, 32 experts, 8 tokens (512) 23.5 / 25.4; 16 x 4096, 64 experts, 8 tokens 27.7 / 18.0,
 // 4096 tokens 54 / 47; 520 x 1032, 8 experts, 1024 tokens (520) 22 / 34. Input 4096 x 2880, one
 // token 36.9 / 29.1; 520 x 1032, 8 experts, 32 tokens (99) 8.6 / 7.4, 256 tokens (288) 9.5 /
-// 16.1. Weights, 128 x 128 / 64 x 64: 4096 x 16, 64 experts, 1000 rows 34.6 / 22.4; 520 x 1032,
-// 8 experts (360) 13.1 / 12.5; 16 x 4096, 64 experts (2048) 12.4 / 15.6.
+// 16.1. Weights, 128 x 128 / 64 x 64: 4096 x 16, 64 experts, 94 rows 34.6 / 22.4; 520 x 1032, 8
+// experts (360) 13.1 / 12.5; 16 x 4096, 64 experts (2048) 12.4 / 15.6.
 bool use_small(const GroupedArgs& a) {
   const int64_t cus = device_cus();
   switch (a.op) {
