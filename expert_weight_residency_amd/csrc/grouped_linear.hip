@@ -916,6 +916,95 @@ __global__ __launch_bounds__(256) void grouped_short(GroupedArgs a, int tiles_a)
   else short_sums<DT, MOE_DTYPE_F16>(a, t);
 }
 
+// Forward with at most 32 outputs and a longer sum (an adapter's first product): few tiles,
+// whose steps' latency is what costs. The 4 wavefronts of a workgroup take the sum's chunks
+// of 64 elements in turn and add their parts in order at the end; a lane's 16 consecutive
+// elements of a chunk, one 32-byte piece of a row, go from memory to the products, D chunks
+// ahead, with no barrier.
+constexpr int kNarrowA = 32, kNarrowB = 32;
+template <int DT, int NF, int D>
+__device__ void narrow_sums(const GroupedArgs& a, const Tile<kForward, kNarrowA, kNarrowB, 4>& t,
+                            f32x4* parts) {
+  constexpr int MF = kNarrowB / 16, kTiles = NF * MF;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int N = a.N, K = a.K, chunks = (K + 63) / 64;
+  const uint8_t* p[NF + MF];  // rows of w, then of x
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+    p[i] = a.w + (t.row * N + min(16 * i + r, N - 1)) * (int64_t)K * 2 + 32 * q;
+#pragma unroll
+  for (int j = 0; j < MF; ++j) {
+    const int slot = a.slots[min(t.m0 + 16 * j + r, t.m1 - 1)];
+    p[NF + j] = a.x + (int64_t)token(a, slot) * K * 2 + 32 * q;
+  }
+  struct Chunk {
+    i32x4 v[NF + MF][2];
+  };
+  // zeros past the end of the sum
+  auto load = [&](int c, Chunk& f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool in = 64 * c + 16 * q + 8 * h < K;
+#pragma unroll
+      for (int i = 0; i < NF + MF; ++i)
+        f.v[i][h] =
+            *reinterpret_cast<const i32x4*>(in ? p[i] + ((int64_t)128 * c + 16 * h) : kZeros);
+    }
+  };
+  f32x4 acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  Chunk f[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(wv + 4 * d, f[d]);
+  for (int c = wv; c < chunks; c += 4 * D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+#pragma unroll
+          for (int j = 0; j < MF; ++j)
+            acc[i][j] = mfma<DT>(f[d].v[i][h], f[d].v[NF + j][h], acc[i][j]);
+      load(c + 4 * (D + d), f[d]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) parts[(wv * kTiles + i * MF + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int tile = wv; tile < kTiles; tile += 4) {
+    f32x4 y = parts[tile * 64 + lane];
+    for (int k = 1; k < 4; ++k) y += parts[(k * kTiles + tile) * 64 + lane];
+    const int n = tile / MF * 16 + 4 * q, at = t.m0 + tile % MF * 16 + r;
+    if (n >= N || at >= t.m1) continue;  // N is a multiple of 8
+    const int64_t out = a.slots[at] * a.ldy + n;
+    if (a.dtype == MOE_DTYPE_F32)
+      *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + out) = y;
+    else if (a.dtype == MOE_DTYPE_BF16)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + out) =
+          make_uint2(pack2<MOE_DTYPE_BF16>(y[0], y[1]), pack2<MOE_DTYPE_BF16>(y[2], y[3]));
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + out) =
+          make_uint2(pack2<MOE_DTYPE_F16>(y[0], y[1]), pack2<MOE_DTYPE_F16>(y[2], y[3]));
+  }
+}
+
+template <int DT, int NF>
+__global__ __launch_bounds__(256) void grouped_narrow(GroupedArgs a) {
+  __shared__ int wsum[4];
+  __shared__ f32x4 parts[4 * NF * (kNarrowB / 16) * 64];
+  extern __shared__ int tpre[];  // [n_active + 1]
+  Tile<kForward, kNarrowA, kNarrowB, 4> t;
+  if (!t.init(a, 1, 1, tpre, wsum, nullptr)) return;  // the whole workgroup
+  narrow_sums<DT, NF, NF == 1 ? 4 : 3>(a, t, parts);
+}
+
 struct Grid {
   int64_t tiles_a, tiles_b, tiles, lds;
 };
@@ -944,6 +1033,15 @@ hipError_t go_short(const GroupedArgs& a, hipStream_t stream) {
   const Grid g = grid_of(a, kShortA, kShortB);
   hipLaunchKernelGGL((grouped_short<DT>), dim3((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds)),
                      dim3(256), g.lds, stream, a, (int)g.tiles_a);
+  return hipGetLastError();
+}
+
+template <int DT, int NF>
+hipError_t go_narrow(const GroupedArgs& a, hipStream_t stream) {
+  const Grid g = grid_of(a, kNarrowA, kNarrowB);
+  hipLaunchKernelGGL((grouped_narrow<DT, NF>),
+                     dim3((unsigned)((g.tiles + kXcds - 1) / kXcds * kXcds)), dim3(256), g.lds,
+                     stream, a);
   return hipGetLastError();
 }
 
@@ -1007,6 +1105,12 @@ hipError_t pick(const GroupedArgs& a, hipStream_t s) {
       // us, 128 x 64 tiles / this: N = 4096, 64 experts, K 16, 6000 slots 44.2 / 18.2; K 64
       // 44.5 / 21.9; K 32, 24576 slots 128 / 46.9; 136 x 64, 16000 slots 12.3 / 12.7
       if (a.K <= kShortK && a.N > 64) return go_short<DT>(a, s);
+      // By N and K alone, as the sum's order is another one. us, 64 x 32 tiles / this: 16 x
+      // 4096, 384 experts, 112 tokens 21.3 / 14.2, one token 18.0 / 9.8; 64 experts, 4096
+      // tokens 55.1 / 49.5; 32 x 4096, 1000 tokens 22.1 / 20.5; 64 x 4096, 4096 tokens 57.8 /
+      // 93.4 in a form for 64 outputs
+      if (a.K > kShortK && a.N <= kNarrowA)
+        return a.N <= 16 ? go_narrow<DT, 1>(a, s) : go_narrow<DT, 2>(a, s);
       return wide    ? go_wide<kForward, DT>(a, s)
              : small ? go<kForward, DT, 64, 32, 2, 2, 6>(a, s)
                      : go<kForward, DT, 128, 64, 4, 2, 3>(a, s);

@@ -29,6 +29,8 @@ SIZES = [
     (1500, 2, 4, 264, 5000, "grouped<0, {}, 64", "grouped_gradient<1, {}>", "grouped<2, {}, 64"),
     (100, 2, 4, 1032, 1800, "grouped<0, {}, 64", "grouped<1, {}, 64", "grouped<2, {}, 128"),
     (700, 3, 7, 2600, 2056, "grouped<0, {}, 128", "grouped<1, {}, 128", "grouped_gradient<2, {}>"),
+    (300, 2, 6, 16, 1032, "grouped_narrow<{}, 1>", "grouped<1, {}, 64", "grouped<2, {}, 64"),
+    (200, 2, 5, 32, 520, "grouped_narrow<{}, 2>", "grouped<1, {}, 64", "grouped<2, {}, 64"),
     (900, 2, 5, 4104, 48, "grouped_short<{}>", "grouped<1, {}, 64", "grouped<2, {}, 64"),
 ]
 
@@ -122,6 +124,31 @@ def test_short_sums(T, N, K, dtype):
             moe.moe_grouped_linear(dev[0], part, split, k, few)
             keep = (ids.reshape(-1) >= 0).cuda()
             assert torch.equal(few[keep], y[keep, at:at + 64])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N", [8, 16, 24, 32])
+@pytest.mark.parametrize("T,K", [(1, 72), (5, 200), (40, 4104), (300, 1000)])
+def test_few_outputs(T, N, K, dtype):
+    """At most 32 outputs: against the formula, and one token's bits alone and in the step."""
+    k, E = 2, 3
+    ids = routing(T, k, E)
+    if T > 1:
+        ids[T // 2, 0] = -1
+    split, _ = make_split(ids, E)
+    for by_token, out in ((True, dtype), (False, torch.float32),
+                          (True, torch.float16 if dtype == torch.bfloat16 else torch.bfloat16)):
+        x, dy, w = inputs(T, k, E, N, K, dtype, by_token, K)
+        dev = [v.cuda() for v in (x, dy, w)]
+        y, dx, dw = run(*dev, split, k, out, torch.float32)
+        check(ids, x, dy, w, y, dx, dw)
+        got = launched(lambda: moe.moe_grouped_linear(dev[0], dev[2], split, k, y), NAMES)
+        assert len(got) == 1 and next(iter(got)).startswith("grouped_narrow<")
+        at, per = T - 1, 1 if by_token else k
+        alone, _ = make_split(ids[at:], E)
+        one = torch.full((k, N), 7.0, dtype=out, device="cuda")
+        moe.moe_grouped_linear(dev[0][at * per:(at + 1) * per], dev[2], alone, k, one)
+        assert torch.equal(one, y[at * k:])
 
 
 @pytest.mark.parametrize("T", [500, 521, 2000])
