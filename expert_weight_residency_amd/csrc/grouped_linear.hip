@@ -1083,15 +1083,16 @@ bool use_wide(const GroupedArgs& a) {
 
 // Small tiles, and many buffers, where the next larger ones are few or mostly empty, us,
 // 128 x 64 / 64 x 32: forward 4096 x 2880, one token's 6 experts (192 tiles) 28.7 / 24.9; 2048
-// x 1408, 32 experts, 8 tokens (512) 23.5 / 25.4; 16 x 4096, 64 experts, 8 tokens 27.7 / 18.0,
-// 4096 tokens 54 / 47; 520 x 1032, 8 experts, 1024 tokens (520) 22 / 34. Input 4096 x 2880, one
-// token 36.9 / 29.1; 520 x 1032, 8 experts, 32 tokens (99) 8.6 / 7.4, 256 tokens (288) 9.5 /
-// 16.1. Weights, 128 x 128 / 64 x 64: 4096 x 16, 64 experts, 94 rows 34.6 / 22.4; 520 x 1032, 8
-// experts (360) 13.1 / 12.5; 16 x 4096, 64 experts (2048) 12.4 / 15.6.
+// x 1408, 32 experts, 8 tokens (512) 23.5 / 25.4; 64 x 4096, 64 experts, 4096 tokens (448)
+// 57.8 / 56.6, 384 experts, 1500 tokens (524) 45.7 / 55.2; 520 x 1032, 8 experts, 1024 tokens
+// (520) 22 / 34. Input 4096 x 2880, one token 36.9 / 29.1; 520 x 1032, 8 experts, 32 tokens
+// (99) 8.6 / 7.4, 256 tokens (288) 9.5 / 16.1. Weights, 128 x 128 / 64 x 64: 4096 x 16, 64
+// experts, 94 rows 34.6 / 22.4; 520 x 1032, 8 experts (360) 13.1 / 12.5; 16 x 4096, 64 experts
+// (2048) 12.4 / 15.6.
 bool use_small(const GroupedArgs& a) {
   const int64_t cus = device_cus();
   switch (a.op) {
-    case kForward: return a.N <= 64 || grid_of(a, 128, 64).tiles < 2 * cus;
+    case kForward: return grid_of(a, 128, 64).tiles < 2 * cus;
     case kInput: return a.K <= 64 || grid_of(a, 128, 64).tiles < cus;
     default: return a.K <= 64 || grid_of(a, 128, 128).tiles < 2 * cus;
   }
