@@ -1086,14 +1086,15 @@ bool use_wide(const GroupedArgs& a) {
 // x 1408, 32 experts, 8 tokens (512) 23.5 / 25.4; 64 x 4096, 64 experts, 4096 tokens (448)
 // 57.8 / 56.6, 384 experts, 1500 tokens (524) 45.7 / 55.2; 520 x 1032, 8 experts, 1024 tokens
 // (520) 22 / 34. Input 4096 x 2880, one token 36.9 / 29.1; 520 x 1032, 8 experts, 32 tokens
-// (99) 8.6 / 7.4, 256 tokens (288) 9.5 / 16.1. Weights, 128 x 128 / 64 x 64: 4096 x 16, 64
-// experts, 94 rows 34.6 / 22.4; 520 x 1032, 8 experts (360) 13.1 / 12.5; 16 x 4096, 64 experts
-// (2048) 12.4 / 15.6.
+// (99) 8.6 / 7.4, 256 tokens (288) 9.5 / 16.1; 4096 x 16, 384 experts, 2 rows each 37.3 /
+// 26.0, 23 rows 47.3 / 54.0, 64 experts, 384 rows 48.1 / 57.4. Weights, 128 x 128 / 64 x 64:
+// 4096 x 16, 64 experts, 94 rows 34.6 / 22.4; 520 x 1032, 8 experts (360) 13.1 / 12.5; 16 x
+// 4096, 64 experts (2048) 12.4 / 15.6.
 bool use_small(const GroupedArgs& a) {
-  const int64_t cus = device_cus();
+  const int64_t cus = device_cus(), cap = a.n_rows < a.M ? a.n_rows : a.M;
   switch (a.op) {
     case kForward: return grid_of(a, 128, 64).tiles < 2 * cus;
-    case kInput: return a.K <= 64 || grid_of(a, 128, 64).tiles < cus;
+    case kInput: return (a.K <= 64 && a.M < 16 * cap) || grid_of(a, 128, 64).tiles < cus;
     default: return a.K <= 64 || grid_of(a, 128, 128).tiles < 2 * cus;
   }
 }
