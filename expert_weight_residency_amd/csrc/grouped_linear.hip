@@ -5,7 +5,8 @@
 //   input    dx[s][k]   = sum over n of w[e][n][k] dy[s][n]
 //   weights  dw[e][n][k] = sum over the slots s of e of dy[s][n] x[s][k]
 //
-// One kernel, with two operands of MFMA tiles (v_mfma_f32_16x16x32): A gives the
+// One kernel (grouped; the others below are forms of it for many rows, short sums and few
+// outputs), with two operands of MFMA tiles (v_mfma_f32_16x16x32): A gives the
 // result's rows, 4 consecutive ones a lane, so the axis that is contiguous in the
 // output (n, k, k); B its columns (slots, slots, n). A step takes 64 elements of the
 // sum's axis, 128 bytes of LDS for each row of either operand, by global-to-LDS
@@ -70,7 +71,6 @@ __device__ __forceinline__ uint32_t from_lane(uint32_t v) {
 // An operand of ROWS result rows (or columns) that is contiguous along the sum.
 template <int ROWS>
 struct Along {
-  static constexpr int kBytes = ROWS * 128;
   // copy c of a step (of ROWS / 8): rows 8 c .. + 7, lane l granule l % 8 of row l /
   // 8 from where the swizzle has it
   static __device__ __forceinline__ int row(int c, int lane) { return 8 * c + (lane >> 3); }
@@ -87,7 +87,7 @@ struct Along {
 template <int COLS>
 struct Across {
   static constexpr int kGran = COLS / 8;  // granules of a row
-  static_assert(COLS == 64 || COLS == 128 || COLS == 256, "whole rows per copy");
+  static_assert(COLS == 64 || COLS == 128, "whole rows per copy");
   // chunks of 32 bytes are swapped: the 4 rows of a turned read lie in different banks
   static __device__ __forceinline__ int swizzle(int row) {
     return COLS == 64 ? row & 3 : (row & 3) | ((row >> 3 & 1) << 2);
