@@ -12,24 +12,27 @@
 // the sum, as long as both operands agree: lane (r, q) holds granules q and 4 + q of
 // row r.
 //
-// The FP8 matrix instruction adds products in groups of 8 of which each is cut at
-// 2^-13 of the group's largest (measured: 2^16 + 2^2 gives 2^16; bits of other
-// groups stay down to 2^-24), about 3e-5 of a sum of Gaussian terms. That is far
-// below a 16-bit output's rounding, so products with such outputs use it, one
-// v_mfma_f32_16x16x128_f8f6f4 per tile and block. Outputs in 32 bits, and gate/up,
-// whose h is quantized again, take EXACT: both operands widened to bf16 (which holds
-// every E4M3 value), 4 v_mfma_f32_16x16x32_bf16 per tile and block, at half the rate.
+// Every sum is taken in fp32. The FP8 matrix instructions do not: they cut each product at
+// 2^-13 of the largest of the 8 that they add first (measured, for v_mfma_f32_16x16x128_f8f6f4
+// and v_mfma_f32_16x16x32_fp8_fp8 alike: 2^16 + 2^2 gives 2^16, and 448 * 448 - 448 * 448 + 90
+// gives 0), so that nothing bounds a sum's error by its own size; an activation of a hundred
+// times its neighbours alone takes it to 2.7e-4 of the products' magnitudes. So both operands
+// are widened to bf16, which holds every E4M3 value, for 4 v_mfma_f32_16x16x32_bf16 per tile
+// and block, at half the rate: these keep 24 bits below the largest of 8 (1e-8 of a sum of
+// Gaussian terms). 4096 x 5760 x 4096 106 us with the FP8 instruction, 172 so; one row 9.5 and
+// 11.3; the down product of 4096 tokens 1,353 and 1,526.
 //
 // Copies, buffers, swizzle and the order of tiles are those of gemm_i8_tile: a
 // step takes 128 bytes, so one block, of each row of the tile.
 //
-// Bounds. Few rows: the weights' bytes (384 experts, H 4096, I 2880, 7 tokens: 140 + 77 us,
-// 5.7 and 5.3 TB/s; one row of 5760 x 4096 9.5 us, two round trips before anything
-// streams). The FFN of 4096 tokens: gate/up 2.7 ms (9.1 GB) and down 1.35 (4.5 GB): copies
-// into LDS at 3.4 TB/s from HBM; the matrix cores are busy for 0.35 and 0.18 of the CUs' busy
-// cycles. Gate/up's share is the widening to bf16, too (the whole FFN 3735 us with the FP8
-// instruction, 4155 so). 128 x 64 tiles on 2 x 2 wavefronts; on 4 x 2 4425, 64 x 64 4715,
-// 128 x 32 4840, 128 x 128 5586. Large dense products: gemm_f8_big.
+// Bounds (times of a trace). Few rows: the weights' bytes (384 experts, H 4096, I 2880, 7
+// tokens: 142 + 80 us, 5.7 and 5.1 TB/s). One row of 5760 x 4096, 12.6 us: bytes in flight, 180
+// workgroups on 256 CUs with 12 KB of weights each, half of every copy being the one
+// activation row again. The FFN of 4096 tokens: gate/up 2.72 ms (9.1 GB) and down 1.53 (4.5
+// GB): copies into LDS at 3.4 and 3.0 TB/s from HBM, and the widening; the matrix cores are
+// busy for 0.35 and 0.33 of the CUs' busy cycles. 128 x 64 tiles on 2 x 2 wavefronts (4,155 us
+// for that FFN while down took the FP8 instruction; then 4 x 2 4,425, 64 x 64 4,715, 128 x 32
+// 4,840, 128 x 128 5,586). Large dense products: gemm_f8_big.
 #include <algorithm>
 
 #include "gemm_tile.h"
@@ -42,15 +45,8 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// One operand of a tile: 32 bytes of a row per lane, or those as bf16.
-template <bool EXACT>
+// One operand of a tile: a lane's 32 bytes of a row, as bf16.
 struct Frag {
-  i32x8 v;
-  __device__ __forceinline__ Frag() {}
-  __device__ __forceinline__ explicit Frag(i32x8 x) : v(x) {}
-};
-template <>
-struct Frag<true> {
   bf16x8 v[4];
   __device__ __forceinline__ Frag() {}
   __device__ __forceinline__ explicit Frag(i32x8 x) {
@@ -65,26 +61,25 @@ struct Frag<true> {
   }
 };
 
-__device__ __forceinline__ f32x4 block_product(const Frag<true>& a, const Frag<true>& b) {
-  f32x4 p = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], p, 0, 0, 0);
-  return p;
+// Quarter i of a block's product: the four in order are the block's sum.
+__device__ __forceinline__ f32x4 quarter(const Frag& a, const Frag& b, int i, f32x4 p) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], p, 0, 0, 0);
 }
 
-__device__ __forceinline__ f32x4 block_product(const Frag<false>& a, const Frag<false>& b) {
-  // scale operands of 0 select the form without block scales
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, f32x4{0, 0, 0, 0}, 0, 0, 0, 0,
-                                                          0, 0);
+__device__ __forceinline__ f32x4 block_product(const Frag& a, const Frag& b) {
+  f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p = quarter(a, b, i, p);
+  return p;
 }
 
 __device__ __forceinline__ float from_lane(float v, int lane) {
   return __int_as_float(__builtin_amdgcn_ds_bpermute(4 * lane, __float_as_int(v)));
 }
 
-// TN x TM tile (weight rows x activation rows), WN x WM wavefronts, S buffers.
-template <int TN, int TM, int WN, int WM, int S, bool GU, bool EXACT>
+// TN x TM tile (weight rows x activation rows), WN x WM wavefronts, S buffers; W32:
+// outputs of 32 bits (gate/up's h among them), else 16.
+template <int TN, int TM, int WN, int WM, int S, bool GU, bool W32>
 __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_f8_tile(F8Args a, int tiles_n) {
   constexpr int kW = WN * WM, kRows = TN + TM, kCopies = kRows / 8 / kW;
   static_assert(kRows % (8 * kW) == 0 && TN % (8 * kW) == 0 && (S == 3 || S == 4),
@@ -92,7 +87,7 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_f8_tile(F8Args
   static_assert((GU ? TN / 2 : TN) <= 128 && 128 % (GU ? TN / 2 : TN) == 0,
                 "a tile's outputs lie in one block of weight rows");
   constexpr int NF = TN / WN / 16, MF = TM / WM / 16;  // MFMA tiles per wavefront
-  static_assert(!GU || NF % 2 == 0, "gate and up tiles in pairs");
+  static_assert(!GU || (NF % 2 == 0 && W32), "gate and up tiles in pairs, h in 32 bits");
   constexpr int kSides = GU ? 2 : 1;
   __shared__ __align__(128) uint8_t buf0[kRows * 128];
   __shared__ __align__(128) uint8_t buf1[kRows * 128];
@@ -195,10 +190,10 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_f8_tile(F8Args
   auto frag = [&](const uint8_t* buf, int row) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(buf + row * 128 + 16 * (q ^ (row & 7)));
     const i32x4 hi = *reinterpret_cast<const i32x4*>(buf + row * 128 + 16 * ((4 + q) ^ (row & 7)));
-    return Frag<EXACT>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    return Frag(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
   auto compute = [&](const uint8_t* buf, int step) {
-    Frag<EXACT> bf[MF], af[NF];
+    Frag bf[MF], af[NF];
 #pragma unroll
     for (int j = 0; j < MF; ++j) bf[j] = frag(buf, TN + (wm * MF + j) * 16 + r);
 #pragma unroll
@@ -276,7 +271,7 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_f8_tile(F8Args
       }
     });
   } else {
-    with_output(a, [&](auto type, auto vec) {
+    with_output<W32 ? 32 : 16>(a, [&](auto type, auto vec) {
       rows([&](int j, int64_t orow) {
 #pragma unroll
         for (int i = 0; i < NF; ++i) {
@@ -292,13 +287,13 @@ __global__ __launch_bounds__(64 * WN * WM, WN * WM / 2) void gemm_f8_tile(F8Args
 
 // Dense products with 16-bit outputs, large enough to fill the card with wide tiles: 8
 // wavefronts (2 x 4) of TN/2 x TM/4 outputs, S buffers of 128 bytes, one block, per row.
-// The weights' operand of two tiles on is read from LDS while a row of tiles is
+// The weights' operand of one or two tiles on is read from LDS while a row of tiles is
 // multiplied, and the row before it is scaled and added; the one barrier per step sits
 // after the last read of the step's buffer. Copies go out one row of tiles at a time: a
-// step's, asked for at once by all wavefronts, hold the products up. 4096 x 5760 x 4096:
-// 106 us, 1.8 PFLOP/s (the library's FP8 product of one scale per tensor 98); the matrix
-// cores are busy for 0.48 of the CUs' busy cycles: operand reads, the scales' fma on every
-// tile (4 per product and lane) and the last round of tiles.
+// step's, asked for at once by all wavefronts, hold the products up. 4096 x 5760 x 4096: 172
+// us, 1.12 PFLOP/s (130 at the rate of the largest library products in bf16); the matrix
+// cores are busy for 0.53 of the CUs' busy cycles: the widening (16 conversions per operand
+// and lane), operand reads, the scales' fma on every tile and the last round of tiles.
 template <int TN, int TM, int S>
 __global__ __launch_bounds__(512, 2) void gemm_f8_big(F8Args a, int tiles_n) {
   constexpr int WN = 2, WM = 4, kW = 8;
@@ -373,36 +368,39 @@ __global__ __launch_bounds__(512, 2) void gemm_f8_big(F8Args a, int tiles_n) {
   for (int i = 0; i < NF; ++i)
 #pragma unroll
     for (int j = 0; j < MF; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  using F = Frag<false>;
   const int off0 = r * 128 + 16 * (q ^ (r & 7)), off1 = r * 128 + 16 * ((4 + q) ^ (r & 7));
   auto frag = [&](const uint8_t* p) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(p + off0);
     const i32x4 hi = *reinterpret_cast<const i32x4*>(p + off1);
-    return F(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   auto fa = [&](const uint8_t* buf, int i) { return frag(buf + (wn * NF + i) * 2048); };
   auto fb = [&](const uint8_t* buf, int j) { return frag(buf + (TN / 16 + wm * MF + j) * 2048); };
 
-  // w: operands i .. i + kAhead
+  // The columns of tiles are taken kHeld at a time, so that their operands stay widened in
+  // registers (the largest tiles go over their rows twice). Rows of a step: NF for each such
+  // part. w: the weights' operands of rows i .. i + kAhead, widened as they are multiplied.
+  constexpr int kHeld = NF * MF >= 32 ? MF / 2 : MF, kRows = NF * (MF / kHeld);
   constexpr int kAhead = NF * MF >= 24 ? 1 : 2, kRing = kAhead == 1 ? 2 : 4;
-  static_assert(NF % kRing == 0 && NF % 2 == 0, "the rings start over with a step");
-  F b[MF], w[kRing];
-  f32x4 p[2][MF];     // block products of rows of tiles i and i - 1 (of the step before's last)
-  float sc[MF], due[MF];  // scales of the step, and of the one before
+  static_assert(NF % kRing == 0, "the ring starts over with a step");
+  i32x8 braw[kHeld], w[kRing];
+  f32x4 p[kHeld];  // block products of a row of tiles
+  float sc[MF];    // the step's scales
 #pragma unroll
-  for (int j = 0; j < MF; ++j) {
-    p[1][j] = f32x4{0, 0, 0, 0};
-    due[j] = 0.0f;
-  }
-  auto add = [&](int i, int j, float f) __attribute__((always_inline)) {
+  for (int j = 0; j < kHeld; ++j) p[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < MF; ++j) sc[j] = 0.0f;
+  // to the sums of row i of a step, what p has for its tile j
+  auto add = [&](int i, int j) __attribute__((always_inline)) {
+    const int at = i / NF * kHeld + j;
 #pragma unroll
     for (int v = 0; v < 4; ++v)
-      acc[i][j][v] = __builtin_fmaf(f, p[i & 1][j][v], acc[i][j][v]);
+      acc[i % NF][at][v] = __builtin_fmaf(sc[at], p[j][v], acc[i % NF][at][v]);
   };
   int s = 0;
   // step s out of `here`; phase: its place among the 4 whose scales are in cur. False
-  // after the last. The order of instructions is fixed: a product of each tile, then the
-  // sums of the tile a row before.
+  // after the last. The order of instructions is fixed: the products of a row of tiles,
+  // with the sums of the row before.
   auto step = [&](auto phase, uint8_t* before, uint8_t* here, const uint8_t* next)
                   __attribute__((always_inline)) {
     if constexpr (phase() == 0) {
@@ -410,39 +408,49 @@ __global__ __launch_bounds__(512, 2) void gemm_f8_big(F8Args a, int tiles_n) {
       scales(s + 4);
     }
 #pragma unroll
-    for (int j = 0; j < MF; ++j) sc[j] = from_lane(cur[j], 16 * phase() + r);
+    for (int j = 0; j < kHeld; ++j) add(kRows - 1, j);  // of the step before
 #pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      if (i == NF - kAhead) {
+    for (int j = 0; j < MF; ++j) sc[j] = from_lane(cur[j], 16 * phase() + r);
+    Frag b[kHeld];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      if (i == kRows - kAhead) {
         tile_barrier(vm_lds((S - 2) * kCopies));  // the next step's copies have arrived
       }
       // a share of the copies for the step S on, into the buffer that this step, and
       // before the barrier the one before, has read
-      const int at = i + kAhead < NF ? i + kAhead : i + kAhead - NF;
-      if (i < NF - kAhead) copy(before, s - 1 + S, at * kCopies / NF, (at + 1) * kCopies / NF);
-      else copy(here, s + S, at * kCopies / NF, (at + 1) * kCopies / NF);
-      w[at % kRing] = i + kAhead < NF ? fa(here, at) : fa(next, at);
+      const int at = i + kAhead < kRows ? i + kAhead : i + kAhead - kRows;
+      if (i < kRows - kAhead)
+        copy(before, s - 1 + S, at * kCopies / kRows, (at + 1) * kCopies / kRows);
+      else
+        copy(here, s + S, at * kCopies / kRows, (at + 1) * kCopies / kRows);
+      w[at % kRing] = i + kAhead < kRows ? fa(here, at % NF) : fa(next, at);
+      if (i % NF == 0) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) b[j] = Frag(braw[j]);
+      }
+      const Frag wide(w[i % kRing]);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < MF; ++j) {
-        p[i & 1][j] = block_product(w[i % kRing], b[j]);
-        if (i == 0) add(NF - 1, j, due[j]);
-        else add(i - 1, j, sc[j]);
-        if (i == NF - 1) b[j] = fb(next, j);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
+      for (int h = 0; h < 4; ++h)
 #pragma unroll
-    for (int j = 0; j < MF; ++j) due[j] = sc[j];
+        for (int j = 0; j < kHeld; ++j) {
+          if (h == 0 && i > 0) add(i - 1, j);
+          p[j] = quarter(wide, b[j], h, h ? p[j] : f32x4{0, 0, 0, 0});
+          if (h == 3 && i % NF == NF - 1)
+            braw[j] = i < kRows - 1 ? fb(here, (i / NF + 1) * kHeld + j) : fb(next, j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    }
     return ++s < blocks;
   };
   scales(0);
   copy(buf0, 0, 0, kCopies);
   if constexpr (S > 2) copy(buf1, 1, 0, kCopies);
-  copy(S > 2 ? buf2 : buf1, S - 1, 0, kAhead * kCopies / NF);  // the first step brings the others
-  tile_barrier(vm_lds((S - 2) * kCopies + kAhead * kCopies / NF));
+  copy(S > 2 ? buf2 : buf1, S - 1, 0, kAhead * kCopies / kRows);  // the first step brings the others
+  tile_barrier(vm_lds((S - 2) * kCopies + kAhead * kCopies / kRows));
 #pragma unroll
-  for (int j = 0; j < MF; ++j) b[j] = fb(buf0, j);
+  for (int j = 0; j < kHeld; ++j) braw[j] = fb(buf0, j);
   w[0] = fa(buf0, 0);
   if constexpr (kAhead > 1) w[1] = fa(buf0, 1);
   constexpr std::integral_constant<int, 0> p0;
@@ -464,8 +472,8 @@ __global__ __launch_bounds__(512, 2) void gemm_f8_big(F8Args a, int tiles_n) {
   }
   __builtin_amdgcn_s_waitcnt(vm_lds(0));  // no copy outlives the workgroup's LDS
 #pragma unroll
-  for (int j = 0; j < MF; ++j) add(NF - 1, j, due[j]);
-  with_output(a, [&](auto type, auto vec) {
+  for (int j = 0; j < kHeld; ++j) add(kRows - 1, j);
+  with_output<16>(a, [&](auto type, auto vec) {
 #pragma unroll
     for (int j = 0; j < MF; ++j) {
       const int m = m0 + (wm * MF + j) * 16 + r;
@@ -490,7 +498,7 @@ hipError_t go_big(const F8Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int TN, int TM, int WN, int WM, int S, bool GU, bool EXACT>
+template <int TN, int TM, int WN, int WM, int S, bool GU, bool W32>
 hipError_t go(const F8Args& a, hipStream_t stream) {
   const int per = GU ? TN / 2 : TN;
   const int64_t tiles_n = (a.N + per - 1) / per;
@@ -504,7 +512,7 @@ hipError_t go(const F8Args& a, hipStream_t stream) {
     tiles_m = (a.M + TM - 1) / TM;
   }
   const unsigned grid = (unsigned)((tiles_m * tiles_n + kXcds - 1) / kXcds * kXcds);
-  hipLaunchKernelGGL((gemm_f8_tile<TN, TM, WN, WM, S, GU, EXACT>), dim3(grid),
+  hipLaunchKernelGGL((gemm_f8_tile<TN, TM, WN, WM, S, GU, W32>), dim3(grid),
                      dim3(64 * WN * WM), lds, stream, a, (int)tiles_n);
   return hipGetLastError();
 }
@@ -523,13 +531,16 @@ bool gemm_f8_fits(const F8Args& a) {
 }
 
 hipError_t launch_gemm_f8(const F8Args& a, hipStream_t s) {
-  // Small tiles and a buffer more where experts have few rows, us for the FFN, 128 x 64 / 64
-  // x 32: 384 experts, H 4096, I 2880, 1 token 79 / 63, 16 551 / 467, 112 1337 / 1228, 256 (4
-  // rows each) 1826 / 1697, 4096 (64) 4190 / 5090; 32 experts, H 2048, I 1408, 12 rows each 68
-  // / 63, 24 71 / 70; 8 experts, H 4096, 12 rows 73 / 59, 48 79 / 96.
+  // All times here: us, calls in a row by events. Small tiles and a buffer more where experts
+  // have few rows, the FFN, 128 x 64 / 64 x 32: 384 experts, H 4096, I 2880, 1 token 70 / 53, 16
+  // 592 / 518, 256 (4 rows each) 2608 / 2292, 1024 (16) 2778 / 2642, 1536 (24) 2858 / 2897, 2048
+  // (32) 2931 / 3461, 4096 (64) 3998 / 5088; 32 experts, H 2048, I 1408, 12 rows each 74 / 67, 24
+  // 79 / 70, 32 81 / 82; 8 experts, H 4096, I 2880, 24 rows 79 / 65, 48 83 / 101. M counts the
+  // picks of both banks of a step, so that a bank with a small share is taken for a fuller one:
+  // 89 rows with 230 of 24576 slots 671 / 656, 720 slots 681 / 708.
   if (a.slots) {
     const int64_t cap = a.n_rows < a.M ? a.n_rows : a.M;
-    const bool few = a.M <= 16 * cap;
+    const bool few = a.M <= 24 * cap;
     if (a.gate_up)
       return few ? go<64, 32, 2, 2, 4, true, true>(a, s) : go<128, 64, 2, 2, 3, true, true>(a, s);
     return few ? go<64, 32, 2, 2, 4, false, false>(a, s) : go<128, 64, 2, 2, 3, false, false>(a, s);
@@ -539,24 +550,26 @@ hipError_t launch_gemm_f8(const F8Args& a, hipStream_t s) {
     return (int64_t)((a.N + tn - 1) / tn) * ((a.M + tm - 1) / tm);
   };
   const bool wide = a.dtype == MOE_DTYPE_F32;
-  // Wide tiles where they fill the card, or half of it with a long sum, us, wide / small:
-  // 1024 x 4096 x 4096 26 / 41, 512 x 4096 x 4096 (128 tiles) 24 / 26, 1001 x 2047 x 1040
-  // (128 tiles) 12.8 / 11.1. Of them the one whose rounds over the CUs cost least; a
-  // round's cost is its time per step, 2.0, 1.6, 1.12 and 0.72 us (4096 x 5760 x 4096: 143,
-  // 118, 121, 176 us; 4096 x 4096 x 2880: 58, 82, 61, 78; 8192 x 8192 x 8192: 520, 588, 580,
-  // 730; 8192 x 1024 x 4096: 62, 52, 40, 49).
+  // Wide tiles where they fill the card, or where small ones, twice as many, would start a
+  // second round over the CUs with a long sum, wide / small: 1024 x 4096 x 4096 40 / 47, 640 x
+  // 4096 x 4096 (160 tiles) 38 / 43, 512 x 4096 x 4096 (128 tiles) 37 / 30, 1030 x 2047 x 4096
+  // (144) 40 / 43, x 2064 26 / 28, x 1040 18 / 18. Of them the one whose rounds over the CUs
+  // cost least; a round's cost is its time per step, 3.6, 2.6, 1.9 and 1.15 us (4096 x 5760 x
+  // 4096: 238, 171, 184, 217 us; 4096 x 4096 x 2880: 98, 122, 96, 113; 8192 x 8192 x 8192: 890,
+  // 924, 926, 1082; 8192 x 1024 x 4096: 116, 84, 64, 77). 32-bit outputs have no such kernel:
+  // 4096 x 5760 x 4096 252.
   const int64_t small = tiles(128, 128);
-  if (!wide && a.lda <= 1 << 22 && (small >= cus || (small >= cus / 2 && a.K >= 2048))) {
+  if (!wide && a.lda <= 1 << 22 && (small >= cus || (2 * small > cus && a.K >= 2048))) {
     auto cost = [&](int tn, int tm, int us) { return (tiles(tn, tm) + cus - 1) / cus * us; };
-    const int64_t c[4] = {cost(256, 256, 200), cost(256, 192, 160), cost(256, 128, 112),
-                          cost(128, 128, 72)};
+    const int64_t c[4] = {cost(256, 256, 360), cost(256, 192, 260), cost(256, 128, 190),
+                          cost(128, 128, 115)};
     const int64_t least = std::min(std::min(c[0], c[1]), std::min(c[2], c[3]));
     if (least == c[0]) return go_big<256, 256, 2>(a, s);
     if (least == c[1]) return go_big<256, 192, 2>(a, s);
     if (least == c[2]) return go_big<256, 128, 3>(a, s);
     return go_big<128, 128, 3>(a, s);
   }
-  // 1 x 5760 x 4096 9.6 us with tiles of 64 rows, 8.4 with 32
+  // Tiles of 64 rows / 32, 5760 x 4096: 1 row 13.8 / 11.3, 32 15.0 / 11.4, 33 15.2 / 16.0
   if (a.M <= 32)
     return wide ? go<32, 32, 2, 2, 4, false, true>(a, s) : go<32, 32, 2, 2, 4, false, false>(a, s);
   if (tiles(128, 64) >= cus)

@@ -97,14 +97,18 @@ __device__ __forceinline__ void store4(const A& a, int64_t row, int n, const flo
 // f(type, vec) for the launch's output type and alignment, both compile-time in
 // f: the branches sit around one copy of the epilogue each. (Inside it, at every
 // store, they made the 256 x 256 tile's epilogue thousands of instructions.)
-template <typename A, typename F>
+// BITS: 16 or 32 where only such types come here.
+template <int BITS = 0, typename A, typename F>
 __device__ __forceinline__ void with_output(const A& a, F f) {
   const bool vec = ((a.ldy | a.N) & 3) == 0 &&
                    (reinterpret_cast<uintptr_t>(a.y) & (4 * dtype_bytes(a.dtype) - 1)) == 0;
   auto by_type = [&](auto v) {
-    if (a.dtype == MOE_DTYPE_BF16) f(std::integral_constant<int, MOE_DTYPE_BF16>(), v);
-    else if (a.dtype == MOE_DTYPE_F16) f(std::integral_constant<int, MOE_DTYPE_F16>(), v);
-    else f(std::integral_constant<int, MOE_DTYPE_F32>(), v);
+    if constexpr (BITS != 32) {
+      if (a.dtype == MOE_DTYPE_BF16) return f(std::integral_constant<int, MOE_DTYPE_BF16>(), v);
+      if (BITS == 16 || a.dtype == MOE_DTYPE_F16)
+        return f(std::integral_constant<int, MOE_DTYPE_F16>(), v);
+    }
+    if constexpr (BITS != 16) f(std::integral_constant<int, MOE_DTYPE_F32>(), v);
   };
   if (vec) by_type(std::true_type());
   else by_type(std::false_type());
