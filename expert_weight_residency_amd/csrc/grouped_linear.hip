@@ -1058,45 +1058,61 @@ hipError_t go_wide(const GroupedArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Wide tiles where they fill the card (forward one workgroup per CU, the gradients two)
-// and, but for the weights' gradient, an expert has rows for them. us, small tiles / wide
-// ones: forward 2880 x 4096, 64 experts, 48 rows each 305 / 334, 56 309 / 332, 64 347 / 327,
-// 80 372 / 330, 384 1000 / 790; 5760 x 4096, 384 experts, 64 rows 3980 / 3790; 2048 x 1408,
-// 128 experts, 64 rows 182 / 186, 80 207 / 188; 4096 x 2880, 8 experts, 96 rows (128 wide
-// tiles) 36 / 47, 192 60 / 52; 4096 x 256, 16 experts, 2048 rows 257 / 205; 4096 x 512, 125
-// rows 28 / 30, 512 rows 84 / 72. Input 2880 x 4096, 64 experts, 12 rows 263 / 276, 24 287 /
-// 275, 384 970 / 700; 8 experts, 192 rows (192 wide tiles) 73 / 85. Weights 2880 x 4096, 64
-// experts, 12 rows 975 / 470, 384 2250 / 1010; 1024 x 1024, 4 experts (128 wide tiles), 256
-// rows 11 / 15, 4096 75 / 143; 4096 x 16, 64 experts, 94 rows 22.7 / 31.9, 4096 x 64 27.2 /
-// 34.2, 4096 x 96 38.5 / 36.7, 16 x 4096 30.5 / 20.6.
+// Times in the rules below: us, calls in a row by events, so with operands in the caches
+// where they fit, each kernel launched whatever the rule. Rows are T k / n_rows: with two
+// banks both banks' picks count for each, so that one with a small share is taken for a
+// fuller one (89 rows of 5760 x 4096 with 230, 720 and 2525 of 24576 slots: 128 x 64 691, 719,
+// 751; wide, which it takes, 687, 716, 753).
+//
+// Wide tiles where they fill the card (forward one workgroup per CU, the gradients two), the
+// result is wider than one ordinary tile (for the weights' gradient a small one) and, but
+// there, an expert has rows for them. 128 x 64 tiles / wide ones:
+// forward 2880 x 4096, 64 experts, 48 rows each 285 / 287, 56 310 / 290, 64 341 / 294, 80 396 /
+// 299, 384 1016 / 794; 5760 x 4096, 384 experts, 64 rows 3863 / 3421; 2048 x 1408, 128 experts,
+// 64 rows 196 / 174; 4096 x 2880, 8 experts, 96 rows (112 wide tiles) 39 / 43, 192 66 / 52; 4096
+// x 256, 16 experts, 2048 rows 265 / 213; 4096 x 512, 125 rows 30 / 34, 512 85 / 74. By width, 64
+// experts, K 4096, 384 rows: 40 outputs 45 / 57, 64 48 / 58, 96 49 / 58, 128 66 / 64, 136 102 / 64,
+// 256 125 / 87; 128 outputs, 16 experts, K 1024, 4096 rows 45 / 57.
+// Input 2880 x 4096, 64 experts, 12 rows 275 / 271, 24 282 / 274, 384 1039 / 735; by width, N 4096,
+// 64 experts, 384 rows: 16 columns 48 / 76, 64 51 / 80, 128 67 / 82, 136 112 / 80, 256 131 / 99.
+// Above about 510 rows in the bank the prefix of its tiles no longer fits beside two
+// workgroups' buffers, and the input's gradient takes 128 x 64 tiles.
+// Weights (128 x 128 / wide) 2880 x 4096, 64 experts, 12 rows 766 / 475, 384 1749 / 1078 (1,190
+// with operands from HBM); 4096 x 96, 64 experts, 94 rows 42 / 36, 72 x 4096 39 / 26.
 bool use_wide(const GroupedArgs& a) {
   const Grid g = grid_of(a, kWideA, kWideB);
   const int64_t cus = device_cus(), cap = a.n_rows < a.M ? a.n_rows : a.M;
   const size_t fixed = a.op == kForward ? 3 * (kWideA + kWideB) * 128 + 256 : 78 << 10;
   if (g.lds + fixed > (a.op == kForward ? device_lds_per_block() : 80 << 10)) return false;
   switch (a.op) {
-    case kForward: return a.M >= 64 * cap && g.tiles >= cus;
-    case kInput: return a.M >= 24 * cap && g.tiles >= 2 * cus;
+    case kForward: return a.N > 128 && a.M >= 64 * cap && g.tiles >= cus;
+    case kInput: return a.K > 128 && a.M >= 24 * cap && g.tiles >= 2 * cus;
     default: return a.K > 64 && g.tiles >= 2 * cus;
   }
 }
 
-// Small tiles, and many buffers, where the next larger ones are few or mostly empty, us,
-// 128 x 64 / 64 x 32: forward 4096 x 2880, one token's 6 experts (192 tiles) 28.7 / 24.9; 2048
-// x 1408, 32 experts, 8 tokens (512) 23.5 / 25.4; 64 x 4096, 64 experts, 4096 tokens (448)
-// 57.8 / 56.6, 384 experts, 1500 tokens (524) 45.7 / 55.2; 520 x 1032, 8 experts, 1024 tokens
-// (520) 22 / 34. Input 4096 x 2880, one token 36.9 / 29.1; 520 x 1032, 8 experts, 32 tokens
-// (99) 8.6 / 7.4, 256 tokens (288) 9.5 / 16.1; 4096 x 16, 384 experts, 2 rows each 37.3 /
-// 26.0, 23 rows 47.3 / 54.0, 64 experts, 384 rows 48.1 / 57.4. Weights, 128 x 128 / 64 x 64:
-// 4096 x 16, 64 experts, 94 rows 34.6 / 22.4; 520 x 1032, 8 experts (360) 13.1 / 12.5; 16 x
-// 4096, 64 experts (2048) 12.4 / 15.6.
+// Small tiles (64 x 32, two workgroups per CU), with many buffers, where all that there may
+// be are about one round of them: 2 1/4 per CU, as part-filled ones are counted for every
+// expert. 128 x 64 / small, with that count: forward 4096 x 2880, one token's 6 experts (384)
+// 27 / 24, 12 (768) 41 / 44; 2048 x 1408, 16 slots (512) 15.9 / 14.9, 32 experts, 64 slots (1088)
+// 27 / 30; 1024 x 4096, 64 experts, 64 slots (1056) 76 / 78; 264 x 5000, 4 experts, 3000 rows
+// (485) 49 / 39, 6000 (955) 68 / 78; 520 x 1032, 8 experts, 1000 rows (351) 12.4 / 10.2, 2048
+// (648) 12.7 / 16.5; 64 x 4096, 64 experts, 96 rows each (256) 34 / 23, 384 (832) 48 / 53; 4096 x
+// 4096, 256 rows (576) 35 / 24, 400 (832) 36 / 43. Input 4096 x 2880, one token (270) 38 / 28; N
+// 4096, K 16, 384 experts, 2 rows each (408) 45 / 30, 16 (571) 48 / 31, 23 (665) 48 / 32, 31 (758)
+// 49 / 55; 64 experts, 192 rows (448) 40 / 31, 384 (832) 48 / 57; 1024 x 1024, 16 experts, 32 rows
+// (512) 14.5 / 13.2, 100 (1056) 15.8 / 21.5.
+// The weights' small tiles (64 x 64, three per CU) for up to 64 columns, and else where
+// they start no round more than 128 x 128 ones (one per CU). 128 x 128 / small: 4096 x 16, 64
+// experts, 94 rows 33 / 23, 4096 x 64 37 / 28; 1024 x 1024 by experts, 4096 rows each: 2 69 / 57, 3
+// (192 tiles of 128 x 128, 768 small) 69 / 65, 4 (256) 73 / 108; 1024 x 1280, 4 (320) 134 / 114,
+// 1024 x 1536 (384) 134 / 121, 1024 x 1792 (448) 134 / 159; 520 x 1032, 8 (360), 256 rows 17 / 15;
+// 264 x 5000, 4 (480), 750 rows 32 / 37; 2048 x 2048, 1 (256), 2048 rows 39 / 56.
 bool use_small(const GroupedArgs& a) {
-  const int64_t cus = device_cus(), cap = a.n_rows < a.M ? a.n_rows : a.M;
-  switch (a.op) {
-    case kForward: return grid_of(a, 128, 64).tiles < 2 * cus;
-    case kInput: return (a.K <= 64 && a.M < 16 * cap) || grid_of(a, 128, 64).tiles < cus;
-    default: return a.K <= 64 || grid_of(a, 128, 128).tiles < 2 * cus;
-  }
+  const int64_t cus = device_cus();
+  if (a.op != kWeights) return 4 * grid_of(a, 64, 32).tiles <= 9 * cus;
+  const int64_t tiles = grid_of(a, 128, 128).tiles;
+  return a.K <= 64 || 4 * tiles <= 3 * cus || (tiles > cus && tiles < 2 * cus);
 }
 
 template <int DT>
@@ -1104,13 +1120,13 @@ hipError_t pick(const GroupedArgs& a, hipStream_t s) {
   const bool wide = use_wide(a), small = use_small(a);
   switch (a.op) {
     case kForward:
-      // us, 128 x 64 tiles / this: N = 4096, 64 experts, K 16, 6000 slots 44.2 / 18.2; K 64
-      // 44.5 / 21.9; K 32, 24576 slots 128 / 46.9; 136 x 64, 16000 slots 12.3 / 12.7
+      // 128 x 64 tiles / this: N 4096, 64 experts, K 16, 6000 slots 45 / 23, K 64 46 / 29; K 32,
+      // 24576 slots 130 / 46; 136 x 64, 16000 slots 10.3 / 10.1
       if (a.K <= kShortK && a.N > 64) return go_short<DT>(a, s);
-      // By N and K alone, as the sum's order is another one. us, 64 x 32 tiles / this: 16 x
-      // 4096, 384 experts, 112 tokens 21.3 / 14.2, one token 18.0 / 9.8; 64 experts, 4096
-      // tokens 55.1 / 49.5; 32 x 4096, 1000 tokens 22.1 / 20.5; 64 x 4096, 4096 tokens 57.8 /
-      // 93.4 in a form for 64 outputs
+      // By N and K alone, as the sum's order is another one. 64 x 32 tiles / this: 16 x 4096,
+      // 384 experts, 112 tokens 23.7 / 18.3, one token 18.4 / 10.4; 64 experts, 4096 tokens 49.3
+      // / 49.6; 32 x 4096, 384 experts, 1000 tokens 28 / 33; a form for 64 outputs, 64 x 4096, 64
+      // experts, 4096 tokens, 93 against 48 with 128 x 64 tiles
       if (a.K > kShortK && a.N <= kNarrowA)
         return a.N <= 16 ? go_narrow<DT, 1>(a, s) : go_narrow<DT, 2>(a, s);
       return wide    ? go_wide<kForward, DT>(a, s)
