@@ -852,7 +852,9 @@ def moe_grouped_linear(x, w, split: Split, k: int, y, stream=None) -> None:
 
 def moe_grouped_linear_dx(dy, w, split: Split, k: int, dx, stream=None) -> None:
     """The gradient of moe_grouped_linear's input rows: dy [T*k,N] and w [R,N,K] in one
-    type -> dx [T*k,K] (bfloat16, float16 or float32)."""
+    type -> dx [T*k,K] (bfloat16, float16 or float32). Rows of picks of no expert are
+    left as they were: where a token's row is shared, bfloat16 dx is summed by
+    moe_finalize with weight 0 for such picks and 1 for the others."""
     dev, s = _current(stream)
     _on(dev, dy=dy, w=w, dx=dx, slots=split.slots)
     yp, code = _grouped_rows(dy, "dy", _grouped_types())

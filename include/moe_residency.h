@@ -572,11 +572,17 @@ int moe_expert_ffn_f8(const moe_bank *bank, moe_split split, const uint8_t *xq, 
  *                                        dy[s][n] * x[s][k],
  * zero for a row without a slot (and for every row when T == 0). One rounding, to
  * the output's type. Only the split's slots of y and dx are written. by_token:
- * slot s reads row s / k of x, [T][K] (a token's row is shared by its k picks; the
- * gradient of such a row is the sum of dx over the token's slots, for bf16
- * moe_finalize with weights 1); else row s of x, [T*k][K]. The sums of y and dx have
- * one order, so their bits depend on no bank, step size or place in a step; those of
- * dw one order for the slots' order and the call's sizes.
+ * slot s reads row s / k of x, [T][K] (a token's row is shared by its k picks); else
+ * row s of x, [T*k][K]. The sums of y and dx have one order, so their bits depend on
+ * no bank, step size or place in a step; those of dw one order for the slots' order
+ * and the call's sizes.
+ *
+ * The gradient of a row that k picks share is the sum of dx over those of the
+ * token's slots that some bank's split lists. For bf16 dx that is moe_finalize with
+ * weight 1 for such a pick and 0 for any other (an id of -1 or outside the map, a row
+ * outside its bank): dx has nothing in the latter's rows but what the buffer held
+ * before, which a weight of 1 would add. No entry point sums fp16 or fp32 rows; dx
+ * that the caller sums by itself has to be zero there before the call.
  *
  * dtype: type of x, w and dy, MOE_DTYPE_BF16 or MOE_DTYPE_F16; ydtype, xdtype,
  * wdtype: that of the output, any. w: [n_rows][N][K], device, or with on_host =
