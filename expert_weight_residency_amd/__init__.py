@@ -252,6 +252,8 @@ def _bank_abi(bank, dtypes) -> MoeBankC:
             if str(t.dtype) != want or not t.is_contiguous():
                 raise _bad(f"bank {name}", f"a contiguous {want[6:]} tensor", t)
             host = where == BANK_HOST or (where == BANK_HOST_WEIGHTS and name[0] == "w")
+            if not t.numel():
+                continue  # a bank of no rows: nothing of it is read, and torch pins no empty tensor
             if host and (t.device.type != "cpu" or not t.is_pinned()):
                 raise _bad(f"bank {name}", f"pinned host memory (on_host={where})", t)
             if not host and t.device.type != "cuda":
@@ -787,21 +789,23 @@ def moe_expert_ffn_f8(bank: BankF8, split: Split, xq, xs, k: int, I: int, worksp
 
 def _grouped_rows(t, name: str, dtypes, dtype=None, shape=None):
     """(pointer, dtype code) of a contiguous GPU tensor of one of the types (of
-    `dtype` if given) and of the shape."""
+    `dtype` if given) and of the shape (None: any size), of rows at least."""
     code = dtypes.get(t.dtype)
     if code is None or not t.is_cuda or not t.is_contiguous() or (dtype is not None and
                                                                   t.dtype != dtype):
         want = str(dtype) if dtype is not None else ", ".join(str(d) for d in dtypes)
         raise _bad(name, f"a contiguous GPU tensor ({want})", t)
-    if shape is not None and tuple(t.shape) != shape:
-        raise MoeError(MOE_EINVAL, f"{name} {tuple(t.shape)}: need {shape}")
+    if t.dim() < 2 or (shape is not None and (t.dim() != len(shape) or any(
+            n is not None and n != m for n, m in zip(shape, t.shape)))):
+        raise MoeError(MOE_EINVAL, f"{name} {tuple(t.shape)}: need {shape or 'rows'}")
     return t.data_ptr(), code
 
 
 def _grouped_weights(w, dtype):
-    """(pointer, rows, N, K, on_host) of weights [rows,N,K] on the GPU or pinned."""
+    """(pointer, rows, N, K, on_host) of weights [rows,N,K] on the GPU or pinned (torch
+    pins none of no rows)."""
     if w.dim() != 3 or w.dtype != dtype or not w.is_contiguous() or \
-            not (w.is_cuda or (w.device.type == "cpu" and w.is_pinned())):
+            not (w.is_cuda or (w.device.type == "cpu" and (w.shape[0] == 0 or w.is_pinned()))):
         raise _bad("w", f"contiguous [rows,N,K] weights ({dtype}) on the GPU or in pinned memory", w)
     return (w.data_ptr(), *w.shape, BANK_DEVICE if w.is_cuda else BANK_HOST)
 
@@ -841,7 +845,7 @@ def moe_grouped_linear(x, w, split: Split, k: int, y, stream=None) -> None:
     _on(dev, x=x, w=w, y=y, slots=split.slots)
     xp, code = _grouped_rows(x, "x", _grouped_types())
     wp, rows, N, K, on_host = _grouped_weights(w, x.dtype)
-    yp, ycode = _grouped_rows(y, "y", _dtypes(), shape=(int(y.shape[0]), N))
+    yp, ycode = _grouped_rows(y, "y", _dtypes(), shape=(None, N))
     T = _grouped_split(split, int(y.shape[0]), k, rows)
     by_token = _grouped_by_token(x, T, k)
     if x.shape[1] != K:
