@@ -138,6 +138,8 @@ int moe_expert_ffn_f8(const moe_bank* bank, moe_split split, const uint8_t* xq, 
   d.K = I;
   d.by_token = 0;
   d.gate_up = 0;
+  // a pick's row is rounded to bf16, as in the other layers: what moe_finalize reads, half the
+  // bytes (0.0024 of the layer's output instead of 0.0017 in all)
   d.y = Y;
   d.dtype = MOE_DTYPE_BF16;
   d.ldy = H;

@@ -26,9 +26,9 @@
 // step takes 128 bytes, so one block, of each row of the tile.
 //
 // Bounds (times of a trace). Few rows: the weights' bytes (384 experts, H 4096, I 2880, 7
-// tokens: 142 + 80 us, 5.7 and 5.1 TB/s). One row of 5760 x 4096, 12.6 us: bytes in flight, 180
+// tokens: 141 + 80 us, 5.7 and 5.1 TB/s). One row of 5760 x 4096, 12.8 us: bytes in flight, 180
 // workgroups on 256 CUs with 12 KB of weights each, half of every copy being the one
-// activation row again. The FFN of 4096 tokens: gate/up 2.72 ms (9.1 GB) and down 1.53 (4.5
+// activation row again. The FFN of 4096 tokens: gate/up 2.71 ms (9.1 GB) and down 1.52 (4.5
 // GB): copies into LDS at 3.4 and 3.0 TB/s from HBM, and the widening; the matrix cores are
 // busy for 0.35 and 0.33 of the CUs' busy cycles. 128 x 64 tiles on 2 x 2 wavefronts (4,155 us
 // for that FFN while down took the FP8 instruction; then 4 x 2 4,425, 64 x 64 4,715, 128 x 32
@@ -447,7 +447,8 @@ __global__ __launch_bounds__(512, 2) void gemm_f8_big(F8Args a, int tiles_n) {
   scales(0);
   copy(buf0, 0, 0, kCopies);
   if constexpr (S > 2) copy(buf1, 1, 0, kCopies);
-  copy(S > 2 ? buf2 : buf1, S - 1, 0, kAhead * kCopies / kRows);  // the first step brings the others
+  // the first step brings the others
+  copy(S > 2 ? buf2 : buf1, S - 1, 0, kAhead * kCopies / kRows);
   tile_barrier(vm_lds((S - 2) * kCopies + kAhead * kCopies / kRows));
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) braw[j] = fb(buf0, j);

@@ -23,12 +23,15 @@
 // order).
 //
 // Bounds, at 384 experts of 5760 x 4096, 64 rows each (18.4 GB, 2.87 ms at the read rate):
-// 3.76 ms, 4.9 TB/s. Few rows: the weights' bytes; one token's 6 experts of 4096 x 2880 24.9
+// 3.76 ms, 4.9 TB/s. Few rows: the weights' bytes; one token's 6 experts of 4096 x 2880 25
 // us (5.7 TB/s). Many rows (64 experts, 2880 x 4096, 384 rows: 580 GFLOP, 391 us at the rate
-// of a large library product): forward 800 us, input 700, weights 1190 (3.0 GB written); the
-// matrix cores are busy for 0.48, 0.49 and 0.24 of the CUs' busy cycles, no bank conflicts;
-// operands' way from the L2 into LDS, about 10 TB/s with products running, and where the
-// weights come from HBM (with one expert's weights for all: 690 and 610 us).
+// of a large library product): forward 800 us, input 700, weights 1190 (3.0 GB written;
+// 1078 with the operands in the caches). Of the CUs' busy cycles the matrix cores are busy for
+// 0.47, 0.49 and 0.25, operand reads from LDS for 0.30, 0.19 and 0.14 (no bank conflicts);
+// HBM gives 2.5, 2.3 and 0.6 GB. So none of the three is full. The wavefronts wait for 0.45,
+// 0.21 and 0.27 of their cycles: forward at the barrier of each step, with one workgroup per CU
+// and nothing beside it. With one expert's weights for all 690 and 610 us (forward, input):
+// what HBM's latency adds.
 #include "gemm_tile.h"
 #include "tile_items.h"
 
